@@ -58,7 +58,14 @@ typedef enum {
   PSISPEC_ESCRATCH = -6      /* sizes beyond the fixed scratch of the no-allocation entry point */
 } psispec_status;
 
-typedef enum { PSISPEC_F32 = 0, PSISPEC_BF16 = 1 } psispec_dtype;
+/* Logits are F32 or BF16.  The paged-cache calls take queries, keys and values in BF16 or F16 and
+   caches in their type or in F8E4M3 (8 bits: 4 exponent, 3 mantissa; no infinities, largest 448). */
+typedef enum {
+  PSISPEC_F32 = 0,
+  PSISPEC_BF16 = 1,
+  PSISPEC_F16 = 2,
+  PSISPEC_F8E4M3 = 3
+} psispec_dtype;
 
 /* flags */
 #define PSISPEC_FIRST_FROM_TARGET 1u /* Uno layout: position 0 is the AR's own sample and is always
@@ -79,6 +86,9 @@ typedef enum { PSISPEC_F32 = 0, PSISPEC_BF16 = 1 } psispec_dtype;
 #define PSISPEC_ST_RESID_ZERO 8  /* residual mass 0 at a rejection: drew from the target row */
 #define PSISPEC_ST_BAD_PARENT 16 /* tree: parent[j] outside [-1, j-1] or depth beyond max_depth */
 #define PSISPEC_ST_BAD_KEEP 32   /* KV commit: kept count, kept positions or length invalid */
+#define PSISPEC_ST_BAD_PAGE 64   /* paged cache: length, row count, source line or a page that the
+                                    call needs is invalid */
+#define PSISPEC_ST_NO_PAGE 128   /* psispec_pages_reserve: not enough free pages for the line */
 
 typedef struct {
   double temperature;    /* > 0 and finite: logits are divided by it */
@@ -278,6 +288,205 @@ psispec_status psispec_lmhead_verify(const void* h_ar, const void* h_draft, cons
                                      uint64_t* accept_mask, int32_t* status, float* p_logits_dbg,
                                      float* q_logits_dbg, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/*
+ * Paged KV cache.  Instead of one contiguous line per sequence (psispec_kv_commit), the lines of
+ * all sequences share a pool of pages of page_size positions each; table[r][s] is the page that
+ * holds positions s * page_size .. (s + 1) * page_size - 1 of line r, or -1.  The verify forward's
+ * path over it: psispec_pages_reserve gives every line pages for its next block,
+ * psispec_qkv_append writes the block's rows at positions len[r] .. len[r]+n-1,
+ * psispec_paged_attention reads them, psispec_paged_commit keeps the accepted ones and advances
+ * len, psispec_pages_assign forks, cuts and frees lines.
+ *
+ * One layer's keys and values as the append and the attention see them.  Element (page p, offset o,
+ * head h, dimension d) of K is k[p * page_stride + o * row_stride + h * head_stride + d], of V the
+ * same from v: any order of pages, positions and heads, for example views into a pool that holds
+ * every layer.  Bases 16-byte aligned and strides multiples of 16 bytes.
+ */
+typedef struct {
+  void* k;                /* device; the attention only reads both */
+  void* v;
+  const float* k_scale;   /* device [heads], F8E4M3 caches only: a stored number x stands for */
+  const float* v_scale;   /* x * scale[head]; NULL means 1 */
+  const int32_t* table;   /* device [batch][table_stride], the first `slots` entries of a row used */
+  int64_t page_stride;    /* elements */
+  int64_t row_stride;     /* elements */
+  int64_t head_stride;    /* elements */
+  int64_t table_stride;   /* entries, >= slots */
+  int32_t num_pages;      /* >= 1: valid page ids are 0 .. num_pages-1 */
+  int32_t page_size;      /* positions per page, 1..4096 */
+  int32_t slots;          /* >= 1 and slots * page_size <= 2^30 */
+  int32_t heads;          /* key/value heads, >= 1 */
+  int32_t dim;            /* head dimension, a multiple of 16, 16..256 */
+  int32_t dtype;          /* psispec_dtype: the calls' element type or PSISPEC_F8E4M3 */
+} psispec_paged_cache;
+
+/* Norm and position rotation of psispec_qkv_append. */
+#define PSISPEC_ROPE_INTERLEAVED 1u /* pairs are dimensions (2j, 2j+1); else (j, j + rot/2) */
+typedef struct {
+  const void* q_weight;   /* device [dim] of the call's dtype: norm weight of the query heads, or
+                             NULL: queries are not normalised */
+  const void* k_weight;   /* the same for the key heads */
+  const double* inv_freq; /* device [rot/2]: angle per position of pair j (the long-context scalings
+                             are other frequencies, and rope_scale); NULL only when rot = 0 */
+  double eps;             /* >= 0: added to the mean square */
+  double rope_scale;      /* finite: the rotated pairs are multiplied by it */
+  int32_t rot;            /* leading dimensions that are rotated: a multiple of 16, 0..dim */
+  uint32_t flags;         /* PSISPEC_ROPE_INTERLEAVED or 0 */
+} psispec_qkv_prep;
+
+/*
+ * The block's queries, keys and values, normalised, rotated and written where the attention reads
+ * them, in one pass:
+ *   x = x / sqrt(mean(x^2) + eps) * weight              (query and key heads with a weight)
+ *   (a, b) = rope_scale (a cos t - b sin t, b cos t + a sin t), t = position * inv_freq[j]
+ *                                                       (pair j of the first rot dimensions)
+ * in 32 bits with the angles formed and reduced in 64, rounded once to the output's type.  Queries
+ * go to q_out, keys and values to the cache at positions len[r] .. len[r]+n-1 of line r, n =
+ * n_new[r] (blk when NULL).  An 8-bit cache stores x / scale[head], clamped to +-448 and rounded to
+ * the nearest (NaN stays NaN).
+ *   c          host pointer; heads and dim are those of k and v
+ *   p          host pointer
+ *   q, k, v    row (r, i) at (r * blk + i) * stride elements: heads_q (q) or c->heads (k, v) heads of
+ *              dim contiguous elements; dtype PSISPEC_BF16 or PSISPEC_F16.  Views into one packed
+ *              projection are fine; pointers 16-byte aligned, strides multiples of 8 elements
+ *   positions  [batch][blk] int32 rotation position of each row (a tree's len + depth; any value),
+ *              or NULL: len[r] + i
+ *   len        [batch] int32 rows that the line holds already
+ *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] are neither read nor written
+ *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride
+ *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when len < 0, n_new is outside [0, blk]
+ *              or the rows do not fit the slots (nothing of the line is then written, q_out
+ *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a
+ *              page are then not written, q_out included)
+ *   blk 1..2^20;  batch >= 0 (0 launches nothing);  heads_q >= 1
+ * The pages written must be the line's own (psispec_pages_reserve sees to it): rows of two lines
+ * in one page position race.  Asynchronous on `stream`; no workspace.
+ */
+psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qkv_prep* p,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, psispec_dtype dtype,
+                                  int32_t batch, int32_t blk, int32_t heads_q,
+                                  const int32_t* positions, const int32_t* len,
+                                  const int32_t* n_new, void* q_out, int64_t q_out_stride,
+                                  int32_t* status, void* stream);
+
+/*
+ * Attention of the block's queries over the paged cache: one new token per line (blk = 1) or the
+ * drafted block of a verify forward.  Row i of line r sees the line's first len[r] positions and, of
+ * the block's rows (which the cache already holds at len[r] ..), rows 0..i (parent NULL) or row i
+ * and its ancestors in the tree:
+ *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * q . k_t)   over the positions t that it sees
+ * Query heads share key/value heads in groups: head h reads key/value head h / (heads_q / heads).
+ * Products of the matrix cores in the inputs' type with 32-bit sums; softmax statistics in 32 bits;
+ * weights enter the second product as a pair of 16-bit numbers (relative error 2^-16), so out is as
+ * exact as its own rounding.  A position that a row does not see has no effect on it, whatever the
+ * cache holds there.
+ *   q, out     row (r, i) at (r * blk + i) * stride elements: heads_q heads of c->dim contiguous
+ *              elements; dtype PSISPEC_BF16 or PSISPEC_F16; 16-byte aligned, strides multiples of 8
+ *   parent     [batch][blk] int32: the block row that row j follows, -1 = the line's last position;
+ *              must be < j.  NULL: row j follows row j-1
+ *   len, n_new as in psispec_qkv_append; rows i >= n_new[r] of out are left as they are
+ *   scale      finite
+ *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE as in psispec_qkv_append, for every page
+ *              of the line's first len + n_new positions; PSISPEC_ST_BAD_PARENT.  Out rows of such a
+ *              line are unspecified, other lines are not affected
+ *   blk 1..1024;  batch >= 0 (0 launches nothing);  heads_q a multiple of c->heads, at most 1024
+ * The work is cut into equal shares over the whole batch by the lines' lengths, read on the device,
+ * and rows cut by a share's border are joined in a fixed order: reruns are bitwise identical.
+ */
+size_t psispec_paged_attention_workspace(int32_t batch, int32_t blk, int32_t heads_q,
+                                         int32_t heads_kv, int32_t dim);
+
+psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void* q, int64_t q_stride,
+                                       psispec_dtype dtype, int32_t batch, int32_t blk,
+                                       int32_t heads_q, const int32_t* parent, const int32_t* len,
+                                       const int32_t* n_new, double scale, void* out,
+                                       int64_t out_stride, int32_t* status, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * A pool of pages as the calls that move rows see it: `planes` planes (layers, K and V, or whatever
+ * lies apart), each num_pages pages of page_size rows of row_bytes opaque bytes.  Row o of page p of
+ * plane w starts at base + w * plane_stride + p * page_stride + o * row_bytes.
+ */
+typedef struct {
+  void* base;             /* device, 16-byte aligned */
+  int64_t plane_stride;   /* bytes, a multiple of 16; planes do not overlap */
+  int64_t page_stride;    /* bytes, a multiple of 16, >= page_size * row_bytes */
+  int64_t row_bytes;      /* a multiple of 16, >= 16 */
+  int32_t planes;         /* >= 1 */
+  int32_t num_pages;      /* >= 1 */
+  int32_t page_size;      /* 1..4096 */
+  int32_t reserved;       /* must be 0 */
+} psispec_page_pool;
+
+/*
+ * psispec_kv_commit for lines in pages: the kept rows, block positions keep[r][0..n_keep[r]-1], move
+ * to positions len[r] .. len[r]+n_keep[r]-1 of line r, in every plane, and new_len[r] becomes
+ * len[r] + n_keep[r].  Pages that the block needed stay with the line for its next block.
+ *   table      [batch][table_stride] int32, the first `slots` entries of a row used
+ *   blk, keep, keep_stride, n_keep   as in psispec_kv_commit (blk 1..1024)
+ *   len        [batch] int32 with len + blk <= slots * page_size
+ *   new_len    [batch] int32; may be len itself
+ *   status     [batch] int32, nullable: PSISPEC_ST_BAD_KEEP as in psispec_kv_commit,
+ *              PSISPEC_ST_BAD_PAGE when a page of the rows that move is not in 0..num_pages-1;
+ *              nothing of such a line moves and its length stays
+ * Asynchronous on `stream`; no workspace.
+ */
+psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t* table,
+                                    int64_t table_stride, int32_t slots, int32_t batch, int32_t blk,
+                                    const int32_t* keep, int32_t keep_stride, const int32_t* n_keep,
+                                    const int32_t* len, int32_t* new_len, int32_t* status,
+                                    void* stream);
+
+/*
+ * Owners of pages.  refs[p] counts the table entries of all lines that name page p; a page with
+ * count 0 is free.  All lines that share a pool are rows of one table.  An empty pool has refs all
+ * 0, tables all -1 and lengths 0.
+ *
+ * psispec_pages_assign makes every line r a copy of the first new_len[r] positions of the line
+ * src[r] as it was before the call, by sharing its pages (no row moves): src[r] = r and new_len[r] =
+ * len[r] keeps a line, a smaller new_len cuts it, src[r] = -1 or new_len 0 frees it, another line
+ * forks that line (any number of lines from one; a beam's reorder is one call).  Slots past
+ * ceil(new_len / page_size) become -1, those reserved for a block included.  Pages that no line
+ * holds any more are free from then on.
+ *   table      [batch][table_stride] int32, in/out
+ *   refs       [num_pages] int32, in/out
+ *   len        [batch] int32, in/out
+ *   src        [batch] int32 in [-1, batch)
+ *   new_len    [batch] int32 in [0, len[src]] (ignored when src = -1)
+ *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when src, new_len or a page of the
+ *              positions taken is invalid; that line then stays as it is
+ */
+size_t psispec_pages_workspace(int32_t batch, int32_t slots, int32_t num_pages, int32_t blk,
+                               int32_t page_size);
+
+psispec_status psispec_pages_assign(int32_t* table, int64_t table_stride, int32_t slots,
+                                    int32_t* refs, int32_t num_pages, int32_t page_size,
+                                    int32_t* len, const int32_t* src, const int32_t* new_len,
+                                    int32_t* status, int32_t batch, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * psispec_pages_reserve gives every line pages of its own for positions len[r] .. len[r]+n-1, n =
+ * n_new[r] (blk when NULL): slots without a page get the lowest-numbered free pages in the order
+ * of lines and slots, and a page among them that other lines hold too is replaced by a free one, the
+ * line's rows before len[r] in it copied in every plane (the copy on a first write after a fork).
+ * Every page that holds the reserved positions then has count 1.
+ *   status     [batch] int32, nullable: PSISPEC_ST_NO_PAGE when the free pages run out before this
+ *              line is served (then neither it nor any later line that needs a page is),
+ *              PSISPEC_ST_BAD_PAGE when len, n_new or a page of these slots is invalid; such a line
+ *              stays as it is
+ *   blk        1..2^20 (a whole prompt may be reserved at once)
+ * Pages that become free in the call are given out by later calls only.  Workspace of both calls:
+ * psispec_pages_workspace (blk of the reserve).
+ */
+psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* table,
+                                     int64_t table_stride, int32_t slots, int32_t* refs,
+                                     const int32_t* len, const int32_t* n_new, int32_t blk,
+                                     int32_t* status, int32_t batch, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* Message for a return code (static string). */
 const char* psispec_strerror(psispec_status code);

@@ -7,7 +7,9 @@ if libpsispec.so is missing or a tensor is not on a GPU, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -15,17 +17,20 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpsispec.so")
 
-PSISPEC_F32, PSISPEC_BF16 = 0, 1
+PSISPEC_F32, PSISPEC_BF16, PSISPEC_F16, PSISPEC_F8E4M3 = 0, 1, 2, 3
 PSISPEC_FIRST_FROM_TARGET = 1
 PSISPEC_MAX_CHILDREN_SHIFT = 4  # flags bits 4..7: bound on children per node (sampled tree)
 ST_NONFINITE, ST_BAD_TOKEN, ST_Q_ZERO, ST_RESID_ZERO, ST_BAD_PARENT = 1, 2, 4, 8, 16
-ST_BAD_KEEP = 32
+ST_BAD_KEEP, ST_BAD_PAGE, ST_NO_PAGE = 32, 64, 128
+PSISPEC_ROPE_INTERLEAVED = 1
 
 EXPORTS = ("psispec_verify_linear_workspace", "psispec_verify_linear",
            "psispec_verify_linear_noalloc",
            "psispec_verify_tree_workspace", "psispec_verify_tree", "psispec_lmhead_verify_workspace",
            "psispec_lmhead_verify", "psispec_sample_drafts_workspace", "psispec_sample_drafts",
-           "psispec_kv_commit", "psispec_strerror", "psispec_timing_enable",
+           "psispec_kv_commit", "psispec_qkv_append", "psispec_paged_attention_workspace",
+           "psispec_paged_attention", "psispec_paged_commit", "psispec_pages_workspace",
+           "psispec_pages_assign", "psispec_pages_reserve", "psispec_strerror", "psispec_timing_enable",
            "psispec_timing_read", "psispec_peak_read", "psispec_peak_mfma")
 
 
@@ -38,6 +43,28 @@ class psispec_sampling(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("step", ctypes.c_uint32),
                 ("request_base", ctypes.c_uint32), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class psispec_paged_cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table")]
+                + [(n, ctypes.c_int64) for n in ("page_stride", "row_stride", "head_stride",
+                                                 "table_stride")]
+                + [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "slots", "heads", "dim",
+                                                 "dtype")])
+
+
+class psispec_qkv_prep(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("eps", ctypes.c_double),
+                ("rope_scale", ctypes.c_double), ("rot", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+class psispec_page_pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("plane_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int64),
+                ("planes", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -77,6 +104,23 @@ def lib():
         L.psispec_kv_commit.argtypes = [P, ctypes.c_int64, ctypes.c_int64, i32, i32, P, i32, P, P, P,
                                         i32, P]
         L.psispec_kv_commit.restype = i32
+        i64 = ctypes.c_int64
+        L.psispec_qkv_append.argtypes = [P, P, P, i64, P, i64, P, i64, i32, i32, i32, i32, P, P, P, P,
+                                         i64, P, P]
+        L.psispec_qkv_append.restype = i32
+        L.psispec_paged_attention_workspace.argtypes = [i32, i32, i32, i32, i32]
+        L.psispec_paged_attention_workspace.restype = sz
+        L.psispec_paged_attention.argtypes = [P, P, i64, i32, i32, i32, i32, P, P, P, ctypes.c_double,
+                                              P, i64, P, P, sz, P]
+        L.psispec_paged_attention.restype = i32
+        L.psispec_paged_commit.argtypes = [P, P, i64, i32, i32, i32, P, i32, P, P, P, P, P]
+        L.psispec_paged_commit.restype = i32
+        L.psispec_pages_workspace.argtypes = [i32, i32, i32, i32, i32]
+        L.psispec_pages_workspace.restype = sz
+        L.psispec_pages_assign.argtypes = [P, i64, i32, P, i32, i32, P, P, P, P, i32, P, sz, P]
+        L.psispec_pages_assign.restype = i32
+        L.psispec_pages_reserve.argtypes = [P, P, i64, i32, P, P, P, i32, P, i32, P, sz, P]
+        L.psispec_pages_reserve.restype = i32
         L.psispec_strerror.argtypes = [i32]
         L.psispec_strerror.restype = ctypes.c_char_p
         L.psispec_timing_enable.argtypes = [i32]
@@ -498,6 +542,364 @@ def psispec_kv_commit(kv: torch.Tensor, blk: int, n_keep: torch.Tensor, length: 
                                  ks, _ptr(n_keep), _ptr(length), _ptr(status), batch,
                                  _stream(stream))
     _check(rc, "psispec_kv_commit")
+    return status
+
+
+# ------------------------------------------------------------------------------------------------
+# Paged KV cache
+# ------------------------------------------------------------------------------------------------
+_PAGED_DTYPES = {torch.bfloat16: PSISPEC_BF16, torch.float16: PSISPEC_F16,
+                 torch.float8_e4m3fn: PSISPEC_F8E4M3}
+
+
+def _on(dev, stream):
+    """The guard under which a call on `dev` allocates and launches: `dev` current and, when a stream
+    is given, that stream (which must be one of `dev`'s)."""
+    if stream is not None:
+        if stream.device != dev:
+            raise PsispecError(f"stream is on {stream.device}, expected {dev}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != dev.index:
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _int32(t: torch.Tensor, shape, dev, name: str) -> int:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise PsispecError(f"{name} must be int32 {list(shape)}")
+    _same_dev(t, dev, name)
+    return _dev(t, name)
+
+
+def _table(table: torch.Tensor, batch: int, dev):
+    """(pointer, row stride, slots) of a page table [batch][slots]; rows contiguous."""
+    if table.dim() != 2 or table.shape[0] != batch or table.dtype != torch.int32:
+        raise PsispecError("table must be int32 [batch][slots]")
+    if not table.is_cuda:
+        raise PsispecError("table must be a GPU tensor (the library has no CPU path)")
+    _same_dev(table, dev, "table")
+    slots = table.shape[1]
+    stride = table.stride(0) if batch > 1 else max(slots, 1)
+    if slots < 1 or (slots > 1 and table.stride(1) != 1) or stride < slots:
+        raise PsispecError("table rows must be contiguous and not overlap")
+    return table.data_ptr(), stride, slots
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, dev):
+    """(pointer, elements from one token row to the next) of [batch][blk][heads][dim], whose heads and
+    dims are contiguous within a row and whose rows are evenly spaced."""
+    if t.dim() != 4:
+        raise PsispecError(f"{name} must be [batch][blk][heads][dim]")
+    if not t.is_cuda:
+        raise PsispecError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    _same_dev(t, dev, name)
+    if t.dtype != dtype:
+        raise PsispecError(f"{name} must be {dtype}, got {t.dtype}")
+    (b, n, h, d), st = t.shape, t.stride()
+    rows = st[1] if n > 1 else st[0] if b > 1 else h * d
+    if (st[3] != 1 or (h > 1 and st[2] != d) or (n > 1 and b > 1 and st[0] != n * rows)
+            or rows < h * d):
+        raise PsispecError(f"{name} must have contiguous [heads][dim] rows, evenly spaced")
+    return t.data_ptr(), rows
+
+
+def _scale_ptr(t, heads, dev, name):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (heads,):
+        raise PsispecError(f"{name} must be float32 [heads]")
+    _same_dev(t, dev, name)
+    return _dev(t, name)
+
+
+def _paged_cache(k_cache, v_cache, table, batch, dtype, dev, k_scale, v_scale):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise PsispecError("k_cache and v_cache must be [pages][page_size][heads][dim]")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_cuda:
+            raise PsispecError(f"{name} must be a GPU tensor (the library has no CPU path)")
+        _same_dev(t, dev, name)
+        if t.dtype != k_cache.dtype or t.dtype not in (dtype, torch.float8_e4m3fn):
+            raise PsispecError(f"{name} must be {dtype} or torch.float8_e4m3fn, got {t.dtype}")
+    pages, ps, heads, dim = k_cache.shape
+    # an extent of 1 has no stride of its own
+    sk, sv = ([s if n > 1 else dim for s, n in zip(t.stride(), t.shape)] for t in (k_cache, v_cache))
+    if sk != sv or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise PsispecError("k_cache and v_cache must have the same strides, the last one 1")
+    if (k_scale is not None or v_scale is not None) and k_cache.dtype != torch.float8_e4m3fn:
+        raise PsispecError("k_scale and v_scale go with a float8_e4m3fn cache")
+    tp, ts, slots = _table(table, batch, dev)
+    return psispec_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(),
+                               _scale_ptr(k_scale, heads, dev, "k_scale"),
+                               _scale_ptr(v_scale, heads, dev, "v_scale"), tp, sk[0], sk[1], sk[2],
+                               ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[k_cache.dtype])
+
+
+def _page_pool(pool: torch.Tensor):
+    if pool.dim() < 4:
+        raise PsispecError("pool must be [planes][pages][page_size][...]")
+    if not pool.is_cuda:
+        raise PsispecError("pool must be a GPU tensor (the library has no CPU path)")
+    planes, pages, ps = pool.shape[:3]
+    es, row = pool.element_size(), 1
+    for n, st in zip(reversed(pool.shape[3:]), reversed(pool.stride()[3:])):
+        if n > 1 and st != row:
+            raise PsispecError("a row of pool (its dimensions after the first three) must be contiguous")
+        row *= n
+    if ps > 1 and pool.stride(2) != row:
+        raise PsispecError("the rows of a page of pool must be contiguous")
+    page = pool.stride(1) if pages > 1 else ps * row
+    plane = pool.stride(0) if planes > 1 else pages * page
+    if planes > 1 and plane < row or min(plane, page) < 0:
+        raise PsispecError("the planes of pool must not overlap")
+    return psispec_page_pool(pool.data_ptr(), plane * es, page * es, row * es, planes, pages, ps, 0)
+
+
+def _workspace_for(workspace, need, dev, what):
+    if need == 0:
+        raise PsispecError(f"unsupported sizes for {what}")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if (not workspace.is_cuda or workspace.device != dev or workspace.dtype != torch.uint8
+            or not workspace.is_contiguous() or workspace.numel() < need):
+        raise PsispecError(f"workspace must be a contiguous uint8 tensor on {dev} with at least "
+                           f"{need} elements")
+    return workspace
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, fast: float = 32.0, slow: float = 1.0, device=None):
+    """(inv_freq, rope_scale) for psispec_qkv_append: float64 [rot/2] angles per position of the
+    pairs, and the factor of the rotated values.
+      "none"      base^(-2j/rot)
+      "linear"    those divided by factor (positions compressed)
+      "base"      those of the base times factor^(rot/(rot-2)): the slowest pair turns factor times
+                  slower, the fastest as before
+      "by_parts"  pairs that turn more than `fast` times within original_length positions as they
+                  are, those that turn less than `slow` times divided by factor, in between mixed
+                  linearly in j between the (rounded) borders; values times 0.1 ln(factor) + 1"""
+    if rot < 2 or rot % 2 or not base > 0 or not factor > 0:
+        raise PsispecError("rot must be even and positive, base and factor positive")
+    j = torch.arange(rot // 2, dtype=torch.float64)
+    mag = 1.0
+    if scaling == "base":
+        if rot < 4:
+            raise PsispecError("base scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * j / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if original_length < 1 or not fast > slow > 0 or base == 1:
+            raise PsispecError("by_parts needs original_length, fast > slow > 0 and a base other than 1")
+        # pair j turns original_length * base^(-2j/rot) / (2 pi) times
+        def border(turns):
+            return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+        lo = max(math.floor(border(fast)), 0)
+        hi = min(math.ceil(border(slow)), rot // 2 - 1)
+        mix = ((j - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - mix) + f / factor * mix
+        mag = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in ("none", "base"):
+        raise PsispecError(f"unknown scaling {scaling!r}")
+    return f.to(device), mag
+
+
+def psispec_qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
+                       n_new: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                       q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                       eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                       interleaved: bool = False, rope_scale: float = 1.0,
+                       k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                       q_out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Norm, position rotation and paged write of a block's rows.  q [batch][blk][heads_q][dim], k and
+    v [batch][blk][heads][dim] (bf16 or f16; views into one packed projection are fine); k_cache and
+    v_cache [pages][page_size][heads][dim] of any page, position and head strides (the same for both),
+    of q's dtype or float8_e4m3fn with k_scale / v_scale float32 [heads]; table int32 [batch][slots];
+    length int32 [batch].  Query and key heads are RMS-normalised when a weight [dim] is given; the
+    first 2 * inv_freq.numel() dimensions are rotated by position * inv_freq (float64, see
+    rope_frequencies), positions int32 [batch][blk] or length + i.  Row i of line r goes to position
+    length[r] + i; rows i >= n_new[r] (int32 [batch]) are left out.  Returns q_out (allocated when not
+    given; q itself rotates in place)."""
+    if q.dim() != 4:
+        raise PsispecError("q must be [batch][blk][heads_q][dim]")
+    batch, blk, hq, dim = q.shape
+    dev, dt = q.device, q.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise PsispecError(f"q must be bfloat16 or float16, got {dt}")
+    qp, qs = _token_rows(q, "q", dt, dev)
+    kp, ks = _token_rows(k, "k", dt, dev)
+    vp, vs = _token_rows(v, "v", dt, dev)
+    c = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
+    if k.shape != v.shape or tuple(k.shape) != (batch, blk, c.heads, dim) or c.dim != dim:
+        raise PsispecError("k and v must be [batch][blk][heads][dim] with the cache's heads and q's dim")
+    wp = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype != dt or tuple(w.shape) != (dim,):
+                raise PsispecError(f"{name} must be {dt} [dim]")
+            _same_dev(w, dev, name)
+        wp.append(None if w is None else _dev(w, name))
+    fp, rot = None, 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+            raise PsispecError("inv_freq must be float64 [rot/2]")
+        _same_dev(inv_freq, dev, "inv_freq")
+        fp, rot = _dev(inv_freq, "inv_freq"), 2 * inv_freq.numel()
+    lp = _int32(length, (batch,), dev, "length")
+    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
+    pp = None if positions is None else _int32(positions, (batch, blk), dev, "positions")
+    sp = None if status is None else _int32(status, (batch,), dev, "status")
+    prep = psispec_qkv_prep(wp[0], wp[1], fp, float(eps), float(rope_scale), rot,
+                            PSISPEC_ROPE_INTERLEAVED if interleaved else 0)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((batch, blk, hq, dim), dtype=dt, device=dev)
+        elif tuple(q_out.shape) != (batch, blk, hq, dim):
+            raise PsispecError("q_out must have the shape of q")
+        op, os_ = _token_rows(q_out, "q_out", dt, dev)
+        rc = lib().psispec_qkv_append(ctypes.byref(c), ctypes.byref(prep), qp, qs, kp, ks, vp, vs,
+                                      _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_, op, os_, sp,
+                                      _stream(None))
+    _check(rc, "psispec_qkv_append")
+    return q_out
+
+
+def paged_attention_workspace_bytes(batch, blk, heads_q, heads_kv, dim) -> int:
+    return int(lib().psispec_paged_attention_workspace(batch, blk, heads_q, heads_kv, dim))
+
+
+def psispec_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            table: torch.Tensor, length: torch.Tensor,
+                            n_new: torch.Tensor | None = None, parent: torch.Tensor | None = None,
+                            scale: float | None = None, k_scale: torch.Tensor | None = None,
+                            v_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of a block's queries over the paged cache.  q [batch][blk][heads_q][dim] (bf16 or
+    f16), heads_q a multiple of the cache's heads; k_cache, v_cache, table, k_scale and v_scale as in
+    psispec_qkv_append, which has written the block's rows at length[r] ..; length int32 [batch] counts
+    the rows before them.  Row i sees those, and of the block rows 0..i, or itself and its ancestors
+    under parent (int32 [batch][blk], -1 = none).  Rows i >= n_new[r] of out are left as they are (a
+    new out starts unspecified there).  scale defaults to dim ** -0.5."""
+    if q.dim() != 4:
+        raise PsispecError("q must be [batch][blk][heads_q][dim]")
+    batch, blk, hq, dim = q.shape
+    dev, dt = q.device, q.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise PsispecError(f"q must be bfloat16 or float16, got {dt}")
+    qp, qs = _token_rows(q, "q", dt, dev)
+    c = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
+    if c.dim != dim:
+        raise PsispecError("q and the cache must have the same dim")
+    lp = _int32(length, (batch,), dev, "length")
+    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
+    pp = None if parent is None else _int32(parent, (batch, blk), dev, "parent")
+    sp = None if status is None else _int32(status, (batch,), dev, "status")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((batch, blk, hq, dim), dtype=dt, device=dev)
+        elif tuple(out.shape) != (batch, blk, hq, dim):
+            raise PsispecError("out must have the shape of q")
+        op, os_ = _token_rows(out, "out", dt, dev)
+        workspace = _workspace_for(workspace,
+                                   paged_attention_workspace_bytes(batch, blk, hq, c.heads, dim), dev,
+                                   "psispec_paged_attention (blk 1..1024, heads_q a multiple of the "
+                                   "cache's heads, dim a multiple of 16 up to 256)")
+        rc = lib().psispec_paged_attention(
+            ctypes.byref(c), qp, qs, _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_,
+            dim ** -0.5 if scale is None else float(scale), op, os_, sp, workspace.data_ptr(),
+            workspace.numel(), _stream(None))
+    _check(rc, "psispec_paged_attention")
+    return out
+
+
+def psispec_paged_commit(pool: torch.Tensor, table: torch.Tensor, length: torch.Tensor, blk: int,
+                         n_keep: torch.Tensor, keep: torch.Tensor | None = None,
+                         new_length: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """psispec_kv_commit for lines in pages.  pool [planes][pages][page_size][...] (any dtype, rows of
+    16-byte multiples; e.g. layers x K and V as planes); table int32 [batch][slots].  The kept rows
+    keep[r][:n_keep[r]] of the block at length[r] move to length[r] onwards in every plane, and
+    new_length (length itself when not given) becomes length + n_keep.  Returns `status` (int32
+    [batch], ST_BAD_KEEP or ST_BAD_PAGE for an invalid line, which stays as it is) when given."""
+    batch, dev = length.shape[0] if length.dim() == 1 else -1, pool.device
+    c = _page_pool(pool)
+    lp = _int32(length, (batch,), dev, "length")
+    tp, ts, slots = _table(table, batch, dev)
+    kp = _int32(n_keep, (batch,), dev, "n_keep")
+    np_ = lp if new_length is None else _int32(new_length, (batch,), dev, "new_length")
+    sp = None if status is None else _int32(status, (batch,), dev, "status")
+    ks, keepp = 0, None
+    if keep is not None:
+        if keep.dim() != 2:
+            raise PsispecError("keep must be int32 [batch][k]")
+        ks = keep.shape[1]
+        keepp = _int32(keep, (batch, ks), dev, "keep")
+    with _on(dev, stream):
+        rc = lib().psispec_paged_commit(ctypes.byref(c), tp, ts, slots, batch, int(blk), keepp, ks, kp,
+                                        lp, np_, sp, _stream(None))
+    _check(rc, "psispec_paged_commit")
+    return status
+
+
+def pages_workspace_bytes(batch, slots, num_pages, blk, page_size) -> int:
+    return int(lib().psispec_pages_workspace(batch, slots, num_pages, blk, page_size))
+
+
+def psispec_pages_assign(table: torch.Tensor, refs: torch.Tensor, length: torch.Tensor,
+                         src: torch.Tensor, new_length: torch.Tensor, page_size: int,
+                         status: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor | None:
+    """Every line r becomes the first new_length[r] positions of the line src[r] (-1: empty) as it was
+    before the call, by sharing its pages: forks, cuts, frees and reorders lines.  table int32
+    [batch][slots], refs int32 [pages] (table entries that name each page; 0 = free) and length int32
+    [batch] are updated in place.  Returns `status` (ST_BAD_PAGE for an invalid line, which stays as
+    it is) when given."""
+    batch, dev = length.shape[0] if length.dim() == 1 else -1, table.device
+    lp = _int32(length, (batch,), dev, "length")
+    tp, ts, slots = _table(table, batch, dev)
+    if refs.dim() != 1:
+        raise PsispecError("refs must be int32 [pages]")
+    rp = _int32(refs, tuple(refs.shape), dev, "refs")
+    srcp, nlp = _int32(src, (batch,), dev, "src"), _int32(new_length, (batch,), dev, "new_length")
+    sp = None if status is None else _int32(status, (batch,), dev, "status")
+    with _on(dev, stream):
+        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, refs.shape[0], 1,
+                                                                    int(page_size)), dev,
+                                   "psispec_pages_assign")
+        rc = lib().psispec_pages_assign(tp, ts, slots, rp, refs.shape[0], int(page_size), lp, srcp, nlp,
+                                        sp, batch, workspace.data_ptr(), workspace.numel(),
+                                        _stream(None))
+    _check(rc, "psispec_pages_assign")
+    return status
+
+
+def psispec_pages_reserve(pool: torch.Tensor, table: torch.Tensor, refs: torch.Tensor,
+                          length: torch.Tensor, blk: int, n_new: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor | None:
+    """Pages of its own for the next n_new[r] (int32 [batch]; blk when None) positions of every line,
+    from the lowest-numbered free ones; a tail page that other lines hold too is copied first (pool
+    [planes][pages][page_size][...], as in psispec_paged_commit).  table and refs are updated in place.
+    Returns `status` when given: ST_NO_PAGE for a line that the free pages did not reach, ST_BAD_PAGE
+    for an invalid one; such lines stay as they are."""
+    batch, dev = length.shape[0] if length.dim() == 1 else -1, pool.device
+    c = _page_pool(pool)
+    lp = _int32(length, (batch,), dev, "length")
+    tp, ts, slots = _table(table, batch, dev)
+    rp = _int32(refs, (c.num_pages,), dev, "refs")
+    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
+    sp = None if status is None else _int32(status, (batch,), dev, "status")
+    with _on(dev, stream):
+        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, c.num_pages, int(blk),
+                                                                    c.page_size), dev,
+                                   "psispec_pages_reserve")
+        rc = lib().psispec_pages_reserve(ctypes.byref(c), tp, ts, slots, rp, lp, np_, int(blk), sp,
+                                         batch, workspace.data_ptr(), workspace.numel(), _stream(None))
+    _check(rc, "psispec_pages_reserve")
     return status
 
 

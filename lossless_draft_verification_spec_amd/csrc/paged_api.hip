@@ -1,0 +1,270 @@
+// paged_api.hip -- the C ABI of the paged KV cache: argument checks, then the launches of append.hip,
+// attend.hip and pages.hip.
+#include <limits.h>
+#include <math.h>
+
+#include "paged.h"
+
+using namespace psispec;
+
+namespace {
+
+constexpr int kMaxHeads = 1024;
+constexpr int64_t kMaxPositions = int64_t(1) << 30;
+
+bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
+
+// A grid of `blocks` workgroups can be launched: at most 2^32 - 1 threads in x, of 256 each.
+bool grid_ok(int64_t blocks) { return blocks <= (int64_t(1) << 24) - 1; }
+
+psispec_status check_cache(const psispec_paged_cache* c, psispec_dtype dtype) {
+  if (!c) return PSISPEC_EINVAL;
+  if (dtype != PSISPEC_BF16 && dtype != PSISPEC_F16) return PSISPEC_EDTYPE;
+  if (c->dtype != (int32_t)dtype && c->dtype != PSISPEC_F8E4M3) return PSISPEC_EDTYPE;
+  if (c->num_pages < 1 || c->page_size < 1 || c->page_size > kMaxPageSize || c->slots < 1 ||
+      (int64_t)c->slots * c->page_size > kMaxPositions || c->table_stride < c->slots)
+    return PSISPEC_EINVAL;
+  if (c->heads < 1 || c->heads > kMaxHeads || c->dim < 16 || c->dim > kMaxHeadDim || c->dim % 16)
+    return PSISPEC_EINVAL;
+  const int64_t es = c->dtype == PSISPEC_F8E4M3 ? 1 : 2;
+  if (c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0 || (c->page_stride * es) % 16 ||
+      (c->row_stride * es) % 16 || (c->head_stride * es) % 16)
+    return PSISPEC_EINVAL;
+  if (c->dtype != PSISPEC_F8E4M3 && (c->k_scale || c->v_scale)) return PSISPEC_EINVAL;
+  return PSISPEC_OK;
+}
+
+bool cache_pointers_ok(const psispec_paged_cache* c) {
+  return c->k && c->v && c->table && aligned(c->k, 16) && aligned(c->v, 16);
+}
+
+// Rows of `width` contiguous elements, `stride` elements apart, read and written 16 bytes at a time.
+bool rows_ok(const void* p, int64_t stride, int64_t width) {
+  return p && aligned(p, 16) && stride >= width && stride % 8 == 0;
+}
+
+psispec_status check_pool(const psispec_page_pool* p) {
+  if (!p || p->reserved != 0) return PSISPEC_EINVAL;
+  if (p->planes < 1 || p->num_pages < 1 || p->page_size < 1 || p->page_size > kMaxPageSize)
+    return PSISPEC_EINVAL;
+  if (p->row_bytes < 16 || p->row_bytes % 16 || p->row_bytes > (int64_t(1) << 32) ||
+      p->plane_stride % 16 || p->page_stride % 16 || p->plane_stride < 0 ||
+      p->page_stride < p->page_size * p->row_bytes)
+    return PSISPEC_EINVAL;
+  return PSISPEC_OK;
+}
+
+bool slots_ok(int32_t slots, int64_t table_stride, int32_t page_size) {
+  return slots >= 1 && table_stride >= slots && (int64_t)slots * page_size <= kMaxPositions;
+}
+
+}  // namespace
+
+extern "C" {
+
+psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qkv_prep* p,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, psispec_dtype dtype,
+                                  int32_t batch, int32_t blk, int32_t heads_q,
+                                  const int32_t* positions, const int32_t* len,
+                                  const int32_t* n_new, void* q_out, int64_t q_out_stride,
+                                  int32_t* status, void* stream) {
+  const psispec_status e = check_cache(c, dtype);
+  if (e != PSISPEC_OK) return e;
+  if (batch < 0 || blk < 1 || blk > kMaxAppendBlock || heads_q < 1 || heads_q > kMaxHeads || !p)
+    return PSISPEC_EINVAL;
+  // two rows of a line may not share their place
+  if (c->head_stride < c->dim && c->heads > 1) return PSISPEC_EINVAL;
+  if ((c->row_stride < c->dim && c->page_size > 1) || (c->page_stride < c->dim && c->num_pages > 1))
+    return PSISPEC_EINVAL;
+  if (!(p->eps >= 0.0) || !isfinite(p->eps) || !isfinite(p->rope_scale) || p->rot < 0 ||
+      p->rot > c->dim || p->rot % 16 || (p->flags & ~PSISPEC_ROPE_INTERLEAVED) ||
+      (p->rot > 0 && !p->inv_freq) || !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16))
+    return PSISPEC_EINVAL;
+  if (!grid_ok((int64_t)batch * blk)) return PSISPEC_EINVAL;
+  if (batch == 0) return PSISPEC_OK;
+  if (!cache_pointers_ok(c) || !len) return PSISPEC_EINVAL;
+  const int64_t wq = (int64_t)heads_q * c->dim, wk = (int64_t)c->heads * c->dim;
+  if (!rows_ok(q, q_stride, wq) || !rows_ok(k, k_stride, wk) || !rows_ok(v, v_stride, wk) ||
+      !rows_ok(q_out, q_out_stride, wq))
+    return PSISPEC_EINVAL;
+  AppendArgs a{};
+  a.c = *c;
+  a.p = *p;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.positions = positions;
+  a.len = len;
+  a.n_new = n_new;
+  a.status = status;
+  a.batch = batch;
+  a.blk = blk;
+  a.heads_q = heads_q;
+  return launch_qkv_append(a, dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? PSISPEC_OK
+                                                                                    : PSISPEC_EHIP;
+}
+
+static bool attend_sizes_ok(int32_t batch, int32_t blk, int32_t heads_q, int32_t heads_kv,
+                            int32_t dim) {
+  return batch >= 0 && blk >= 1 && blk <= kMaxAttendBlock && heads_kv >= 1 && heads_q >= heads_kv &&
+         heads_q <= kMaxHeads && heads_q % heads_kv == 0 && dim >= 16 && dim <= kMaxHeadDim &&
+         dim % 16 == 0 && grid_ok((int64_t)batch * blk * heads_q);
+}
+
+size_t psispec_paged_attention_workspace(int32_t batch, int32_t blk, int32_t heads_q,
+                                         int32_t heads_kv, int32_t dim) {
+  if (!attend_sizes_ok(batch, blk, heads_q, heads_kv, dim)) return 0;
+  return attend_workspace_bytes(batch, blk, heads_q, heads_kv, dim);
+}
+
+psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void* q, int64_t q_stride,
+                                       psispec_dtype dtype, int32_t batch, int32_t blk,
+                                       int32_t heads_q, const int32_t* parent, const int32_t* len,
+                                       const int32_t* n_new, double scale, void* out,
+                                       int64_t out_stride, int32_t* status, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  const psispec_status e = check_cache(c, dtype);
+  if (e != PSISPEC_OK) return e;
+  if (!attend_sizes_ok(batch, blk, heads_q, c->heads, c->dim) || !isfinite((float)scale))
+    return PSISPEC_EINVAL;
+  if (batch == 0) return PSISPEC_OK;
+  const int64_t wq = (int64_t)heads_q * c->dim;
+  if (!cache_pointers_ok(c) || !len || !rows_ok(q, q_stride, wq) || !rows_ok(out, out_stride, wq))
+    return PSISPEC_EINVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attend_workspace_bytes(batch, blk, heads_q, c->heads, c->dim))
+    return PSISPEC_EWORKSPACE;
+  AttendArgs a{};
+  a.c = *c;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.parent = parent;
+  a.len = len;
+  a.n_new = n_new;
+  a.status = status;
+  a.scale = (float)scale;
+  a.batch = batch;
+  a.blk = blk;
+  a.heads_q = heads_q;
+  return launch_attend(a, dtype, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? PSISPEC_OK
+             : PSISPEC_EHIP;
+}
+
+psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t* table,
+                                    int64_t table_stride, int32_t slots, int32_t batch, int32_t blk,
+                                    const int32_t* keep, int32_t keep_stride, const int32_t* n_keep,
+                                    const int32_t* len, int32_t* new_len, int32_t* status,
+                                    void* stream) {
+  const psispec_status e = check_pool(pool);
+  if (e != PSISPEC_OK) return e;
+  if (batch < 0 || blk < 1 || blk > kMaxKvBlock || !slots_ok(slots, table_stride, pool->page_size) ||
+      blk > (int64_t)slots * pool->page_size || (keep && keep_stride < 1))
+    return PSISPEC_EINVAL;
+  const int64_t tiles = pool->row_bytes / 16 > (int64_t(1) << 32) / pool->planes
+                            ? INT64_C(1) << 32
+                            : pool->planes * (pool->row_bytes / 16) / 256 + 1;
+  if (!grid_ok(tiles) || !grid_ok(batch * tiles)) return PSISPEC_EINVAL;
+  if (batch == 0) return PSISPEC_OK;
+  if (!pool->base || !aligned(pool->base, 16) || !table || !n_keep || !len || !new_len)
+    return PSISPEC_EINVAL;
+  PagedCommitArgs a{};
+  a.pool = *pool;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.slots = slots;
+  a.batch = batch;
+  a.blk = blk;
+  a.keep = keep;
+  a.keep_stride = keep_stride;
+  a.n_keep = n_keep;
+  a.len = len;
+  a.new_len = new_len;
+  a.status = status;
+  return launch_paged_commit(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PSISPEC_OK
+                                                                               : PSISPEC_EHIP;
+}
+
+static size_t pages_ws(int32_t batch, int32_t slots, int32_t num_pages, int32_t blk,
+                       int32_t page_size) {
+  if (batch < 0 || batch > (1 << 24) || slots < 1 || num_pages < 1 || blk < 1 ||
+      blk > kMaxAppendBlock || page_size < 1 || page_size > kMaxPageSize ||
+      (int64_t)slots * page_size > kMaxPositions)
+    return 0;
+  return pages_workspace_bytes(batch, slots, num_pages, blk, page_size);
+}
+
+size_t psispec_pages_workspace(int32_t batch, int32_t slots, int32_t num_pages, int32_t blk,
+                               int32_t page_size) {
+  return pages_ws(batch, slots, num_pages, blk, page_size);
+}
+
+psispec_status psispec_pages_assign(int32_t* table, int64_t table_stride, int32_t slots,
+                                    int32_t* refs, int32_t num_pages, int32_t page_size,
+                                    int32_t* len, const int32_t* src, const int32_t* new_len,
+                                    int32_t* status, int32_t batch, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  const size_t need = pages_ws(batch, slots, num_pages, 1, page_size);
+  if (need == 0 || table_stride < slots) return PSISPEC_EINVAL;
+  if (batch == 0) return PSISPEC_OK;
+  if (!table || !refs || !len || !src || !new_len) return PSISPEC_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PSISPEC_EWORKSPACE;
+  AssignArgs a{};
+  a.table = table;
+  a.table_stride = table_stride;
+  a.slots = slots;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.batch = batch;
+  a.refs = refs;
+  a.len = len;
+  a.src = src;
+  a.new_len = new_len;
+  a.status = status;
+  return launch_pages_assign(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? PSISPEC_OK
+             : PSISPEC_EHIP;
+}
+
+psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* table,
+                                     int64_t table_stride, int32_t slots, int32_t* refs,
+                                     const int32_t* len, const int32_t* n_new, int32_t blk,
+                                     int32_t* status, int32_t batch, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  const psispec_status e = check_pool(pool);
+  if (e != PSISPEC_OK) return e;
+  if (!slots_ok(slots, table_stride, pool->page_size)) return PSISPEC_EINVAL;
+  const size_t need = pages_ws(batch, slots, pool->num_pages, blk, pool->page_size);
+  if (need == 0) return PSISPEC_EINVAL;
+  const int64_t per_plane = pool->page_size * pool->row_bytes / 16384 + 1;
+  if (!grid_ok(per_plane) || !grid_ok(per_plane * pool->planes) ||
+      !grid_ok(batch * (per_plane * pool->planes)))
+    return PSISPEC_EINVAL;
+  if (batch == 0) return PSISPEC_OK;
+  if (!pool->base || !aligned(pool->base, 16) || !table || !refs || !len) return PSISPEC_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PSISPEC_EWORKSPACE;
+  ReserveArgs a{};
+  a.pool = *pool;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.slots = slots;
+  a.blk = blk;
+  a.batch = batch;
+  a.refs = refs;
+  a.len = len;
+  a.n_new = n_new;
+  a.status = status;
+  return launch_pages_reserve(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? PSISPEC_OK
+             : PSISPEC_EHIP;
+}
+
+}  // extern "C"
