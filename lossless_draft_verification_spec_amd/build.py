@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpsispec.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "rows.hip", "topp.hip", "linear.hip", "tree.hip", "draw.hip", "drafts.hip",
-           "kv.hip", "treeq.hip", "lmhead.hip", "peak.hip", "append.hip", "attend.hip", "pages.hip",
+           "kv.hip", "treeq.hip", "lmhead.hip", "peak.hip", "append.hip", "attend.hip", "attend_bf16.hip",
+           "attend_f16.hip", "attend_bf16_f8.hip", "attend_f16_f8.hip", "pages.hip",
            "paged_api.hip"]
 ARCH = "gfx950"
 

@@ -1,0 +1,776 @@
+// attend.h -- the attention kernel over the paged cache (one instantiation set per translation unit).
+//
+//   out_m = sum_t w_mt v_t / sum_t w_mt,  w_mt = exp2(x_mt - max), x_mt = scale log2(e) q_m . k_t
+//
+// One key/value head serves G query heads, so its query rows (block row i, head g) -> m = i G + g share
+// every key and value read: they form the 16-row tiles of the matrix products.  A workgroup's job is
+// (line, key/value head, group of up to 16 MT rows); its four waves take disjoint runs of 32-position
+// tiles, each with softmax statistics of its own, and are joined at the end.
+//
+// Products (v_mfma_f32_16x16x32, 32-bit sums).  Transposed, so that a lane owns one query row:
+//   S^T = K Q^T   A = 16 positions x 32 dims of K, B = Q (in registers for the whole job)
+//   O^T = V^T P^T A = 16 dims x 32 positions of V (transposing LDS reads), B = P
+// The lane (row l % 16, group g = l / 16) that gets scores of positions 4g..4g+3 of both 16-position
+// halves holds exactly the B fragment of the second product when its contraction index (g, j) is
+// read as position 16 (j / 4) + 4 g + j % 4: weights go from one product to the next in registers.
+// The running maximum and sum are per lane; the maximum is raised (and sums rescaled) only when a score
+// exceeds it by more than 2^8, so most tiles need no exchange between lanes.  P is split into a
+// 16-bit pair (hi + lo, relative error 2^-16) and multiplied twice: a single 16-bit P would add an
+// error as large as the output's own rounding, and the product is not what bounds the kernel.
+//
+// Memory.  K and V go from HBM to LDS by 16-byte direct loads (no registers), each wave into a
+// ring of its own (no barrier in the loop): K and V of a tile have separate places, each refilled as
+// soon as its product is done, so one of the two is always in flight.  A row's 16-byte chunks are
+// permuted by its position (on the load's source side) so that the reads of 16 rows at one chunk
+// meet no LDS bank twice.  Page ids come 64 at a time, one in each lane.
+//
+// Work.  All jobs of the call laid end to end, in steps of 128 positions, are cut into one equal
+// share per workgroup, however uneven the lines are; a job cut by a border leaves its parts (maximum,
+// sum, unnormalised output in 32 bits) in the workspace and k_attend_join adds them in order.
+#pragma once
+
+#include <type_traits>
+
+#include "paged.h"
+
+namespace psispec {
+
+constexpr int kAttendCUs = 256;
+constexpr int kAttendWaves = 4;
+constexpr int kAttendThreads = 64 * kAttendWaves;
+constexpr int kAttendTile = 32;                          // positions per tile
+constexpr int kAttendStep = kAttendTile * kAttendWaves;  // positions per step of the shares
+
+// The job that starts in a workgroup's share and ends in a later one (parts == 0: none).
+struct AttendInfo {
+  int32_t r, h, mt, parts, slot, pad[3];
+};
+
+struct AttendPlan {
+  int mt;         // 16-row tiles per job
+  int nmt;        // groups of 16 mt rows per (line, head)
+  int dp;         // head dimension rounded up to 64, 128 or 256
+  int wgs;        // shares
+  int mask_words; // 64-bit words of a block row's mask (tree)
+  size_t off_ml, off_o, off_mask, total;
+};
+
+struct AttendKernelArgs {
+  AttendArgs a;
+  int G, nmt, mask_words, wgs;
+  uint32_t ps_magic;         // ceil(2^32 / page_size)
+  int row_groups;            // the rows of one load instruction lie in one page, within 2^31 bytes
+  float c;                   // scale log2(e)
+  AttendInfo* info;          // [wgs]
+  float2* ml;                // [2 wgs][16 MT]
+  float* o;                  // [2 wgs][16 MT][DP]
+  const uint64_t* mask;      // [batch][blk][mask_words] or null
+};
+
+// rows of a job that are live and the positions that it reads
+__device__ __host__ inline int job_keys(int L, int n, int G, int mt, int rows) {
+  const int first = mt * rows / G;
+  if (first >= n) return 0;
+  int last = (mt * rows + rows - 1) / G;
+  if (last > n - 1) last = n - 1;
+  return L + last + 1;
+}
+
+// Two workgroups per CU (64 KiB rings, 256 registers per lane) for up to four row tiles of heads up to
+// 128, one (128 KiB, 512 registers) beyond.
+__host__ __device__ constexpr bool attend_two(int rb, int dp, int mt) {
+  return rb <= 256 && dp <= 128 && mt * dp <= 384 && mt <= 4;
+}
+
+// Launchers, one per translation unit
+hipError_t launch_attend_bf16(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream);
+hipError_t launch_attend_f16(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream);
+hipError_t launch_attend_bf16_f8(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream);
+hipError_t launch_attend_f16_f8(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream);
+
+namespace attend {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+template <typename T> struct Elem;
+template <> struct Elem<__bf16> {
+  typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 x4 __attribute__((ext_vector_type(4)));
+  typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+  static constexpr uint32_t kExp = 0x7f80u;
+  __device__ static f32x4 mfma(x8 a, x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI> __device__ static x2 from_f8(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
+  }
+  __device__ static x4 tr(const __attribute__((address_space(3))) x4* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) x4*)p);
+  }
+};
+template <> struct Elem<_Float16> {
+  typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 x4 __attribute__((ext_vector_type(4)));
+  typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+  static constexpr uint32_t kExp = 0x7c00u;
+  __device__ static f32x4 mfma(x8 a, x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI> __device__ static x2 from_f8(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
+  }
+  __device__ static x4 tr(const __attribute__((address_space(3))) x4* p) {
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                      (__attribute__((address_space(3))) i16x4*)p));
+  }
+};
+
+// LDS reads.  The restrict-qualified (inlined) parameters give the accesses alias scopes of their
+// own, so the compiler adds no wait for the direct-to-LDS loads in flight: the kernel orders those
+// itself (vmcnt waits before a tile is read, a wait for its reads before it is refilled).
+template <typename V>
+__device__ __attribute__((always_inline)) inline V lds_read(const char* __restrict__ p) {
+  return *reinterpret_cast<const V*>(p);
+}
+template <typename T>
+__device__ __attribute__((always_inline)) inline typename Elem<T>::x4 lds_tr16(
+    const char* __restrict__ p) {
+  typedef typename Elem<T>::x4 x4;
+  return Elem<T>::tr((const __attribute__((address_space(3))) x4*)p);
+}
+__device__ __attribute__((always_inline)) inline i32x2 lds_tr8(const char* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
+}
+
+// eight 8-bit numbers as T (exact)
+template <typename T>
+__device__ inline typename Elem<T>::x8 widen(uint32_t w0, uint32_t w1) {
+  typedef Elem<T> E;
+  typename E::x8 y;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const typename E::x2 lo = E::template from_f8<false>(e ? w1 : w0);
+    const typename E::x2 hi = E::template from_f8<true>(e ? w1 : w0);
+    y[4 * e] = lo[0];
+    y[4 * e + 1] = lo[1];
+    y[4 * e + 2] = hi[0];
+    y[4 * e + 3] = hi[1];
+  }
+  return y;
+}
+
+// all ones in the places of a word's finite elements, zeros in those of NaN and infinities
+template <typename T, bool F8> __device__ inline uint32_t finite_mask(uint32_t w) {
+  uint32_t m = ~0u;
+  if constexpr (F8) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (((w >> (8 * b)) & 0x7fu) == 0x7fu) m &= ~(0xffu << (8 * b));
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (((w >> (16 * b)) & Elem<T>::kExp) == Elem<T>::kExp) m &= ~(0xffffu << (16 * b));
+  }
+  return m;
+}
+
+// Wait until at most n (wave-uniform) loads are outstanding; a smaller count waits longer.
+template <int UNIT> __device__ inline void wait_vm(int units) {
+  // units of UNIT loads; counts above 63 do not exist
+  if (units <= 0)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  else if (units == 1)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(UNIT) : "memory");
+  else if (units == 2)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * UNIT) : "memory");
+  else if (units == 3)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * UNIT > 63 ? 63 : 3 * UNIT) : "memory");
+  else if (units == 4)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * UNIT > 63 ? 63 : 4 * UNIT) : "memory");
+  else if (units == 5)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * UNIT > 63 ? 63 : 5 * UNIT) : "memory");
+  else if (units == 6)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * UNIT > 63 ? 63 : 6 * UNIT) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(7 * UNIT > 63 ? 63 : 7 * UNIT) : "memory");
+}
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Maximum / sum over the four 16-lane groups of a wave (lanes l, l^16, l^32, l^48).
+__device__ inline float group_max(float x) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float group_sum(float x) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Exclusive sum over the workgroup; *total: the whole.  s: one int64 of LDS per wave.
+__device__ inline int64_t block_scan(int64_t x, int64_t* s, int64_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t inc = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t y = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 63) s[wave] = inc;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttendWaves; ++w) {
+    before += w < wave ? s[w] : 0;
+    all += s[w];
+  }
+  *total = all;
+  return before + inc - x;
+}
+
+// steps of job group mt of a line
+__device__ inline int job_steps(int L, int n, int G, int mt, int rows) {
+  const int keys = job_keys(L, n, G, mt, rows);
+  return (keys + kAttendStep - 1) / kAttendStep;
+}
+__device__ inline int64_t line_steps(const AttendKernelArgs& k, int r, int rows) {
+  int L, n;
+  if (!line_rows(k.a.len, k.a.n_new, r, k.a.blk, k.a.c.slots, k.a.c.page_size, &L, &n) || n == 0)
+    return 0;
+  int64_t s = 0;
+  for (int mt = 0; mt < k.nmt; ++mt) s += job_steps(L, n, k.G, mt, rows);
+  return s * k.a.c.heads;
+}
+
+// A workgroup's LDS: the waves' rings of K and V tiles, and for many rows the queries.
+template <int RB, int MT, int DP> struct Shape {
+  static constexpr bool kTwo = attend_two(RB, DP, MT);
+  static constexpr int kStage = 2 * kAttendTile * RB;  // K and V of one tile
+  static constexpr int kRing = (kTwo ? 65536 : 131072) / kAttendWaves;
+  static constexpr int kStages = kRing / kStage;
+  static constexpr int kPerCU = kTwo ? 2 : 1;
+  static constexpr bool kQLds = MT * DP > 256;         // the queries' fragments stay in LDS
+  static constexpr int kLds = kRing * kAttendWaves + (kQLds ? MT * 16 * DP * 2 : 0);
+};
+
+// Where chunk c of row `row` lies in the row: at c ^ swz(row).  Both are bitwise in the row (so
+// swz(a + b) = swz(a) ^ swz(b) for disjoint bits), and chosen so that the lanes of one read spread over
+// all banks: a K read takes one chunk of 16 rows, a 16-bit V read two neighbouring chunks of 8 rows
+// per half wave, an 8-bit V read one chunk of 16 rows (0-7 and 16-23) per half wave.
+template <int RB> __device__ __host__ constexpr int swz_k(int row) {
+  return (row / (RB >= 256 ? 1 : 256 / RB)) & ((RB >= 256 ? 16 : RB / 16) - 1);
+}
+template <int RB, bool F8> __device__ __host__ constexpr int swz_v(int row) {
+  return F8 ? (((row & 7) | ((row >> 4) & 1) << 3) / (RB >= 256 ? 1 : 256 / RB)) &
+                  ((RB >= 256 ? 16 : RB / 16) - 1)
+            : ((row / (RB >= 256 ? 1 : 256 / RB)) & ((RB >= 256 ? 16 : RB / 16) / 2 - 1)) << 1;
+}
+
+template <typename T, bool F8, int DP, int MT>
+__global__ __launch_bounds__(kAttendThreads, (Shape<(F8 ? 1 : 2) * DP, MT, DP>::kPerCU))
+void k_attend(AttendKernelArgs k) {
+  typedef Elem<T> E;
+  typedef typename E::x4 x4;
+  typedef typename E::x8 x8;
+  constexpr int ES = F8 ? 1 : 2;
+  constexpr int RB = DP * ES;                 // bytes of a row in LDS
+  typedef Shape<RB, MT, DP> Sh;
+  constexpr int NST = Sh::kStages;
+  constexpr int CPR = RB / 16;                // 16-byte chunks of a row
+  constexpr int RPI = 1024 / RB;              // rows that one load instruction fills
+  constexpr int TILE = kAttendTile * RB;
+  constexpr int NLD = TILE / 1024;            // load instructions per tile of K or V
+  constexpr int ROWS = 16 * MT;
+  constexpr int NT = DP / 16;                 // 16-dim tiles of the output
+  constexpr int KS = DP / 32;                 // contraction steps of the first product
+  static_assert(NST >= 1 && 4 * NST * NLD * 2 * 1024 <= 131072, "the ring fits the LDS");
+  static_assert(16 * (DP + 4) * 4 <= Sh::kRing, "a wave's part of the output fits its ring");
+
+  constexpr bool kQLds = Sh::kQLds;
+  extern __shared__ __align__(1024) char ring[];  // [waves][stages][K tile, V tile], then queries
+  char* const q_lds = ring + Sh::kRing * kAttendWaves;
+  __shared__ float s_m[kAttendWaves][ROWS], s_l[kAttendWaves][ROWS];
+  __shared__ int64_t s_scan[kAttendWaves];
+  __shared__ int64_t s_base;
+  __shared__ int s_line;
+
+  const AttendArgs& a = k.a;
+  const psispec_paged_cache& c = a.c;
+  const int G = k.G, dim = c.dim;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n16 = lane & 15, g = lane >> 4;
+  const int ps = c.page_size;
+
+  // ---- this workgroup's share [x, x_end) of all steps, and the line that holds step x
+  int64_t total = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += kAttendThreads) {
+    const int r = r0 + tid;
+    total += r < a.batch ? line_steps(k, r, ROWS) : 0;
+  }
+  int64_t all;
+  block_scan(total, s_scan, &all);
+  const int64_t shares = all < k.wgs ? all : k.wgs;
+  const int64_t w = blockIdx.x;
+  if (w >= shares) {
+    if (tid == 0) k.info[w].parts = 0;
+    return;
+  }
+  int64_t x = all * w / shares;
+  const int64_t x_end = all * (w + 1) / shares;
+  int64_t base = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += kAttendThreads) {
+    const int r = r0 + tid;
+    const int64_t mine = r < a.batch ? line_steps(k, r, ROWS) : 0;
+    int64_t part;
+    const int64_t at = base + block_scan(mine, s_scan, &part);
+    if (at <= x && x < at + mine) {
+      s_line = r;
+      s_base = at;
+    }
+    base += part;
+    if (base > x) break;
+  }
+  __syncthreads();
+  int r = s_line;
+  int64_t off = x - s_base;  // step within the line's jobs
+  if (tid == 0) k.info[w].parts = 0;
+
+  char* const my_ring = ring + wave * Sh::kRing;
+  bool first_segment = true;
+
+  for (;; ++r) {  // lines of the share
+    int L, n;
+    const bool live_line =
+        line_rows(a.len, a.n_new, r, a.blk, c.slots, ps, &L, &n) && n > 0;
+    if (!live_line) continue;  // cannot run past the batch: steps are left
+    const int32_t* const tab = c.table + (int64_t)r * c.table_stride;
+    for (int h = 0; h < c.heads && x < x_end; ++h) {
+      for (int mt0 = 0; mt0 < k.nmt && x < x_end; ++mt0) {
+        const int keys = job_keys(L, n, G, mt0, ROWS);
+        const int steps = (keys + kAttendStep - 1) / kAttendStep;
+        if (off >= steps) {
+          off -= steps;
+          continue;
+        }
+        // ---- segment: steps [off, off + ns) of the job
+        const int ns = (int)(steps - off < x_end - x ? steps - off : x_end - x);
+        const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
+        const int tile0 = (int)off * kAttendWaves;
+        const int tile1 = min(tile0 + ns * kAttendWaves, ntiles);
+        const int cnt = tile1 - tile0;
+        const int t0 = tile0 + cnt * wave / kAttendWaves;
+        const int t1 = tile0 + cnt * (wave + 1) / kAttendWaves;
+
+        // ---- loads: tile t into stage t % NST
+        const int chunks = dim * ES / 16;       // real chunks of a row
+        const int64_t head_off = (int64_t)h * c.head_stride * ES;
+        const char* const kbase = static_cast<const char*>(c.k) + head_off;
+        const char* const vbase = static_cast<const char*>(c.v) + head_off;
+        int tab_chunk = -1, tab_now = 0, tab_next = 0;
+        const int last_slot = (keys - 1) / ps;
+        auto fetch_tab = [&](int chunk) {
+          const int s = chunk * 64 + lane;
+          int p = tab[s < last_slot ? s : last_slot];
+          return (uint32_t)p < (uint32_t)c.num_pages ? p : 0;  // a bad id stays in bounds
+        };
+        // tile t into `to`: row i * RPI + lane / CPR of each load instruction; rows behind the job's
+        // last position are read as the last
+        auto issue = [&](int t, const char* from, char* to, auto is_v) {
+          const int chunk = t * kAttendTile / (64 * ps);  // tiles never straddle 64 pages
+          if (chunk != tab_chunk) {
+            tab_now = chunk == tab_chunk + 1 && tab_chunk >= 0 ? tab_next : fetch_tab(chunk);
+            tab_chunk = chunk;
+            tab_next = fetch_tab(chunk + 1);
+          }
+          const int rel0 = t * kAttendTile - chunk * 64 * ps;
+          const int lim = keys - 1 - chunk * 64 * ps;
+          const int lane_row = lane / CPR;
+          const int swz = is_v() ? swz_v<RB, F8>(lane_row) : swz_k<RB>(lane_row);
+          const int lane_chunk = (lane % CPR) ^ swz;
+          if (k.row_groups) {  // the rows of one instruction lie in one page
+#pragma unroll
+            for (int i = 0; i < NLD; ++i) {
+              const int rel = min(rel0 + i * RPI, lim);
+              const int idx = ps == 1 ? rel : (int)__umulhi((uint32_t)rel, k.ps_magic);
+              const int page = __builtin_amdgcn_readlane(tab_now, idx);
+              const char* const at =
+                  from + ((int64_t)page * c.page_stride + (int64_t)(rel - idx * ps) * c.row_stride) * ES;
+              const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
+              const uint32_t lofs =
+                  (uint32_t)(min(lane_row, lim - rel) * (int)c.row_stride * ES + (ch << 4));
+              if (ch < chunks)
+                __builtin_amdgcn_global_load_lds((global_void*)(at + lofs), (lds_void*)(to + i * 1024), 16,
+                                                 0, 0);
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < NLD; ++i) {
+              const int rel = min(rel0 + i * RPI + lane_row, lim);
+              const int idx = ps == 1 ? rel : (int)__umulhi((uint32_t)rel, k.ps_magic);
+              const int page = __shfl(tab_now, idx, 64);
+              const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
+              const char* const at =
+                  from + ((int64_t)page * c.page_stride + (int64_t)(rel - idx * ps) * c.row_stride) * ES +
+                  (ch << 4);
+              if (ch < chunks)
+                __builtin_amdgcn_global_load_lds((global_void*)at, (lds_void*)(to + i * 1024), 16, 0, 0);
+            }
+          }
+        };
+        // ---- queries: row n16 of each 16-row tile, in registers, or for many rows in LDS in the
+        // order of the fragments
+        x8 qf[kQLds ? 1 : MT][kQLds ? 1 : KS];
+        int irow[MT];  // block row, or -1 behind the job's last
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int m = mt0 * ROWS + mt * 16 + n16;
+          const int i = m / G;
+          irow[mt] = i < n ? i : -1;
+          const T* q = static_cast<const T*>(k.a.q) +
+                       ((int64_t)r * k.a.blk + (i < n ? i : 0)) * k.a.q_stride +
+                       (int64_t)(h * G + (m - i * G)) * dim;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if (kQLds && (mt * KS + s) % kAttendWaves != wave) continue;
+            // the dims of the lane's K fragment: 16-bit rows, chunk 4 s + g; 8-bit rows, half s % 2 of
+            // chunk 4 (s / 2) + g
+            const int d = F8 ? (4 * (s >> 1) + g) * 16 + (s & 1) * 8 : (4 * s + g) * 8;
+            x8 z = {};
+            if (d < dim && i < n) z = *reinterpret_cast<const x8*>(q + d);
+            if constexpr (kQLds)
+              *reinterpret_cast<x8*>(q_lds + ((mt * KS + s) * 64 + lane) * 16) = z;
+            else
+              qf[mt][s] = z;
+          }
+        }
+        const float sc = k.c * (F8 && c.k_scale ? c.k_scale[h] : 1.0f);
+        if constexpr (kQLds) __syncthreads();
+
+        char* const stage0 = my_ring;
+        if (dim != DP) {  // the chunks behind the head's last are never loaded
+          for (int b = lane * 16; b < Sh::kRing; b += 1024)
+            *reinterpret_cast<u32x4*>(my_ring + b) = u32x4{0, 0, 0, 0};
+          wait_lds();
+        }
+#pragma unroll
+        for (int s = 0; s < NST; ++s) {
+          if (t0 + s < t1) {
+            issue(t0 + s, kbase, stage0 + s * Sh::kStage, std::false_type{});
+            issue(t0 + s, vbase, stage0 + s * Sh::kStage + TILE, std::true_type{});
+          }
+        }
+
+        f32x4 acc[MT][NT];
+        float m_run[MT], l_run[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          m_run[mt] = kNegBig;
+          l_run[mt] = 0.0f;
+#pragma unroll
+          for (int d = 0; d < NT; ++d) acc[mt][d] = f32x4{0, 0, 0, 0};
+        }
+
+        // Positions pos0 .. pos0 + 31 that block row i (-1: none) sees, as bits; some reach behind L.
+        auto visible = [&](int i, int pos0) -> uint32_t {
+          if (!k.mask) {
+            const int cnt = max(min(L + i + 1 - pos0, 32), 0);
+            return (uint32_t)((1ull << cnt) - 1);
+          }
+          const uint64_t* const words =
+              k.mask + ((int64_t)r * k.a.blk + max(i, 0)) * k.mask_words;
+          const int j0 = pos0 - L, before = max(-j0, 0), j = max(j0, 0), sh = j & 63;
+          const int w0 = min(j >> 6, k.mask_words - 1), w1 = min(w0 + 1, k.mask_words - 1);
+          uint64_t bits = words[w0] >> sh;
+          bits |= w1 > w0 && sh > 0 ? words[w1] << (64 - sh) : 0;
+          return (uint32_t)((i < 0 ? 0 : bits) << before | ((1ull << before) - 1));
+        };
+
+        // ---- one tile; TAIL: it reaches behind the line's first L positions
+        int st = 0;
+        bool odd = false;
+        auto tile = [&](int t, auto is_tail) {
+          constexpr bool TAIL = decltype(is_tail)::value;
+          char* const kt = stage0 + st * Sh::kStage;
+          char* const vt = kt + TILE;
+          const int later = min(NST - 1, t1 - 1 - t);  // whole tiles in flight behind this one
+          const bool refill = t + NST < t1;
+          wait_vm<NLD>(1 + 2 * later);
+
+          // ---- S^T = K Q^T
+          f32x4 s[MT][2];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4{0, 0, 0, 0};
+          const int k_at = n16 * RB + ((g ^ swz_k<RB>(n16)) << 4);
+          u32x4 raw[2];
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            x8 kf[2];
+            if constexpr (!F8) {
+#pragma unroll
+              for (int sub = 0; sub < 2; ++sub)
+                kf[sub] = lds_read<x8>(kt + (k_at ^ (ks << 6)) + sub * 16 * RB);
+            } else {
+#pragma unroll
+              for (int sub = 0; sub < 2; ++sub) {
+                if (ks % 2 == 0) raw[sub] = lds_read<u32x4>(kt + (k_at ^ (ks / 2 << 6)) + sub * 16 * RB);
+                kf[sub] = widen<T>(raw[sub][2 * (ks & 1)], raw[sub][2 * (ks & 1) + 1]);
+              }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              x8 q;
+              if constexpr (kQLds)
+                q = lds_read<x8>(q_lds + ((mt * KS + ks) * 64 + lane) * 16);
+              else
+                q = qf[mt][ks];
+              s[mt][0] = E::mfma(kf[0], q, s[mt][0]);
+              s[mt][1] = E::mfma(kf[1], q, s[mt][1]);
+            }
+          }
+          wait_lds();  // K is read: its place is free
+          if (refill) issue(t + NST, kbase, kt, std::false_type{});
+
+          // ---- weights
+          const int pos0 = t * kAttendTile;
+          x8 p_hi[MT], p_lo[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float xs[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xs[e] = s[mt][e >> 2][e & 3] * sc;
+            if constexpr (TAIL) {
+              const uint32_t see = visible(irow[mt], pos0) >> (4 * g);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                xs[e] = (see >> (16 * (e >> 2) + (e & 3))) & 1u ? xs[e] : -INFINITY;
+            }
+            float mx = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])),
+                             fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
+            if (__any(mx > m_run[mt] + 8.0f)) {
+              mx = fmaxf(group_max(mx), m_run[mt]);
+              const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
+              m_run[mt] = mx;
+              l_run[mt] *= f;
+#pragma unroll
+              for (int d = 0; d < NT; ++d) acc[mt][d] *= f;
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p = __builtin_amdgcn_exp2f(xs[e] - m_run[mt]);
+              sum += p;
+              const T hi = (T)p;
+              p_hi[mt][e] = hi;
+              p_lo[mt][e] = (T)(p - (float)hi);
+            }
+            l_run[mt] += sum;
+          }
+
+          // ---- O^T += V^T P^T
+          wait_vm<NLD>(2 * later + (refill ? 1 : 0));
+          if constexpr (TAIL) {
+            // Rows behind the job's last position hold a copy of it: zero them.  Block rows may hold
+            // NaN or infinities that some of the queries do not see, and 0 * inf is not 0: such values
+            // (rare) become 0 here and are added at the end, to the rows that see them.
+#pragma unroll
+            for (int i = 0; i < NLD; ++i) {
+              char* const at = vt + i * 1024 + lane * 16;
+              const int pos = pos0 + i * RPI + lane / CPR;
+              u32x4 v = {0, 0, 0, 0};
+              if (pos < keys) v = lds_read<u32x4>(at);
+              if (pos >= L) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t keep = finite_mask<T, F8>(v[e]);
+                  odd |= keep != ~0u;
+                  v[e] &= keep;
+                }
+                *reinterpret_cast<u32x4*>(at) = v;
+              }
+            }
+            wait_lds();
+          }
+#pragma unroll
+          for (int d = 0; d < NT; ++d) {
+            x8 vf;  // the lane's 8 positions of dims 16 d .. 16 d + 15
+            if constexpr (!F8) {
+              // group g, lane i of it: address of position 4 g + i / 4, dims 4 (i % 4) of the tile
+              const int row = 4 * g + (n16 >> 2);
+              const int v_at = row * RB + ((((n16 & 3) >> 1) ^ swz_v<RB, F8>(row)) << 4) + (n16 & 1) * 8;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const x4 v4 = lds_tr16<T>(vt + (v_at ^ (d << 5)) + half * 16 * RB);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) vf[4 * half + e] = v4[e];
+              }
+            } else {
+              // lane i: position j = i / 2 of the group's eight, 8 of the 16 dims
+              const int j = n16 >> 1;
+              const int row = 16 * (j >> 2) + 4 * g + (j & 3);
+              const int v_at = row * RB + (swz_v<RB, F8>(row) << 4) + (n16 & 1) * 8;
+              const i32x2 v = lds_tr8(vt + (v_at ^ (d << 4)));
+              vf = widen<T>((uint32_t)v[0], (uint32_t)v[1]);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[mt][d] = E::mfma(vf, p_hi[mt], acc[mt][d]);
+              acc[mt][d] = E::mfma(vf, p_lo[mt], acc[mt][d]);
+            }
+          }
+          wait_lds();  // V is read: its place is free
+          if (refill) issue(t + NST, vbase, vt, std::true_type{});
+          st = st + 1 == NST ? 0 : st + 1;
+        };
+        int t = t0;
+        for (const int tm = min(t1, L / kAttendTile); t < tm; ++t) tile(t, std::false_type{});
+        for (; t < t1; ++t) tile(t, std::true_type{});
+
+        // ---- join the waves
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float l = group_sum(l_run[mt]);
+          if (g == 0) {
+            s_m[wave][mt * 16 + n16] = m_run[mt];
+            s_l[wave][mt * 16 + n16] = l;
+          }
+        }
+        const bool any_odd = __syncthreads_or(odd);
+        const bool whole = off == 0 && ns == steps;
+        const int slot = (int)(2 * w + (first_segment ? 0 : 1));
+        const float vscale = F8 && c.v_scale ? c.v_scale[h] : 1.0f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float mx = kNegBig;
+#pragma unroll
+          for (int u = 0; u < kAttendWaves; ++u) mx = fmaxf(mx, s_m[u][mt * 16 + n16]);
+          const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
+          char* const mine = my_ring + n16 * (DP + 4) * 4 + 4 * g * 4;
+#pragma unroll
+          for (int d = 0; d < NT; ++d)
+            *reinterpret_cast<f32x4*>(mine + 16 * d * 4) = acc[mt][d] * f;
+          __syncthreads();
+          for (int it = tid; it < 16 * DP / 4; it += kAttendThreads) {
+            const int row = it / (DP / 4), d = (it - row * (DP / 4)) * 4;
+            const int m = mt0 * ROWS + mt * 16 + row;
+            const int i = m / G;
+            f32x4 y = {0, 0, 0, 0};
+            float rm = kNegBig, rl = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kAttendWaves; ++u) {
+              y += *reinterpret_cast<const f32x4*>(ring + u * Sh::kRing + row * (DP + 4) * 4 + d * 4);
+              rm = fmaxf(rm, s_m[u][mt * 16 + row]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAttendWaves; ++u)
+              rl += s_l[u][mt * 16 + row] * __builtin_amdgcn_exp2f(s_m[u][mt * 16 + row] - rm);
+            if (any_odd) {  // NaN and infinities of the block rows that this row sees
+              const int j1 = min(tile1 * kAttendTile, keys) - L;
+              for (int j = max(tile0 * kAttendTile - L, 0); j < j1; ++j) {
+                const bool on = (visible(i < n ? i : -1, L + j) & 1u) != 0;
+                const int s = (L + j) / ps;
+                const int page = (uint32_t)tab[s] < (uint32_t)c.num_pages ? tab[s] : 0;
+                const char* v = static_cast<const char*>(c.v) + head_off + min(d, dim - 4) * ES +
+                                ((int64_t)page * c.page_stride + (int64_t)(L + j - s * ps) * c.row_stride) * ES;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float z;
+                  if constexpr (F8)
+                    z = (float)E::template from_f8<false>(reinterpret_cast<const uint8_t*>(v)[e])[0];
+                  else
+                    z = (float)reinterpret_cast<const T*>(v)[e];
+                  y[e] += on && !__builtin_isfinite(z) ? z : 0.0f;
+                }
+              }
+            }
+            if (!whole) {
+              if (i < n) {
+                *reinterpret_cast<f32x4*>(k.o + ((int64_t)slot * ROWS + mt * 16 + row) * DP + d) = y;
+                if (d == 0) k.ml[(int64_t)slot * ROWS + mt * 16 + row] = make_float2(rm, rl);
+              }
+            } else if (i < n && d < dim) {
+              x4 z;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] / rl * vscale);
+              T* out = static_cast<T*>(a.out) + ((int64_t)r * a.blk + i) * a.out_stride +
+                       (int64_t)(h * G + (m - i * G)) * dim + d;
+              *reinterpret_cast<x4*>(out) = z;
+            }
+          }
+          __syncthreads();
+        }
+        if (!whole && off == 0 && tid == 0) {  // the job starts here and ends in a later share
+          const int64_t last = x + steps - 1;  // its last step
+          const int64_t wl = ((last + 1) * shares - 1) / all;
+          AttendInfo& o = k.info[w];
+          o.r = r;
+          o.h = h;
+          o.mt = mt0;
+          o.slot = slot;
+          o.parts = (int)(wl - w) + 1;
+        }
+        x += ns;
+        off = 0;
+        first_segment = false;
+      }
+    }
+    if (x >= x_end) return;
+  }
+}
+
+template <typename T, bool F8, int DP, int MT>
+hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
+  typedef Shape<(F8 ? 1 : 2) * DP, MT, DP> Sh;
+  constexpr int shm = Sh::kLds;
+  // more dynamic LDS than the default limit, once per device
+  static unsigned long long done = 0;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_RELAXED) >> dev & 1)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<T, F8, DP, MT>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, shm);
+    if (e != hipSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
+  }
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((unsigned)k.wgs), dim3(kAttendThreads), shm,
+                 stream, k);
+  return hipGetLastError();
+}
+
+template <typename T, bool F8>
+hipError_t launch_typed(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream) {
+  if (dp == 64) {
+    switch (mt) {
+      case 1: return launch_one<T, F8, 64, 1>(k, stream);
+      case 2: return launch_one<T, F8, 64, 2>(k, stream);
+      case 4: return launch_one<T, F8, 64, 4>(k, stream);
+      case 6: return launch_one<T, F8, 64, 6>(k, stream);
+    }
+  } else if (dp == 128) {
+    switch (mt) {
+      case 1: return launch_one<T, F8, 128, 1>(k, stream);
+      case 2: return launch_one<T, F8, 128, 2>(k, stream);
+      case 3: return launch_one<T, F8, 128, 3>(k, stream);
+      case 4: return launch_one<T, F8, 128, 4>(k, stream);
+      case 5: return launch_one<T, F8, 128, 5>(k, stream);
+    }
+  } else if (dp == 256) {
+    switch (mt) {
+      case 1: return launch_one<T, F8, 256, 1>(k, stream);
+      case 2: return launch_one<T, F8, 256, 2>(k, stream);
+    }
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace attend
+}  // namespace psispec

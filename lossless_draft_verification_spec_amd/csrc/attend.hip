@@ -1,42 +1,88 @@
-// attend.hip -- attention of a block's new tokens over the paged cache.
-//
-//   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale q . k_t) over the positions t that the row sees
-#include "paged.h"
+// attend.hip -- attention over the paged cache: the shapes of its launches, the masks of a tree, and
+// the join of the parts that the attention kernel's shares leave.
+#include "attend.h"
 
 namespace psispec {
 namespace {
 
-constexpr int kAtThreads = 256;
+using attend::f32x4;
 
-template <typename T> __device__ inline float cache_f32(const void* p, int64_t i) {
-  return (float)static_cast<const T*>(p)[i];
-}
-struct f8_t {};
-template <> __device__ inline float cache_f32<f8_t>(const void* p, int64_t i) {
-  return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(p)[i], 0);
+// Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
+// the instantiated sizes allow (each group reads every key and value again), then the smallest
+// size that holds a group: rows that pad a tile cost matrix work.
+AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int dim) {
+  AttendPlan p{};
+  p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+  static const int k64[] = {1, 2, 4, 6}, k128[] = {1, 2, 3, 4, 5}, k256[] = {1, 2};
+  const int* sizes = p.dp == 64 ? k64 : p.dp == 128 ? k128 : k256;
+  const int ns = p.dp == 64 ? 4 : p.dp == 128 ? 5 : 2;
+  const int64_t rows = (int64_t)blk * (heads_q / heads_kv);
+  const int most = sizes[ns - 1] * 16;
+  p.nmt = (int)((rows + most - 1) / most);
+  const int tiles = (int)(((rows + p.nmt - 1) / p.nmt + 15) / 16);
+  for (int i = ns - 1; i >= 0; --i)
+    if (sizes[i] >= tiles) p.mt = sizes[i];
+  p.nmt = (int)((rows + p.mt * 16 - 1) / (p.mt * 16));
+  p.wgs = 2 * kAttendCUs;  // the kernels that run one workgroup per CU use half of them
+  p.mask_words = (blk + 63) / 64;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = (off + n + 255) / 256 * 256;
+    return at;
+  };
+  take(sizeof(AttendInfo) * p.wgs);
+  p.off_ml = take(sizeof(float2) * 2 * p.wgs * p.mt * 16);
+  p.off_o = take(sizeof(float) * 2 * p.wgs * p.mt * 16 * (size_t)p.dp);
+  p.off_mask = take(sizeof(uint64_t) * (size_t)batch * blk * p.mask_words);
+  p.total = off;
+  return p;
 }
 
-// One workgroup per (line, block row, query head); each wave takes every fourth position, its lanes
-// the dimensions lane, lane + 64, ...
-template <typename T, typename C>
-__global__ __launch_bounds__(kAtThreads) void k_attend(AttendArgs a) {
+// A tree's masks: row j's word w holds bit i for every ancestor-or-self 64 w + i of row j.
+__global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask, int words) {
+  __shared__ int s_par[kMaxAttendBlock];
+  const int r = blockIdx.x;
+  for (int j = threadIdx.x; j < a.blk; j += 256) s_par[j] = a.parent[(int64_t)r * a.blk + j];
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.blk; j += 256) {
+    uint64_t* out = mask + ((int64_t)r * a.blk + j) * words;
+    int i = j;
+    for (int w = words - 1; w >= 0; --w) {  // parents come before their children
+      uint64_t bits = 0;
+      while (i >= 64 * w) {
+        bits |= 1ull << (i & 63);
+        const int p = s_par[i];
+        i = p < i ? p : -1;  // a bad parent ends the path
+      }
+      out[w] = bits;
+    }
+  }
+}
+
+// Blocks [0, wgs * groups): four rows of the job that starts in share w and ends in a later one; the
+// four waves take every fourth part, a lane the same 16 bytes of each, and are added in order.
+// Blocks behind them: the status of one line each.
+constexpr int kJoinRows = 4;
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int rows, int groups, int f8) {
+  constexpr int NV = kJoinRows * DP / 4 / 64;  // 16-byte pieces per lane
+  __shared__ f32x4 s_o[4][kJoinRows * DP / 4];
+  __shared__ float s_m[4][kJoinRows], s_l[4][kJoinRows];
+  const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
-  const int hq = blockIdx.x % a.heads_q;
-  const int64_t row = blockIdx.x / a.heads_q;
-  const int r = (int)(row / a.blk), i = (int)(row - (int64_t)r * a.blk);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __shared__ uint32_t s_seen[kMaxAttendBlock / 32];
-  __shared__ float s_m[4], s_l[4], s_o[4][kMaxHeadDim];
-  int L, n;
-  const bool ok = line_rows(a.len, a.n_new, r, a.blk, c.slots, c.page_size, &L, &n);
-  const int32_t* tab = c.table + (int64_t)r * c.table_stride;
-  if (a.status && i == 0 && hq == 0) {
-    bool bad = !ok, badp = false;
-    if (ok) {
-      for (int s = threadIdx.x; (int64_t)s * c.page_size < (int64_t)L + n; s += kAtThreads)
-        bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
+  if ((int)blockIdx.x >= k.wgs * groups) {
+    const int r = blockIdx.x - k.wgs * groups;
+    int L, n;
+    bool bad = !line_rows(a.len, a.n_new, r, a.blk, c.slots, c.page_size, &L, &n), badp = false;
+    if (!bad && n > 0) {
+      const int32_t* tab = c.table + (int64_t)r * c.table_stride;
+      const int last = (int)(((int64_t)L + n - 1) / c.page_size);
+      for (int s = threadIdx.x; s <= last; s += 256) bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
       if (a.parent)
-        for (int j = threadIdx.x; j < n; j += kAtThreads) {
+        for (int j = threadIdx.x; j < n; j += 256) {
           const int p = a.parent[(int64_t)r * a.blk + j];
           badp |= p < -1 || p >= j;
         }
@@ -44,92 +90,148 @@ __global__ __launch_bounds__(kAtThreads) void k_attend(AttendArgs a) {
     const bool b0 = __syncthreads_or(bad), b1 = __syncthreads_or(badp);
     if (threadIdx.x == 0)
       a.status[r] = (b0 ? PSISPEC_ST_BAD_PAGE : 0) | (b1 ? PSISPEC_ST_BAD_PARENT : 0);
+    return;
   }
-  if (!ok || i >= n) return;
-  for (int w = threadIdx.x; w < kMaxAttendBlock / 32; w += kAtThreads)
-    s_seen[w] = a.parent ? 0u : w < (i >> 5) ? ~0u : w == (i >> 5) ? (2u << (i & 31)) - 1u : 0u;
-  __syncthreads();
-  if (a.parent && threadIdx.x == 0) {
-    int j = i;
-    while (j >= 0) {
-      s_seen[j >> 5] |= 1u << (j & 31);
-      const int p = a.parent[(int64_t)r * a.blk + j];
-      j = p < j ? p : -1;
+  const int w = blockIdx.x / groups;
+  const int row0 = (blockIdx.x - w * groups) * kJoinRows;
+  const AttendInfo in = k.info[w];
+  if (in.parts == 0) return;
+  int L, n;
+  line_rows(a.len, a.n_new, in.r, a.blk, c.slots, c.page_size, &L, &n);
+  const int live = min(n * k.G - in.mt * rows, rows) - row0;  // live rows from row0 on
+  if (live <= 0) return;
+
+  f32x4 o[NV];
+  float m[NV], l[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    o[v] = f32x4{0, 0, 0, 0};
+    m[v] = kNegBig;
+    l[v] = 0.0f;
+  }
+  constexpr int kAhead = 4;  // parts loaded together
+  for (int p0 = wave; p0 < in.parts; p0 += 4 * kAhead) {
+    f32x4 y[kAhead][NV];
+    float2 ml[kAhead][NV];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int p = p0 + 4 * u;
+      if (p < in.parts) {
+        const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int e = (v * 64 + lane) * 4, row = e / DP;
+          if (row < live) {
+            ml[u][v] = k.ml[slot * rows + row0 + row];
+            y[u][v] = *reinterpret_cast<const f32x4*>(k.o + (slot * rows + row0) * DP + e);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (p0 + 4 * u < in.parts) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if ((v * 64 + lane) * 4 / DP < live) {
+            const float mx = fmaxf(m[v], ml[u][v].x);
+            const float f0 = __builtin_amdgcn_exp2f(m[v] - mx);
+            const float f1 = __builtin_amdgcn_exp2f(ml[u][v].x - mx);
+            o[v] = o[v] * f0 + y[u][v] * f1;
+            l[v] = l[v] * f0 + ml[u][v].y * f1;
+            m[v] = mx;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = v * 64 + lane;
+    s_o[wave][e] = o[v];
+    if (e * 4 % DP == 0) {
+      s_m[wave][e * 4 / DP] = m[v];
+      s_l[wave][e * 4 / DP] = l[v];
     }
   }
   __syncthreads();
-  const int h = hq / (a.heads_q / c.heads);
-  const T* q = static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)hq * c.dim;
-  float qf[4], o[4] = {};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) qf[k] = lane + 64 * k < c.dim ? (float)q[lane + 64 * k] : 0.0f;
-  const float ks = c.k_scale ? c.k_scale[h] : 1.0f, vs = c.v_scale ? c.v_scale[h] : 1.0f;
-  float m = -INFINITY, l = 0.0f;
-  for (int t = wave; t < L + i + 1; t += 4) {
-    if (t >= L && !((s_seen[(t - L) >> 5] >> ((t - L) & 31)) & 1u)) continue;
-    const int slot = t / c.page_size;
-    const int page = tab[slot];
-    if ((uint32_t)page >= (uint32_t)c.num_pages) continue;
-    const int64_t at = (int64_t)page * c.page_stride + (int64_t)(t - slot * c.page_size) * c.row_stride +
-                       (int64_t)h * c.head_stride;
-    float s = 0.0f, v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool on = lane + 64 * k < c.dim;
-      s += on ? qf[k] * cache_f32<C>(c.k, at + lane + 64 * k) : 0.0f;
-      v[k] = on ? cache_f32<C>(c.v, at + lane + 64 * k) : 0.0f;
+  for (int it = threadIdx.x; it < kJoinRows * DP / 4; it += 256) {
+    const int row = it * 4 / DP, d = it * 4 - row * DP;
+    if (row >= live || d >= c.dim) continue;
+    float mx = kNegBig, sum = 0.0f;
+    for (int u = 0; u < 4; ++u) mx = fmaxf(mx, s_m[u][row]);
+    f32x4 y = {0, 0, 0, 0};
+    for (int u = 0; u < 4; ++u) {
+      const float f = __builtin_amdgcn_exp2f(s_m[u][row] - mx);
+      y += s_o[u][it] * f;
+      sum += s_l[u][row] * f;
     }
+    const float vs = f8 && c.v_scale ? c.v_scale[in.h] : 1.0f;
+    const int q = in.mt * rows + row0 + row, i = q / k.G;
+    typename attend::Elem<T>::x4 z;
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) s += __shfl_xor(s, x, 64);
-    s *= a.scale * ks;
-    const float mn = fmaxf(m, s);
-    const float f = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = o[k] * f + p * v[k];
-    m = mn;
+    for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] / sum * vs);
+    T* out = static_cast<T*>(a.out) + ((int64_t)in.r * a.blk + i) * a.out_stride +
+             (int64_t)(in.h * k.G + (q - i * k.G)) * c.dim + d;
+    *reinterpret_cast<typename attend::Elem<T>::x4*>(out) = z;
   }
-  if (lane == 0) {
-    s_m[wave] = m;
-    s_l[wave] = l;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) s_o[wave][lane + 64 * k] = o[k];
-  __syncthreads();
-  float mx = s_m[0], sum = 0.0f, f[4];
-  for (int w = 1; w < 4; ++w) mx = fmaxf(mx, s_m[w]);
-  for (int w = 0; w < 4; ++w) {
-    f[w] = s_m[w] == -INFINITY ? 0.0f : expf(s_m[w] - mx);
-    sum += f[w] * s_l[w];
-  }
-  T* out = static_cast<T*>(a.out) + row * a.out_stride + (int64_t)hq * c.dim;
-  if ((int)threadIdx.x < c.dim) {
-    float y = 0.0f;
-    for (int w = 0; w < 4; ++w)
-      if (s_l[w] != 0.0f) y += f[w] * s_o[w][threadIdx.x];
-    out[threadIdx.x] = (T)(y / sum * vs);
-  }
+}
+
+template <typename T>
+hipError_t launch_join(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
+  const int rows = p.mt * 16, groups = rows / kJoinRows;
+  const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
+  const dim3 grid((unsigned)(k.wgs * groups + (k.a.status ? k.a.batch : 0))), block(256);
+  if (p.dp == 64)
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 64>), grid, block, 0, stream, k, rows, groups, f8);
+  else if (p.dp == 128)
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 128>), grid, block, 0, stream, k, rows, groups, f8);
+  else
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 256>), grid, block, 0, stream, k, rows, groups, f8);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t attend_workspace_bytes(int batch, int blk, int heads_q, int heads_kv, int dim) {
+  return make_attend_plan(batch, blk, heads_q, heads_kv, dim).total;
+}
 
-hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void*, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.batch * a.blk * a.heads_q)), block(kAtThreads);
+hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspace,
+                         hipStream_t stream) {
+  const AttendPlan p = make_attend_plan(a.batch, a.blk, a.heads_q, a.c.heads, a.c.dim);
   const bool f8 = a.c.dtype == PSISPEC_F8E4M3;
-  if (dtype == PSISPEC_BF16) {
-    if (f8)
-      PSISPEC_LAUNCH("attend", (k_attend<__bf16, f8_t>), grid, block, 0, stream, a);
-    else
-      PSISPEC_LAUNCH("attend", (k_attend<__bf16, __bf16>), grid, block, 0, stream, a);
-  } else {
-    if (f8)
-      PSISPEC_LAUNCH("attend", (k_attend<_Float16, f8_t>), grid, block, 0, stream, a);
-    else
-      PSISPEC_LAUNCH("attend", (k_attend<_Float16, _Float16>), grid, block, 0, stream, a);
+  char* ws = static_cast<char*>(workspace);
+  AttendKernelArgs k{};
+  k.a = a;
+  k.G = a.heads_q / a.c.heads;
+  k.nmt = p.nmt;
+  k.mask_words = p.mask_words;
+  const int rb = p.dp * (f8 ? 1 : 2);
+  k.wgs = attend_two(rb, p.dp, p.mt) ? 2 * kAttendCUs : kAttendCUs;
+  k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
+  const int rows_per_load = 1024 / rb;
+  k.row_groups = a.c.page_size % rows_per_load == 0 &&
+                 a.c.row_stride * (f8 ? 1 : 2) * rows_per_load < (int64_t(1) << 31);
+  k.c = a.scale * 1.4426950408889634f;
+  k.info = reinterpret_cast<AttendInfo*>(ws);
+  k.ml = reinterpret_cast<float2*>(ws + p.off_ml);
+  k.o = reinterpret_cast<float*>(ws + p.off_o);
+  if (a.parent) {
+    uint64_t* mask = reinterpret_cast<uint64_t*>(ws + p.off_mask);
+    k.mask = mask;
+    PSISPEC_LAUNCH("tree_mask", k_tree_mask, dim3((unsigned)a.batch), dim3(256), 0, stream, a, mask,
+                   p.mask_words);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  hipError_t e;
+  if (dtype == PSISPEC_BF16)
+    e = f8 ? launch_attend_bf16_f8(k, p.dp, p.mt, stream) : launch_attend_bf16(k, p.dp, p.mt, stream);
+  else
+    e = f8 ? launch_attend_f16_f8(k, p.dp, p.mt, stream) : launch_attend_f16(k, p.dp, p.mt, stream);
+  if (e != hipSuccess) return e;
+  return dtype == PSISPEC_BF16 ? launch_join<__bf16>(k, p, stream) : launch_join<_Float16>(k, p, stream);
 }
 
 }  // namespace psispec
