@@ -59,7 +59,8 @@ struct AttendKernelArgs {
   AttendArgs a;
   int G, nmt, mask_words, wgs;
   uint32_t ps_magic;         // ceil(2^32 / page_size)
-  int row_groups;            // the rows of one load instruction lie in one page, within 2^31 bytes
+  int row_groups;            // the rows of one load instruction lie in one page, strides below 2^31
+  uint32_t page_bytes, row_bytes;  // the strides in bytes when row_groups
   float c;                   // scale log2(e)
   AttendInfo* info;          // [wgs]
   float2* ml;                // [2 wgs][16 MT]
@@ -178,25 +179,27 @@ template <typename T, bool F8> __device__ inline uint32_t finite_mask(uint32_t w
   return m;
 }
 
-// Wait until at most n (wave-uniform) loads are outstanding; a smaller count waits longer.
-template <int UNIT> __device__ inline void wait_vm(int units) {
-  // units of UNIT loads; counts above 63 do not exist
-  if (units <= 0)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  else if (units == 1)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(UNIT) : "memory");
-  else if (units == 2)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * UNIT) : "memory");
-  else if (units == 3)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * UNIT > 63 ? 63 : 3 * UNIT) : "memory");
-  else if (units == 4)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * UNIT > 63 ? 63 : 4 * UNIT) : "memory");
-  else if (units == 5)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * UNIT > 63 ? 63 : 5 * UNIT) : "memory");
-  else if (units == 6)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * UNIT > 63 ? 63 : 6 * UNIT) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(7 * UNIT > 63 ? 63 : 7 * UNIT) : "memory");
+// Wait until at most units * UNIT loads are outstanding (units wave-uniform, at most MAX).
+template <int N> __device__ inline void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N > 63 ? 63 : N) : "memory");
+}
+template <int UNIT, int MAX> __device__ inline void wait_vm(int units) {
+  if constexpr (MAX == 0) {
+    wait_loads<0>();
+  } else {
+    if (units >= MAX)
+      wait_loads<MAX * UNIT>();
+    else
+      wait_vm<UNIT, MAX - 1>(units);
+  }
+}
+// Wait for the results of the matrix instructions before this point.  The hardware does not hold a
+// reader back, and the waits that the compiler puts in do not always reach across the branch that
+// follows here: a reader on its taken side got a sum without its last product.
+__device__ inline void wait_matrix() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 __device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
@@ -375,41 +378,48 @@ void k_attend(AttendKernelArgs k) {
         const int64_t head_off = (int64_t)h * c.head_stride * ES;
         const char* const kbase = static_cast<const char*>(c.k) + head_off;
         const char* const vbase = static_cast<const char*>(c.v) + head_off;
-        int tab_chunk = -1, tab_now = 0, tab_next = 0;
+        int tab_chunk = -2, tab_now = 0, tab_next = 0, chunk_end = 0;
+        const uint32_t lane_ofs = (uint32_t)(lane / CPR) * k.row_bytes;
         const int last_slot = (keys - 1) / ps;
-        auto fetch_tab = [&](int chunk) {
-          const int s = chunk * 64 + lane;
-          int p = tab[s < last_slot ? s : last_slot];
-          return (uint32_t)p < (uint32_t)c.num_pages ? p : 0;  // a bad id stays in bounds
-        };
+        auto fetch_tab = [&](int chunk) { return tab[min(chunk * 64 + lane, last_slot)]; };
         // tile t into `to`: row i * RPI + lane / CPR of each load instruction; rows behind the job's
         // last position are read as the last
         auto issue = [&](int t, const char* from, char* to, auto is_v) {
-          const int chunk = t * kAttendTile / (64 * ps);  // tiles never straddle 64 pages
-          if (chunk != tab_chunk) {
-            tab_now = chunk == tab_chunk + 1 && tab_chunk >= 0 ? tab_next : fetch_tab(chunk);
+          const int tile_pos = t * kAttendTile;
+          if (tile_pos >= chunk_end) {  // tiles never straddle 64 pages
+            const int chunk = (uint32_t)tile_pos / (64u * ps);
+            const int raw = chunk == tab_chunk + 1 ? tab_next : fetch_tab(chunk);
+            tab_now = (uint32_t)raw < (uint32_t)c.num_pages ? raw : 0;  // a bad id stays in bounds
             tab_chunk = chunk;
+            chunk_end = (chunk + 1) * 64 * ps;
             tab_next = fetch_tab(chunk + 1);
           }
-          const int rel0 = t * kAttendTile - chunk * 64 * ps;
-          const int lim = keys - 1 - chunk * 64 * ps;
+          const int rel0 = tile_pos + 64 * ps - chunk_end;
+          const int lim = keys - 1 + 64 * ps - chunk_end;
           const int lane_row = lane / CPR;
           const int swz = is_v() ? swz_v<RB, F8>(lane_row) : swz_k<RB>(lane_row);
           const int lane_chunk = (lane % CPR) ^ swz;
-          if (k.row_groups) {  // the rows of one instruction lie in one page
-#pragma unroll
-            for (int i = 0; i < NLD; ++i) {
+          if (k.row_groups) {  // the rows of one instruction lie in one page; 32-bit strides
+            auto load = [&](int i, bool all) {
               const int rel = min(rel0 + i * RPI, lim);
               const int idx = ps == 1 ? rel : (int)__umulhi((uint32_t)rel, k.ps_magic);
-              const int page = __builtin_amdgcn_readlane(tab_now, idx);
-              const char* const at =
-                  from + ((int64_t)page * c.page_stride + (int64_t)(rel - idx * ps) * c.row_stride) * ES;
+              const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(tab_now, idx);
+              const char* const at = from + (uint64_t)page * k.page_bytes +
+                                     (uint32_t)(rel - idx * ps) * k.row_bytes;
               const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
-              const uint32_t lofs =
-                  (uint32_t)(min(lane_row, lim - rel) * (int)c.row_stride * ES + (ch << 4));
-              if (ch < chunks)
-                __builtin_amdgcn_global_load_lds((global_void*)(at + lofs), (lds_void*)(to + i * 1024), 16,
-                                                 0, 0);
+              // lane_row * row_bytes unless rows behind the last are asked for
+              const uint32_t row_ofs =
+                  lim - rel >= RPI - 1 ? lane_ofs : (uint32_t)min(lane_row, lim - rel) * k.row_bytes;
+              if (all || ch < chunks)
+                __builtin_amdgcn_global_load_lds((global_void*)(at + (row_ofs + (ch << 4))),
+                                                 (lds_void*)(to + i * 1024), 16, 0, 0);
+            };
+            if (dim == DP) {
+#pragma unroll
+              for (int i = 0; i < NLD; ++i) load(i, true);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < NLD; ++i) load(i, false);
             }
           } else {
 #pragma unroll 1
@@ -453,7 +463,16 @@ void k_attend(AttendKernelArgs k) {
           }
         }
         const float sc = k.c * (F8 && c.k_scale ? c.k_scale[h] : 1.0f);
-        if constexpr (kQLds) __syncthreads();
+        if constexpr (kQLds) {
+          __syncthreads();
+        } else {
+          // The queries arrive before the first tile is asked for: a wait for them inside the loop
+          // would also wait for the tiles in flight.
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(qf[mt][s]));
+        }
 
         char* const stage0 = my_ring;
         if (dim != DP) {  // the chunks behind the head's last are never loaded
@@ -501,9 +520,10 @@ void k_attend(AttendKernelArgs k) {
           constexpr bool TAIL = decltype(is_tail)::value;
           char* const kt = stage0 + st * Sh::kStage;
           char* const vt = kt + TILE;
-          const int later = min(NST - 1, t1 - 1 - t);  // whole tiles in flight behind this one
+          // whole tiles in flight behind this one
+          const int later = NST == 1 ? 0 : min(NST - 1, t1 - 1 - t);
           const bool refill = t + NST < t1;
-          wait_vm<NLD>(1 + 2 * later);
+          wait_vm<NLD, 2 * NST - 1>(1 + 2 * later);
 
           // ---- S^T = K Q^T
           f32x4 s[MT][2];
@@ -537,6 +557,7 @@ void k_attend(AttendKernelArgs k) {
             }
           }
           wait_lds();  // K is read: its place is free
+          wait_matrix();
           if (refill) issue(t + NST, kbase, kt, std::false_type{});
 
           // ---- weights
@@ -576,7 +597,10 @@ void k_attend(AttendKernelArgs k) {
           }
 
           // ---- O^T += V^T P^T
-          wait_vm<NLD>(2 * later + (refill ? 1 : 0));
+          if (refill)
+            wait_loads<(2 * NST - 1) * NLD>();
+          else
+            wait_vm<NLD, 2 * NST - 2>(2 * later);
           if constexpr (TAIL) {
             // Rows behind the job's last position hold a copy of it: zero them.  Block rows may hold
             // NaN or infinities that some of the queries do not see, and 0 * inf is not 0: such values
@@ -627,6 +651,7 @@ void k_attend(AttendKernelArgs k) {
             }
           }
           wait_lds();  // V is read: its place is free
+          wait_matrix();
           if (refill) issue(t + NST, vbase, vt, std::true_type{});
           st = st + 1 == NST ? 0 : st + 1;
         };

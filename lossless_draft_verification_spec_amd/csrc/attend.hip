@@ -210,9 +210,14 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   const int rb = p.dp * (f8 ? 1 : 2);
   k.wgs = attend_two(rb, p.dp, p.mt) ? 2 * kAttendCUs : kAttendCUs;
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
-  const int rows_per_load = 1024 / rb;
-  k.row_groups = a.c.page_size % rows_per_load == 0 &&
-                 a.c.row_stride * (f8 ? 1 : 2) * rows_per_load < (int64_t(1) << 31);
+  const int es = f8 ? 1 : 2;
+  const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
+  k.row_groups = a.c.page_size % (1024 / rb) == 0 && page_bytes < (int64_t(1) << 31) &&
+                 row_bytes * (a.c.page_size + 16) < (int64_t(1) << 31);
+  if (k.row_groups) {
+    k.page_bytes = (uint32_t)page_bytes;
+    k.row_bytes = (uint32_t)row_bytes;
+  }
   k.c = a.scale * 1.4426950408889634f;
   k.info = reinterpret_cast<AttendInfo*>(ws);
   k.ml = reinterpret_cast<float2*>(ws + p.off_ml);
