@@ -4,8 +4,11 @@
 //
 // One key/value head serves G query heads, so its query rows (block row i, head g) -> m = i G + g share
 // every key and value read: they form the 16-row tiles of the matrix products.  A workgroup's job is
-// (line, key/value head, group of up to 16 MT rows); its four waves take disjoint runs of 32-position
-// tiles, each with softmax statistics of its own, and are joined at the end.
+// (line, key/value head, group of up to 16 MT rows), and its four waves take disjoint runs of
+// 32-position tiles, each with softmax statistics of its own, that are joined at the end; or, with few
+// rows and heads in fours, a job is four heads and each wave has one of them to itself: the waves read
+// neighbouring heads of the same positions at about the same time (one after the other, the 128- and
+// 256-byte pieces of a position cost HBM about a tenth of its rate), and no join is needed.
 //
 // Products (v_mfma_f32_16x16x32, 32-bit sums).  Transposed, so that a lane owns one query row:
 //   S^T = K Q^T   A = 16 positions x 32 dims of K, B = Q (in registers for the whole job)
@@ -24,9 +27,9 @@
 // permuted by its position (on the load's source side) so that the reads of 16 rows at one chunk
 // meet no LDS bank twice.  Page ids come 64 at a time, one in each lane.
 //
-// Work.  All jobs of the call laid end to end, in steps of 128 positions, are cut into one equal
-// share per workgroup, however uneven the lines are; a job cut by a border leaves its parts (maximum,
-// sum, unnormalised output in 32 bits) in the workspace and k_attend_join adds them in order.
+// Work.  All jobs of the call laid end to end, in steps of 128 positions, are cut into one share per
+// workgroup, however uneven the lines are; a job cut by a border leaves its parts (maximum, sum,
+// unnormalised output in 32 bits) in the workspace and k_attend_join adds them in order.
 #pragma once
 
 #include <type_traits>
@@ -39,9 +42,33 @@ constexpr int kAttendCUs = 256;
 constexpr int kAttendWaves = 4;
 constexpr int kAttendThreads = 64 * kAttendWaves;
 constexpr int kAttendTile = 32;                          // positions per tile
-constexpr int kAttendStep = kAttendTile * kAttendWaves;  // positions per step of the shares
+constexpr int kNonTemporal = 2;                          // cache policy: every tile is read once
 
-// The job that starts in a workgroup's share and ends in a later one (parts == 0: none).
+// The shares: one per workgroup that runs at once (R of them), or one per unit of work if there are
+// fewer.  A unit is a step, and every job has `job_cost` units more at its start for what a job costs
+// beside its steps.  Of the two workgroups on a CU the one launched later is slower by a seventh, so
+// the first half of the shares is larger (34 : 30).  More, smaller shares given out as places
+// become free even out the rest, and lose more than that to joining.
+__host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int64_t w) {
+  if (shares < R) return w;
+  const int64_t h = R / 2, first = R > kAttendCUs ? 34 : 32;
+  return all * (w < h ? first * w : first * h + (64 - first) * (w - h)) / (64 * h);
+}
+// the share that holds a unit
+__host__ __device__ inline int64_t share_of(int64_t all, int64_t shares, int R, int64_t unit) {
+  int64_t lo = 0, hi = shares;  // start(lo) <= unit < start(hi)
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (share_start(all, shares, R, mid) <= unit)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The job that starts in a workgroup's share and ends in a later one (parts == 0: none); h: head
+// group.
 struct AttendInfo {
   int32_t r, h, mt, parts, slot, pad[3];
 };
@@ -52,19 +79,24 @@ struct AttendPlan {
   int dp;         // head dimension rounded up to 64, 128 or 256
   int wgs;        // shares
   int mask_words; // 64-bit words of a block row's mask (tree)
+  int hpw;        // heads per workgroup
+  int prow;       // rows of a part in the workspace: the job's, at most blk G rounded up to 4
   size_t off_ml, off_o, off_mask, total;
 };
 
 struct AttendKernelArgs {
   AttendArgs a;
   int G, nmt, mask_words, wgs;
+  int job_cost;              // units of a job beside its steps
+  int hpw, hgroups;          // heads per workgroup (1 or 4), groups of them
+  int prow;                  // rows of a part in the workspace
   uint32_t ps_magic;         // ceil(2^32 / page_size)
   int row_groups;            // the rows of one load instruction lie in one page, strides below 2^31
   uint32_t page_bytes, row_bytes;  // the strides in bytes when row_groups
   float c;                   // scale log2(e)
   AttendInfo* info;          // [wgs]
-  float2* ml;                // [2 wgs][16 MT]
-  float* o;                  // [2 wgs][16 MT][DP]
+  float2* ml;                // [2 wgs][hpw][prow]
+  float* o;                  // [2 wgs][hpw][prow][DP]
   const uint64_t* mask;      // [batch][blk][mask_words] or null
 };
 
@@ -77,11 +109,12 @@ __device__ __host__ inline int job_keys(int L, int n, int G, int mt, int rows) {
   return L + last + 1;
 }
 
-// Two workgroups per CU (64 KiB rings, 256 registers per lane) for up to four row tiles of heads up to
-// 128, one (128 KiB, 512 registers) beyond.
-__host__ __device__ constexpr bool attend_two(int rb, int dp, int mt) {
-  return rb <= 256 && dp <= 128 && mt * dp <= 384 && mt <= 4;
-}
+// Two workgroups per CU (64 KiB rings, 256 registers per lane) for heads up to 128, one (128 KiB, 512
+// registers) beyond.
+__host__ __device__ constexpr bool attend_two(int dp) { return dp <= 128; }
+
+// With many rows the queries' fragments stay in LDS instead of registers.
+__host__ __device__ constexpr bool attend_q_lds(int dp, int mt) { return mt * dp > 256 || mt >= 4; }
 
 // Launchers, one per translation unit
 hipError_t launch_attend_bf16(const AttendKernelArgs& k, int dp, int mt, hipStream_t stream);
@@ -239,28 +272,31 @@ __device__ inline int64_t block_scan(int64_t x, int64_t* s, int64_t* total) {
   return before + inc - x;
 }
 
-// steps of job group mt of a line
-__device__ inline int job_steps(int L, int n, int G, int mt, int rows) {
-  const int keys = job_keys(L, n, G, mt, rows);
-  return (keys + kAttendStep - 1) / kAttendStep;
+// steps of job group mt of a line: a step is one tile of each wave
+__device__ inline int job_steps(const AttendKernelArgs& k, int keys) {
+  const int step = kAttendTile * kAttendWaves / k.hpw;
+  return (keys + step - 1) / step;
 }
-__device__ inline int64_t line_steps(const AttendKernelArgs& k, int r, int rows) {
+__device__ inline int64_t line_units(const AttendKernelArgs& k, int r, int rows) {
   int L, n;
   if (!line_rows(k.a.len, k.a.n_new, r, k.a.blk, k.a.c.slots, k.a.c.page_size, &L, &n) || n == 0)
     return 0;
   int64_t s = 0;
-  for (int mt = 0; mt < k.nmt; ++mt) s += job_steps(L, n, k.G, mt, rows);
-  return s * k.a.c.heads;
+  for (int mt = 0; mt < k.nmt; ++mt) {
+    const int keys = job_keys(L, n, k.G, mt, rows);
+    s += keys > 0 ? job_steps(k, keys) + k.job_cost : 0;
+  }
+  return s * k.hgroups;
 }
 
 // A workgroup's LDS: the waves' rings of K and V tiles, and for many rows the queries.
 template <int RB, int MT, int DP> struct Shape {
-  static constexpr bool kTwo = attend_two(RB, DP, MT);
+  static constexpr bool kTwo = attend_two(DP);
   static constexpr int kStage = 2 * kAttendTile * RB;  // K and V of one tile
   static constexpr int kRing = (kTwo ? 65536 : 131072) / kAttendWaves;
   static constexpr int kStages = kRing / kStage;
   static constexpr int kPerCU = kTwo ? 2 : 1;
-  static constexpr bool kQLds = MT * DP > 256;         // the queries' fragments stay in LDS
+  static constexpr bool kQLds = attend_q_lds(DP, MT);
   static constexpr int kLds = kRing * kAttendWaves + (kQLds ? MT * 16 * DP * 2 : 0);
 };
 
@@ -313,39 +349,42 @@ void k_attend(AttendKernelArgs k) {
   const int n16 = lane & 15, g = lane >> 4;
   const int ps = c.page_size;
 
-  // ---- this workgroup's share [x, x_end) of all steps, and the line that holds step x
-  int64_t total = 0;
-  for (int r0 = 0; r0 < a.batch; r0 += kAttendThreads) {
-    const int r = r0 + tid;
-    total += r < a.batch ? line_steps(k, r, ROWS) : 0;
-  }
-  int64_t all;
-  block_scan(total, s_scan, &all);
-  const int64_t shares = all < k.wgs ? all : k.wgs;
+  // ---- this workgroup's share [x, x_end) of all units, and the line that holds unit x
   const int64_t w = blockIdx.x;
-  if (w >= shares) {
-    if (tid == 0) k.info[w].parts = 0;
-    return;
+  if (tid == 0) k.info[w].parts = 0;
+  // units of the lines before line `tid`, of the line, and of all lines; the first 256 lines
+  const int64_t mine0 = tid < a.batch ? line_units(k, tid, ROWS) : 0;
+  int64_t all;
+  const int64_t at0 = block_scan(mine0, s_scan, &all);
+  int64_t base = all;
+  if (a.batch > kAttendThreads) {
+    int64_t more = 0, sum;
+    for (int r0 = kAttendThreads; r0 < a.batch; r0 += kAttendThreads)
+      more += r0 + tid < a.batch ? line_units(k, r0 + tid, ROWS) : 0;
+    block_scan(more, s_scan, &sum);
+    all += sum;
   }
-  int64_t x = all * w / shares;
-  const int64_t x_end = all * (w + 1) / shares;
-  int64_t base = 0;
-  for (int r0 = 0; r0 < a.batch; r0 += kAttendThreads) {
-    const int r = r0 + tid;
-    const int64_t mine = r < a.batch ? line_steps(k, r, ROWS) : 0;
+  const int64_t shares = min(all, (int64_t)k.wgs);
+  if (w >= shares) return;
+  int64_t x = share_start(all, shares, k.wgs, w);
+  const int64_t x_end = share_start(all, shares, k.wgs, w + 1);
+  if (at0 <= x && x < at0 + mine0) {
+    s_line = tid;
+    s_base = at0;
+  }
+  for (int r0 = kAttendThreads; base <= x; r0 += kAttendThreads) {
+    const int64_t mine = r0 + tid < a.batch ? line_units(k, r0 + tid, ROWS) : 0;
     int64_t part;
     const int64_t at = base + block_scan(mine, s_scan, &part);
     if (at <= x && x < at + mine) {
-      s_line = r;
+      s_line = r0 + tid;
       s_base = at;
     }
     base += part;
-    if (base > x) break;
   }
   __syncthreads();
   int r = s_line;
-  int64_t off = x - s_base;  // step within the line's jobs
-  if (tid == 0) k.info[w].parts = 0;
+  int64_t off = x - s_base;  // unit within the line's jobs
 
   char* const my_ring = ring + wave * Sh::kRing;
   bool first_segment = true;
@@ -354,34 +393,47 @@ void k_attend(AttendKernelArgs k) {
     int L, n;
     const bool live_line =
         line_rows(a.len, a.n_new, r, a.blk, c.slots, ps, &L, &n) && n > 0;
-    if (!live_line) continue;  // cannot run past the batch: steps are left
+    if (!live_line) continue;  // cannot run past the batch: units are left
     const int32_t* const tab = c.table + (int64_t)r * c.table_stride;
-    for (int h = 0; h < c.heads && x < x_end; ++h) {
+    for (int hg = 0; hg < k.hgroups && x < x_end; ++hg) {
+      const int h = hg * k.hpw + (k.hpw == 1 ? 0 : wave);
       for (int mt0 = 0; mt0 < k.nmt && x < x_end; ++mt0) {
         const int keys = job_keys(L, n, G, mt0, ROWS);
-        const int steps = (keys + kAttendStep - 1) / kAttendStep;
-        if (off >= steps) {
-          off -= steps;
+        const int steps = job_steps(k, keys);
+        const int units = keys > 0 ? steps + k.job_cost : 0;
+        if (off >= units) {
+          off -= units;
           continue;
         }
-        // ---- segment: steps [off, off + ns) of the job
-        const int ns = (int)(steps - off < x_end - x ? steps - off : x_end - x);
+        // ---- segment: units [off, off + take) of the job, its steps [step0, step1)
+        const int64_t job_x = x - off;
+        const int take = (int)min((int64_t)units - off, x_end - x);
+        const int step0 = max((int)off - k.job_cost, 0);
+        const int step1 = max((int)off + take - k.job_cost, 0);
+        x += take;
+        off = 0;
+        if (step0 >= step1) continue;
         const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
-        const int tile0 = (int)off * kAttendWaves;
-        const int tile1 = min(tile0 + ns * kAttendWaves, ntiles);
+        const int splits = kAttendWaves / k.hpw;  // waves that share a head's positions
+        const int tile0 = step0 * splits;
+        const int tile1 = min(step1 * splits, ntiles);
         const int cnt = tile1 - tile0;
-        const int t0 = tile0 + cnt * wave / kAttendWaves;
-        const int t1 = tile0 + cnt * (wave + 1) / kAttendWaves;
+        const int t0 = k.hpw == 1 ? tile0 + cnt * wave / kAttendWaves : tile0;
+        const int t1 = k.hpw == 1 ? tile0 + cnt * (wave + 1) / kAttendWaves : tile1;
 
         // ---- loads: tile t into stage t % NST
         const int chunks = dim * ES / 16;       // real chunks of a row
         const int64_t head_off = (int64_t)h * c.head_stride * ES;
         const char* const kbase = static_cast<const char*>(c.k) + head_off;
         const char* const vbase = static_cast<const char*>(c.v) + head_off;
-        int tab_chunk = -2, tab_now = 0, tab_next = 0, chunk_end = 0;
+        int tab_chunk, tab_now = 0, tab_next, chunk_end = 0;
         const uint32_t lane_ofs = (uint32_t)(lane / CPR) * k.row_bytes;
         const int last_slot = (keys - 1) / ps;
         auto fetch_tab = [&](int chunk) { return tab[min(chunk * 64 + lane, last_slot)]; };
+        {  // the first page ids are on their way while the queries are asked for
+          tab_chunk = (int)((uint32_t)(t0 * kAttendTile) / (64u * ps)) - 1;
+          tab_next = fetch_tab(tab_chunk + 1);
+        }
         // tile t into `to`: row i * RPI + lane / CPR of each load instruction; rows behind the job's
         // last position are read as the last
         auto issue = [&](int t, const char* from, char* to, auto is_v) {
@@ -412,7 +464,8 @@ void k_attend(AttendKernelArgs k) {
                   lim - rel >= RPI - 1 ? lane_ofs : (uint32_t)min(lane_row, lim - rel) * k.row_bytes;
               if (all || ch < chunks)
                 __builtin_amdgcn_global_load_lds((global_void*)(at + (row_ofs + (ch << 4))),
-                                                 (lds_void*)(to + i * 1024), 16, 0, 0);
+                                                 (lds_void*)(to + i * 1024), 16, 0,
+                                                 kNonTemporal);
             };
             if (dim == DP) {
 #pragma unroll
@@ -432,7 +485,8 @@ void k_attend(AttendKernelArgs k) {
                   from + ((int64_t)page * c.page_stride + (int64_t)(rel - idx * ps) * c.row_stride) * ES +
                   (ch << 4);
               if (ch < chunks)
-                __builtin_amdgcn_global_load_lds((global_void*)at, (lds_void*)(to + i * 1024), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((global_void*)at, (lds_void*)(to + i * 1024), 16, 0,
+                                                 kNonTemporal);
             }
           }
         };
@@ -659,91 +713,104 @@ void k_attend(AttendKernelArgs k) {
         for (const int tm = min(t1, L / kAttendTile); t < tm; ++t) tile(t, std::false_type{});
         for (; t < t1; ++t) tile(t, std::true_type{});
 
-        // ---- join the waves
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float l = group_sum(l_run[mt]);
-          if (g == 0) {
-            s_m[wave][mt * 16 + n16] = m_run[mt];
-            s_l[wave][mt * 16 + n16] = l;
-          }
-        }
-        const bool any_odd = __syncthreads_or(odd);
-        const bool whole = off == 0 && ns == steps;
-        const int slot = (int)(2 * w + (first_segment ? 0 : 1));
+        // ---- the job's output, or its part
+        const bool whole = step0 == 0 && step1 == steps;
+        const int64_t slot = 2 * w + (first_segment ? 0 : 1);
         const float vscale = F8 && c.v_scale ? c.v_scale[h] : 1.0f;
+        // dims d .. d+3 of row `row` of the job: the sums y over maximum m and weight l
+        auto finish = [&](int row, int d, f32x4 y, float m, float l, bool any_odd) {
+          const int q = mt0 * ROWS + row;
+          const int i = q / G;
+          if (any_odd) {  // NaN and infinities of the block rows that this row sees
+            const int j1 = min(tile1 * kAttendTile, keys) - L;
+            for (int j = max(tile0 * kAttendTile - L, 0); j < j1; ++j) {
+              const bool on = (visible(i < n ? i : -1, L + j) & 1u) != 0;
+              const int s = (L + j) / ps;
+              const int page = (uint32_t)tab[s] < (uint32_t)c.num_pages ? tab[s] : 0;
+              const char* v = static_cast<const char*>(c.v) + head_off + min(d, dim - 4) * ES +
+                              ((int64_t)page * c.page_stride + (int64_t)(L + j - s * ps) * c.row_stride) * ES;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float mx = kNegBig;
-#pragma unroll
-          for (int u = 0; u < kAttendWaves; ++u) mx = fmaxf(mx, s_m[u][mt * 16 + n16]);
-          const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
-          char* const mine = my_ring + n16 * (DP + 4) * 4 + 4 * g * 4;
-#pragma unroll
-          for (int d = 0; d < NT; ++d)
-            *reinterpret_cast<f32x4*>(mine + 16 * d * 4) = acc[mt][d] * f;
-          __syncthreads();
-          for (int it = tid; it < 16 * DP / 4; it += kAttendThreads) {
-            const int row = it / (DP / 4), d = (it - row * (DP / 4)) * 4;
-            const int m = mt0 * ROWS + mt * 16 + row;
-            const int i = m / G;
-            f32x4 y = {0, 0, 0, 0};
-            float rm = kNegBig, rl = 0.0f;
-#pragma unroll
-            for (int u = 0; u < kAttendWaves; ++u) {
-              y += *reinterpret_cast<const f32x4*>(ring + u * Sh::kRing + row * (DP + 4) * 4 + d * 4);
-              rm = fmaxf(rm, s_m[u][mt * 16 + row]);
-            }
-#pragma unroll
-            for (int u = 0; u < kAttendWaves; ++u)
-              rl += s_l[u][mt * 16 + row] * __builtin_amdgcn_exp2f(s_m[u][mt * 16 + row] - rm);
-            if (any_odd) {  // NaN and infinities of the block rows that this row sees
-              const int j1 = min(tile1 * kAttendTile, keys) - L;
-              for (int j = max(tile0 * kAttendTile - L, 0); j < j1; ++j) {
-                const bool on = (visible(i < n ? i : -1, L + j) & 1u) != 0;
-                const int s = (L + j) / ps;
-                const int page = (uint32_t)tab[s] < (uint32_t)c.num_pages ? tab[s] : 0;
-                const char* v = static_cast<const char*>(c.v) + head_off + min(d, dim - 4) * ES +
-                                ((int64_t)page * c.page_stride + (int64_t)(L + j - s * ps) * c.row_stride) * ES;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float z;
-                  if constexpr (F8)
-                    z = (float)E::template from_f8<false>(reinterpret_cast<const uint8_t*>(v)[e])[0];
-                  else
-                    z = (float)reinterpret_cast<const T*>(v)[e];
-                  y[e] += on && !__builtin_isfinite(z) ? z : 0.0f;
-                }
+              for (int e = 0; e < 4; ++e) {
+                float z;
+                if constexpr (F8)
+                  z = (float)E::template from_f8<false>(reinterpret_cast<const uint8_t*>(v)[e])[0];
+                else
+                  z = (float)reinterpret_cast<const T*>(v)[e];
+                y[e] += on && !__builtin_isfinite(z) ? z : 0.0f;
               }
-            }
-            if (!whole) {
-              if (i < n) {
-                *reinterpret_cast<f32x4*>(k.o + ((int64_t)slot * ROWS + mt * 16 + row) * DP + d) = y;
-                if (d == 0) k.ml[(int64_t)slot * ROWS + mt * 16 + row] = make_float2(rm, rl);
-              }
-            } else if (i < n && d < dim) {
-              x4 z;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] / rl * vscale);
-              T* out = static_cast<T*>(a.out) + ((int64_t)r * a.blk + i) * a.out_stride +
-                       (int64_t)(h * G + (m - i * G)) * dim + d;
-              *reinterpret_cast<x4*>(out) = z;
             }
           }
-          __syncthreads();
+          if (i >= n) return;
+          if (whole) {
+            if (d >= dim) return;
+            const float f = vscale / l;
+            x4 z;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] * f);
+            *reinterpret_cast<x4*>(static_cast<T*>(a.out) + ((int64_t)r * a.blk + i) * a.out_stride +
+                                   (int64_t)(h * G + (q - i * G)) * dim + d) = z;
+          } else {
+            const int64_t at = (slot * k.hpw + (h - hg * k.hpw)) * k.prow + row;
+            *reinterpret_cast<f32x4*>(k.o + at * DP + d) = y;
+            if (d == 0) k.ml[at] = make_float2(m, l);
+          }
+        };
+        if (!kQLds && k.hpw > 1) {  // the wave has the head to itself
+          const bool any_odd = __any(odd);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float l = group_sum(l_run[mt]);
+#pragma unroll
+            for (int d = 0; d < NT; ++d)
+              finish(mt * 16 + n16, 16 * d + 4 * g, acc[mt][d], m_run[mt], l, any_odd);
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float l = group_sum(l_run[mt]);
+            if (g == 0) {
+              s_m[wave][mt * 16 + n16] = m_run[mt];
+              s_l[wave][mt * 16 + n16] = l;
+            }
+          }
+          const bool any_odd = __syncthreads_or(odd);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float mx = kNegBig;
+#pragma unroll
+            for (int u = 0; u < kAttendWaves; ++u) mx = fmaxf(mx, s_m[u][mt * 16 + n16]);
+            const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
+            char* const mine = my_ring + n16 * (DP + 4) * 4 + 4 * g * 4;
+#pragma unroll
+            for (int d = 0; d < NT; ++d)
+              *reinterpret_cast<f32x4*>(mine + 16 * d * 4) = acc[mt][d] * f;
+            __syncthreads();
+            for (int it = tid; it < 16 * DP / 4; it += kAttendThreads) {
+              const int row = it / (DP / 4), d = (it - row * (DP / 4)) * 4;
+              f32x4 y = {0, 0, 0, 0};
+              float rm = kNegBig, rl = 0.0f;
+#pragma unroll
+              for (int u = 0; u < kAttendWaves; ++u) {
+                y += *reinterpret_cast<const f32x4*>(ring + u * Sh::kRing + row * (DP + 4) * 4 + d * 4);
+                rm = fmaxf(rm, s_m[u][mt * 16 + row]);
+              }
+#pragma unroll
+              for (int u = 0; u < kAttendWaves; ++u)
+                rl += s_l[u][mt * 16 + row] * __builtin_amdgcn_exp2f(s_m[u][mt * 16 + row] - rm);
+              finish(mt * 16 + row, d, y, rm, rl, any_odd);
+            }
+            __syncthreads();
+          }
         }
-        if (!whole && off == 0 && tid == 0) {  // the job starts here and ends in a later share
-          const int64_t last = x + steps - 1;  // its last step
-          const int64_t wl = ((last + 1) * shares - 1) / all;
+        if (!whole && step0 == 0 && tid == 0) {  // the job starts here and ends in a later share
+          const int64_t wl = share_of(all, shares, k.wgs, job_x + units - 1);
           AttendInfo& o = k.info[w];
           o.r = r;
-          o.h = h;
+          o.h = hg;
           o.mt = mt0;
-          o.slot = slot;
+          o.slot = (int)slot;
           o.parts = (int)(wl - w) + 1;
         }
-        x += ns;
-        off = 0;
         first_segment = false;
       }
     }
@@ -778,15 +845,12 @@ hipError_t launch_typed(const AttendKernelArgs& k, int dp, int mt, hipStream_t s
       case 1: return launch_one<T, F8, 64, 1>(k, stream);
       case 2: return launch_one<T, F8, 64, 2>(k, stream);
       case 4: return launch_one<T, F8, 64, 4>(k, stream);
-      case 6: return launch_one<T, F8, 64, 6>(k, stream);
     }
   } else if (dp == 128) {
     switch (mt) {
       case 1: return launch_one<T, F8, 128, 1>(k, stream);
       case 2: return launch_one<T, F8, 128, 2>(k, stream);
       case 3: return launch_one<T, F8, 128, 3>(k, stream);
-      case 4: return launch_one<T, F8, 128, 4>(k, stream);
-      case 5: return launch_one<T, F8, 128, 5>(k, stream);
     }
   } else if (dp == 256) {
     switch (mt) {

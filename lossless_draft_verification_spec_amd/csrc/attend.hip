@@ -7,15 +7,20 @@ namespace {
 
 using attend::f32x4;
 
+constexpr int kJoinRows = 4;
+constexpr int kJoinWaves = 4;
+
 // Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
 // the instantiated sizes allow (each group reads every key and value again), then the smallest
-// size that holds a group: rows that pad a tile cost matrix work.
+// size that holds a group: rows that pad a tile cost matrix work.  The largest sizes are those with
+// which two workgroups run on a CU: 132 rows of 128 dims took 102 us as two groups of 5 tiles, one
+// wave per SIMD, and 92 us as three groups of 3 although every position is read three times.
 AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int dim) {
   AttendPlan p{};
   p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  static const int k64[] = {1, 2, 4, 6}, k128[] = {1, 2, 3, 4, 5}, k256[] = {1, 2};
+  static const int k64[] = {1, 2, 4}, k128[] = {1, 2, 3}, k256[] = {1, 2};
   const int* sizes = p.dp == 64 ? k64 : p.dp == 128 ? k128 : k256;
-  const int ns = p.dp == 64 ? 4 : p.dp == 128 ? 5 : 2;
+  const int ns = p.dp == 256 ? 2 : 3;
   const int64_t rows = (int64_t)blk * (heads_q / heads_kv);
   const int most = sizes[ns - 1] * 16;
   p.nmt = (int)((rows + most - 1) / most);
@@ -23,8 +28,10 @@ AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int d
   for (int i = ns - 1; i >= 0; --i)
     if (sizes[i] >= tiles) p.mt = sizes[i];
   p.nmt = (int)((rows + p.mt * 16 - 1) / (p.mt * 16));
-  p.wgs = 2 * kAttendCUs;  // the kernels that run one workgroup per CU use half of them
+  p.wgs = (attend_two(p.dp) ? 2 : 1) * kAttendCUs;
   p.mask_words = (blk + 63) / 64;
+  p.hpw = !attend_q_lds(p.dp, p.mt) && heads_kv % 4 == 0 ? 4 : 1;
+  p.prow = (int)((rows < p.mt * 16 ? rows : p.mt * 16) + kJoinRows - 1) / kJoinRows * kJoinRows;
   size_t off = 0;
   auto take = [&](size_t n) {
     const size_t at = off;
@@ -32,8 +39,8 @@ AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int d
     return at;
   };
   take(sizeof(AttendInfo) * p.wgs);
-  p.off_ml = take(sizeof(float2) * 2 * p.wgs * p.mt * 16);
-  p.off_o = take(sizeof(float) * 2 * p.wgs * p.mt * 16 * (size_t)p.dp);
+  p.off_ml = take(sizeof(float2) * 2 * p.wgs * p.hpw * p.prow);
+  p.off_o = take(sizeof(float) * 2 * p.wgs * p.hpw * p.prow * (size_t)p.dp);
   p.off_mask = take(sizeof(uint64_t) * (size_t)batch * blk * p.mask_words);
   p.total = off;
   return p;
@@ -60,19 +67,18 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
   }
 }
 
-// Blocks [0, wgs * groups): four rows of the job that starts in share w and ends in a later one; the
-// four waves take every fourth part, a lane the same 16 bytes of each, and are added in order.
+// Blocks [0, wgs * groups): four rows of one head of the job that starts in share w and ends in a later one; the
+// waves take every fourth part, a lane the same 16 bytes of each, and are added in order.
 // Blocks behind them: the status of one line each.
-constexpr int kJoinRows = 4;
-
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int rows, int groups, int f8) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int f8) {
   constexpr int NV = kJoinRows * DP / 4 / 64;  // 16-byte pieces per lane
-  __shared__ f32x4 s_o[4][kJoinRows * DP / 4];
-  __shared__ float s_m[4][kJoinRows], s_l[4][kJoinRows];
+  __shared__ f32x4 s_o[kJoinWaves][kJoinRows * DP / 4];
+  __shared__ float s_m[kJoinWaves][kJoinRows], s_l[kJoinWaves][kJoinRows];
   const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int groups = k.hpw * (k.prow / kJoinRows);
   if ((int)blockIdx.x >= k.wgs * groups) {
     const int r = blockIdx.x - k.wgs * groups;
     int L, n;
@@ -80,9 +86,9 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int row
     if (!bad && n > 0) {
       const int32_t* tab = c.table + (int64_t)r * c.table_stride;
       const int last = (int)(((int64_t)L + n - 1) / c.page_size);
-      for (int s = threadIdx.x; s <= last; s += 256) bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
+      for (int s = threadIdx.x; s <= last; s += 64 * kJoinWaves) bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
       if (a.parent)
-        for (int j = threadIdx.x; j < n; j += 256) {
+        for (int j = threadIdx.x; j < n; j += 64 * kJoinWaves) {
           const int p = a.parent[(int64_t)r * a.blk + j];
           badp |= p < -1 || p >= j;
         }
@@ -93,7 +99,8 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int row
     return;
   }
   const int w = blockIdx.x / groups;
-  const int row0 = (blockIdx.x - w * groups) * kJoinRows;
+  const int hi = (blockIdx.x - w * groups) / (k.prow / kJoinRows);
+  const int row0 = (blockIdx.x - w * groups - hi * (k.prow / kJoinRows)) * kJoinRows;
   const AttendInfo in = k.info[w];
   if (in.parts == 0) return;
   int L, n;
@@ -109,28 +116,29 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int row
     m[v] = kNegBig;
     l[v] = 0.0f;
   }
-  constexpr int kAhead = 4;  // parts loaded together
-  for (int p0 = wave; p0 < in.parts; p0 += 4 * kAhead) {
+  constexpr int kAhead = DP > 128 ? 4 : 8;  // parts loaded together
+  for (int p0 = wave; p0 < in.parts; p0 += kJoinWaves * kAhead) {
     f32x4 y[kAhead][NV];
     float2 ml[kAhead][NV];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int p = p0 + 4 * u;
+      const int p = p0 + kJoinWaves * u;
       if (p < in.parts) {
         const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
+        const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int e = (v * 64 + lane) * 4, row = e / DP;
           if (row < live) {
-            ml[u][v] = k.ml[slot * rows + row0 + row];
-            y[u][v] = *reinterpret_cast<const f32x4*>(k.o + (slot * rows + row0) * DP + e);
+            ml[u][v] = k.ml[at + row];
+            y[u][v] = *reinterpret_cast<const f32x4*>(k.o + at * DP + e);
           }
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (p0 + 4 * u < in.parts) {
+      if (p0 + kJoinWaves * u < in.parts) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           if ((v * 64 + lane) * 4 / DP < live) {
@@ -155,39 +163,40 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendKernelArgs k, int row
     }
   }
   __syncthreads();
-  for (int it = threadIdx.x; it < kJoinRows * DP / 4; it += 256) {
+  for (int it = threadIdx.x; it < kJoinRows * DP / 4; it += 64 * kJoinWaves) {
     const int row = it * 4 / DP, d = it * 4 - row * DP;
     if (row >= live || d >= c.dim) continue;
     float mx = kNegBig, sum = 0.0f;
-    for (int u = 0; u < 4; ++u) mx = fmaxf(mx, s_m[u][row]);
+    for (int u = 0; u < kJoinWaves; ++u) mx = fmaxf(mx, s_m[u][row]);
     f32x4 y = {0, 0, 0, 0};
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kJoinWaves; ++u) {
       const float f = __builtin_amdgcn_exp2f(s_m[u][row] - mx);
       y += s_o[u][it] * f;
       sum += s_l[u][row] * f;
     }
-    const float vs = f8 && c.v_scale ? c.v_scale[in.h] : 1.0f;
+    const int h = in.h * k.hpw + hi;
+    const float vs = f8 && c.v_scale ? c.v_scale[h] : 1.0f;
     const int q = in.mt * rows + row0 + row, i = q / k.G;
     typename attend::Elem<T>::x4 z;
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] / sum * vs);
     T* out = static_cast<T*>(a.out) + ((int64_t)in.r * a.blk + i) * a.out_stride +
-             (int64_t)(in.h * k.G + (q - i * k.G)) * c.dim + d;
+             (int64_t)(h * k.G + (q - i * k.G)) * c.dim + d;
     *reinterpret_cast<typename attend::Elem<T>::x4*>(out) = z;
   }
 }
 
 template <typename T>
 hipError_t launch_join(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
-  const int rows = p.mt * 16, groups = rows / kJoinRows;
+  const int rows = p.mt * 16, groups = p.hpw * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
-  const dim3 grid((unsigned)(k.wgs * groups + (k.a.status ? k.a.batch : 0))), block(256);
+  const dim3 grid((unsigned)(k.wgs * groups + (k.a.status ? k.a.batch : 0))), block(64 * kJoinWaves);
   if (p.dp == 64)
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 64>), grid, block, 0, stream, k, rows, groups, f8);
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 64>), grid, block, 0, stream, k, rows, f8);
   else if (p.dp == 128)
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 128>), grid, block, 0, stream, k, rows, groups, f8);
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 128>), grid, block, 0, stream, k, rows, f8);
   else
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 256>), grid, block, 0, stream, k, rows, groups, f8);
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 256>), grid, block, 0, stream, k, rows, f8);
   return hipGetLastError();
 }
 
@@ -208,7 +217,11 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.nmt = p.nmt;
   k.mask_words = p.mask_words;
   const int rb = p.dp * (f8 ? 1 : 2);
-  k.wgs = attend_two(rb, p.dp, p.mt) ? 2 * kAttendCUs : kAttendCUs;
+  k.wgs = p.wgs;
+  k.hpw = p.hpw;
+  k.hgroups = a.c.heads / p.hpw;
+  k.prow = p.prow;
+  k.job_cost = p.hpw > 1 ? 1 : 3;
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;

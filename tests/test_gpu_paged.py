@@ -9,7 +9,7 @@ import torch
 
 import paged_ref as ref
 from lossless_draft_verification_spec_amd import (
-    PsispecError, psispec_pages_assign, psispec_pages_reserve, psispec_paged_attention,
+    PsispecError, paged_attention_workspace_bytes, pages_workspace_bytes, psispec_pages_assign, psispec_pages_reserve, psispec_paged_attention,
     psispec_paged_commit, psispec_qkv_append, psispec_verify_tree, rope_frequencies, workloads)
 
 pytestmark = pytest.mark.gpu
@@ -256,7 +256,6 @@ def test_attend_strided_rows_streams_and_reruns():
     wide[:, :tab.shape[1]] = tab
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    from lossless_draft_verification_spec_amd import paged_attention_workspace_bytes
     ws = torch.full((paged_attention_workspace_bytes(3, 3, 8, 2, 128),), 255, dtype=torch.uint8,
                     device=DEV)
     torch.cuda.synchronize()
@@ -705,8 +704,9 @@ def test_graph_replays():
         psispec_paged_commit(s["pool"], s["tab"], s["ln"], blk, s["nk"])
 
     def work():
-        return [torch.empty(1 << 16, dtype=torch.uint8, device=DEV),
-                torch.empty(1 << 26, dtype=torch.uint8, device=DEV)]
+        sizes = (pages_workspace_bytes(batch, slots, pages, blk, ps),
+                 paged_attention_workspace_bytes(batch, blk, hq, hkv, dim))
+        return [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
 
     cap = state(0)
     out = torch.zeros((batch, blk, hq, dim), dtype=BF, device=DEV)
