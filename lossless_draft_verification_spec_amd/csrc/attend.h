@@ -42,17 +42,28 @@ constexpr int kAttendCUs = 256;
 constexpr int kAttendWaves = 4;
 constexpr int kAttendThreads = 64 * kAttendWaves;
 constexpr int kAttendTile = 32;                          // positions per tile
-constexpr int kNonTemporal = 2;                          // cache policy: every tile is read once
+// Cache policy of the tiles: nontemporal when each is read once (64 lines of 1000-8000 positions:
+// 210 us without, 187 with); kept when several row groups of a job read them (33-row trees: 89 us
+// nontemporal, 79 kept).
+constexpr int kNonTemporal = 2;
 
 // The shares: one per workgroup that runs at once (R of them), or one per unit of work if there are
 // fewer.  A unit is a step, and every job has `job_cost` units more at its start for what a job costs
-// beside its steps.  Of the two workgroups on a CU the one launched later is slower by a seventh, so
-// the first half of the shares is larger (34 : 30).  More, smaller shares given out as places
-// become free even out the rest, and lose more than that to joining.
+// beside its steps.  Workgroups are dealt to the 8 XCDs in turn; each XCD gets a contiguous run of
+// shares, so that the row groups and heads that read the same pages meet in one L2.  Of the two
+// workgroups on a CU the one launched later is slower by a seventh, so the shares of the first half
+// of an XCD's workgroups are larger (34 : 30).  More, smaller shares given out as places become free
+// even out the rest, and lose more than that to joining.
+constexpr int kXcds = 8;
+__host__ __device__ inline int64_t share_of_block(int64_t shares, int R, int b) {
+  return shares < R ? b : (int64_t)(b % kXcds) * (R / kXcds) + b / kXcds;
+}
 __host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int64_t w) {
   if (shares < R) return w;
-  const int64_t h = R / 2, first = R > kAttendCUs ? 34 : 32;
-  return all * (w < h ? first * w : first * h + (64 - first) * (w - h)) / (64 * h);
+  const int64_t per = R / kXcds, h = per / 2, first = R > kAttendCUs ? 34 : 32;
+  const int64_t x = w / per, j = w - x * per;
+  const int64_t at = j < h ? first * j : first * h + (64 - first) * (j - h);
+  return all * (x * 64 * h + at) / (kXcds * 64 * h);
 }
 // the share that holds a unit
 __host__ __device__ inline int64_t share_of(int64_t all, int64_t shares, int R, int64_t unit) {
@@ -91,8 +102,8 @@ struct AttendKernelArgs {
   int hpw, hgroups;          // heads per workgroup (1 or 4), groups of them
   int prow;                  // rows of a part in the workspace
   uint32_t ps_magic;         // ceil(2^32 / page_size)
-  int row_groups;            // the rows of one load instruction lie in one page, strides below 2^31
-  uint32_t page_bytes, row_bytes;  // the strides in bytes when row_groups
+  int halves;                // whole heads of DP dims, pages of 16-position multiples, strides below 2^31
+  uint32_t page_bytes, row_bytes;  // the strides in bytes when halves
   float c;                   // scale log2(e)
   AttendInfo* info;          // [wgs]
   float2* ml;                // [2 wgs][hpw][prow]
@@ -125,6 +136,7 @@ hipError_t launch_attend_f16_f8(const AttendKernelArgs& k, int dp, int mt, hipSt
 namespace attend {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_void;
@@ -178,6 +190,11 @@ __device__ __attribute__((always_inline)) inline typename Elem<T>::x4 lds_tr16(
 }
 __device__ __attribute__((always_inline)) inline i32x2 lds_tr8(const char* __restrict__ p) {
   return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
+}
+
+// 16 bytes per lane straight to LDS, lane l's at to + 16 l (to: wave-uniform)
+template <int POLICY> __device__ inline void load_lds(const char* from, char* to) {
+  __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, POLICY);
 }
 
 // eight 8-bit numbers as T (exact)
@@ -317,6 +334,7 @@ template <typename T, bool F8, int DP, int MT>
 __global__ __launch_bounds__(kAttendThreads, (Shape<(F8 ? 1 : 2) * DP, MT, DP>::kPerCU))
 void k_attend(AttendKernelArgs k) {
   typedef Elem<T> E;
+  typedef typename E::x2 x2;
   typedef typename E::x4 x4;
   typedef typename E::x8 x8;
   constexpr int ES = F8 ? 1 : 2;
@@ -350,8 +368,6 @@ void k_attend(AttendKernelArgs k) {
   const int ps = c.page_size;
 
   // ---- this workgroup's share [x, x_end) of all units, and the line that holds unit x
-  const int64_t w = blockIdx.x;
-  if (tid == 0) k.info[w].parts = 0;
   // units of the lines before line `tid`, of the line, and of all lines; the first 256 lines
   const int64_t mine0 = tid < a.batch ? line_units(k, tid, ROWS) : 0;
   int64_t all;
@@ -365,6 +381,8 @@ void k_attend(AttendKernelArgs k) {
     all += sum;
   }
   const int64_t shares = min(all, (int64_t)k.wgs);
+  const int64_t w = share_of_block(shares, k.wgs, blockIdx.x);
+  if (tid == 0) k.info[w].parts = 0;
   if (w >= shares) return;
   int64_t x = share_start(all, shares, k.wgs, w);
   const int64_t x_end = share_start(all, shares, k.wgs, w + 1);
@@ -447,35 +465,35 @@ void k_attend(AttendKernelArgs k) {
             tab_next = fetch_tab(chunk + 1);
           }
           const int rel0 = tile_pos + 64 * ps - chunk_end;
-          const int lim = keys - 1 + 64 * ps - chunk_end;
           const int lane_row = lane / CPR;
           const int swz = is_v() ? swz_v<RB, F8>(lane_row) : swz_k<RB>(lane_row);
           const int lane_chunk = (lane % CPR) ^ swz;
-          if (k.row_groups) {  // the rows of one instruction lie in one page; 32-bit strides
-            auto load = [&](int i, bool all) {
-              const int rel = min(rel0 + i * RPI, lim);
-              const int idx = ps == 1 ? rel : (int)__umulhi((uint32_t)rel, k.ps_magic);
-              const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(tab_now, idx);
-              const char* const at = from + (uint64_t)page * k.page_bytes +
-                                     (uint32_t)(rel - idx * ps) * k.row_bytes;
-              const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
-              // lane_row * row_bytes unless rows behind the last are asked for
-              const uint32_t row_ofs =
-                  lim - rel >= RPI - 1 ? lane_ofs : (uint32_t)min(lane_row, lim - rel) * k.row_bytes;
-              if (all || ch < chunks)
-                __builtin_amdgcn_global_load_lds((global_void*)(at + (row_ofs + (ch << 4))),
-                                                 (lds_void*)(to + i * 1024), 16, 0,
-                                                 kNonTemporal);
-            };
-            if (dim == DP) {
+          if (k.halves && tile_pos + kAttendTile <= keys) {
+            // whole tile, each 16 positions of it in one page: two scalar addresses
 #pragma unroll
-              for (int i = 0; i < NLD; ++i) load(i, true);
-            } else {
-#pragma unroll 1
-              for (int i = 0; i < NLD; ++i) load(i, false);
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t rel = rel0 + 16 * half;
+              const uint32_t idx = __umulhi(rel, k.ps_magic);
+              const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(tab_now, idx);
+              const char* const at0 =
+                  from + (uint64_t)page * k.page_bytes + (rel - idx * ps) * k.row_bytes;
+              auto rows = [&](auto policy) {
+                const char* at = at0;
+#pragma unroll
+                for (int i = half * NLD / 2; i < (half + 1) * NLD / 2; ++i) {
+                  const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
+                  load_lds<decltype(policy)::value>(at + (lane_ofs + (ch << 4)), to + i * 1024);
+                  at += RPI * k.row_bytes;
+                }
+              };
+              if (k.nmt > 1)
+                rows(std::integral_constant<int, 0>{});
+              else
+                rows(std::integral_constant<int, kNonTemporal>{});
             }
           } else {
-#pragma unroll 1
+            const int lim = keys - 1 + 64 * ps - chunk_end;
+#pragma unroll 2
             for (int i = 0; i < NLD; ++i) {
               const int rel = min(rel0 + i * RPI + lane_row, lim);
               const int idx = ps == 1 ? rel : (int)__umulhi((uint32_t)rel, k.ps_magic);
@@ -485,11 +503,12 @@ void k_attend(AttendKernelArgs k) {
                   from + ((int64_t)page * c.page_stride + (int64_t)(rel - idx * ps) * c.row_stride) * ES +
                   (ch << 4);
               if (ch < chunks)
-                __builtin_amdgcn_global_load_lds((global_void*)at, (lds_void*)(to + i * 1024), 16, 0,
-                                                 kNonTemporal);
+                load_lds<kNonTemporal>(at, to + i * 1024);
             }
           }
         };
+        const float sc_signed = k.c * (F8 && c.k_scale ? c.k_scale[h] : 1.0f);
+        const float sc = fabsf(sc_signed);
         // ---- queries: row n16 of each 16-row tile, in registers, or for many rows in LDS in the
         // order of the fragments
         x8 qf[kQLds ? 1 : MT][kQLds ? 1 : KS];
@@ -510,13 +529,13 @@ void k_attend(AttendKernelArgs k) {
             const int d = F8 ? (4 * (s >> 1) + g) * 16 + (s & 1) * 8 : (4 * s + g) * 8;
             x8 z = {};
             if (d < dim && i < n) z = *reinterpret_cast<const x8*>(q + d);
+            if (sc_signed < 0.0f) z = -z;
             if constexpr (kQLds)
               *reinterpret_cast<x8*>(q_lds + ((mt * KS + s) * 64 + lane) * 16) = z;
             else
               qf[mt][s] = z;
           }
         }
-        const float sc = k.c * (F8 && c.k_scale ? c.k_scale[h] : 1.0f);
         if constexpr (kQLds) {
           __syncthreads();
         } else {
@@ -619,17 +638,17 @@ void k_attend(AttendKernelArgs k) {
           x8 p_hi[MT], p_lo[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float xs[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) xs[e] = s[mt][e >> 2][e & 3] * sc;
+            uint32_t see = ~0u;
             if constexpr (TAIL) {
-              const uint32_t see = visible(irow[mt], pos0) >> (4 * g);
+              see = visible(irow[mt], pos0) >> (4 * g);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                xs[e] = (see >> (16 * (e >> 2) + (e & 3))) & 1u ? xs[e] : -INFINITY;
+                s[mt][e >> 2][e & 3] =
+                    (see >> (16 * (e >> 2) + (e & 3))) & 1u ? s[mt][e >> 2][e & 3] : -INFINITY;
             }
-            float mx = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])),
-                             fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
+            float mx = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
+                             fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
+            mx *= sc;  // sc >= 0: a negative scale is in the queries' signs
             if (__any(mx > m_run[mt] + 8.0f)) {
               mx = fmaxf(group_max(mx), m_run[mt]);
               const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
@@ -640,12 +659,20 @@ void k_attend(AttendKernelArgs k) {
             }
             float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = __builtin_amdgcn_exp2f(xs[e] - m_run[mt]);
-              sum += p;
-              const T hi = (T)p;
-              p_hi[mt][e] = hi;
-              p_lo[mt][e] = (T)(p - (float)hi);
+            for (int e = 0; e < 8; e += 2) {
+              f32x2 p;
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                p[u] = __builtin_amdgcn_exp2f(fmaf(s[mt][(e + u) >> 2][(e + u) & 3], sc, -m_run[mt]));
+                if constexpr (TAIL) p[u] = (see >> (16 * (e >> 2) + ((e + u) & 3))) & 1u ? p[u] : 0.0f;
+              }
+              sum += p[0] + p[1];
+              const x2 hi = __builtin_convertvector(p, x2);
+              const x2 lo = __builtin_convertvector(p - __builtin_convertvector(hi, f32x2), x2);
+              p_hi[mt][e] = hi[0];
+              p_hi[mt][e + 1] = hi[1];
+              p_lo[mt][e] = lo[0];
+              p_lo[mt][e + 1] = lo[1];
             }
             l_run[mt] += sum;
           }

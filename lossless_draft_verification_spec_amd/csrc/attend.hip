@@ -8,7 +8,6 @@ namespace {
 using attend::f32x4;
 
 constexpr int kJoinRows = 4;
-constexpr int kJoinWaves = 4;
 
 // Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
 // the instantiated sizes allow (each group reads every key and value again), then the smallest
@@ -67,26 +66,85 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
   }
 }
 
-// Blocks [0, wgs * groups): four rows of one head of the job that starts in share w and ends in a later one; the
-// waves take every fourth part, a lane the same 16 bytes of each, and are added in order.
-// Blocks behind them: the status of one line each.
-template <typename T, int DP>
+// An item is four rows of one head of the job that starts in share w and ends in a later one; its parts
+// are added in order, a lane the same 16 bytes of each.  WIDE (few jobs, many parts each): a block per
+// item, its waves take every fourth part and are added at the end.  Otherwise a wave per item.  Blocks
+// behind the items: the status of one line each.
+constexpr int kJoinWaves = 4;
+
+// the parts first, first + stride, ... of rows row0 .. row0+3 (live of them)
+template <int DP> struct JoinSum {
+  static constexpr int NV = kJoinRows * DP / 4 / 64;  // 16-byte pieces per lane
+  f32x4 o[NV];
+  float m[NV], l[NV];
+  __device__ void run(const AttendKernelArgs& k, const AttendInfo& in, int w, int hi, int row0, int live,
+                      int first, int stride) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      o[v] = f32x4{0, 0, 0, 0};
+      m[v] = kNegBig;
+      l[v] = 0.0f;
+    }
+    constexpr int kAhead = DP > 128 ? 4 : 8;  // parts loaded together
+    for (int p0 = first; p0 < in.parts; p0 += stride * kAhead) {
+      f32x4 y[kAhead][NV];
+      float2 ml[kAhead][NV];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int p = p0 + stride * u;
+        if (p < in.parts) {
+          const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
+          const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int e = (v * 64 + lane) * 4, row = e / DP;
+            if (row < live) {
+              ml[u][v] = k.ml[at + row];
+              y[u][v] = *reinterpret_cast<const f32x4*>(k.o + at * DP + e);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (p0 + stride * u < in.parts) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            if ((v * 64 + lane) * 4 / DP < live) {
+              const float mx = fmaxf(m[v], ml[u][v].x);
+              const float f0 = __builtin_amdgcn_exp2f(m[v] - mx);
+              const float f1 = __builtin_amdgcn_exp2f(ml[u][v].x - mx);
+              o[v] = o[v] * f0 + y[u][v] * f1;
+              l[v] = l[v] * f0 + ml[u][v].y * f1;
+              m[v] = mx;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+template <typename T, int DP, bool WIDE>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int f8) {
-  constexpr int NV = kJoinRows * DP / 4 / 64;  // 16-byte pieces per lane
-  __shared__ f32x4 s_o[kJoinWaves][kJoinRows * DP / 4];
+  typedef JoinSum<DP> Sum;
+  __shared__ f32x4 s_o[WIDE ? kJoinWaves : 1][kJoinRows * DP / 4];
   __shared__ float s_m[kJoinWaves][kJoinRows], s_l[kJoinWaves][kJoinRows];
   const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int groups = k.hpw * (k.prow / kJoinRows);
-  if ((int)blockIdx.x >= k.wgs * groups) {
-    const int r = blockIdx.x - k.wgs * groups;
+  const int quads = k.prow / kJoinRows, items = k.wgs * k.hpw * quads;
+  const int item_blocks = WIDE ? items : (items + kJoinWaves - 1) / kJoinWaves;
+  if ((int)blockIdx.x >= item_blocks) {
+    const int r = blockIdx.x - item_blocks;
     int L, n;
     bool bad = !line_rows(a.len, a.n_new, r, a.blk, c.slots, c.page_size, &L, &n), badp = false;
     if (!bad && n > 0) {
       const int32_t* tab = c.table + (int64_t)r * c.table_stride;
       const int last = (int)(((int64_t)L + n - 1) / c.page_size);
-      for (int s = threadIdx.x; s <= last; s += 64 * kJoinWaves) bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
+      for (int s = threadIdx.x; s <= last; s += 64 * kJoinWaves)
+        bad |= (uint32_t)tab[s] >= (uint32_t)c.num_pages;
       if (a.parent)
         for (int j = threadIdx.x; j < n; j += 64 * kJoinWaves) {
           const int p = a.parent[(int64_t)r * a.blk + j];
@@ -98,106 +156,83 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
       a.status[r] = (b0 ? PSISPEC_ST_BAD_PAGE : 0) | (b1 ? PSISPEC_ST_BAD_PARENT : 0);
     return;
   }
-  const int w = blockIdx.x / groups;
-  const int hi = (blockIdx.x - w * groups) / (k.prow / kJoinRows);
-  const int row0 = (blockIdx.x - w * groups - hi * (k.prow / kJoinRows)) * kJoinRows;
+  const int item = WIDE ? blockIdx.x : blockIdx.x * kJoinWaves + wave;
+  if (item >= items) return;
+  const int w = item / (k.hpw * quads);
+  const int hi = (item - w * k.hpw * quads) / quads;
+  const int row0 = (item % quads) * kJoinRows;
   const AttendInfo in = k.info[w];
   if (in.parts == 0) return;
   int L, n;
   line_rows(a.len, a.n_new, in.r, a.blk, c.slots, c.page_size, &L, &n);
   const int live = min(n * k.G - in.mt * rows, rows) - row0;  // live rows from row0 on
   if (live <= 0) return;
-
-  f32x4 o[NV];
-  float m[NV], l[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    o[v] = f32x4{0, 0, 0, 0};
-    m[v] = kNegBig;
-    l[v] = 0.0f;
-  }
-  constexpr int kAhead = DP > 128 ? 4 : 8;  // parts loaded together
-  for (int p0 = wave; p0 < in.parts; p0 += kJoinWaves * kAhead) {
-    f32x4 y[kAhead][NV];
-    float2 ml[kAhead][NV];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int p = p0 + kJoinWaves * u;
-      if (p < in.parts) {
-        const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
-        const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int e = (v * 64 + lane) * 4, row = e / DP;
-          if (row < live) {
-            ml[u][v] = k.ml[at + row];
-            y[u][v] = *reinterpret_cast<const f32x4*>(k.o + at * DP + e);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (p0 + kJoinWaves * u < in.parts) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if ((v * 64 + lane) * 4 / DP < live) {
-            const float mx = fmaxf(m[v], ml[u][v].x);
-            const float f0 = __builtin_amdgcn_exp2f(m[v] - mx);
-            const float f1 = __builtin_amdgcn_exp2f(ml[u][v].x - mx);
-            o[v] = o[v] * f0 + y[u][v] * f1;
-            l[v] = l[v] * f0 + ml[u][v].y * f1;
-            m[v] = mx;
-          }
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = v * 64 + lane;
-    s_o[wave][e] = o[v];
-    if (e * 4 % DP == 0) {
-      s_m[wave][e * 4 / DP] = m[v];
-      s_l[wave][e * 4 / DP] = l[v];
-    }
-  }
-  __syncthreads();
-  for (int it = threadIdx.x; it < kJoinRows * DP / 4; it += 64 * kJoinWaves) {
-    const int row = it * 4 / DP, d = it * 4 - row * DP;
-    if (row >= live || d >= c.dim) continue;
-    float mx = kNegBig, sum = 0.0f;
-    for (int u = 0; u < kJoinWaves; ++u) mx = fmaxf(mx, s_m[u][row]);
-    f32x4 y = {0, 0, 0, 0};
-    for (int u = 0; u < kJoinWaves; ++u) {
-      const float f = __builtin_amdgcn_exp2f(s_m[u][row] - mx);
-      y += s_o[u][it] * f;
-      sum += s_l[u][row] * f;
-    }
-    const int h = in.h * k.hpw + hi;
-    const float vs = f8 && c.v_scale ? c.v_scale[h] : 1.0f;
+  const int h = in.h * k.hpw + hi;
+  const float vs = f8 && c.v_scale ? c.v_scale[h] : 1.0f;
+  auto store = [&](int e, f32x4 y, float l) {  // 16 bytes e of the four rows
+    const int row = e * 4 / DP, d = e * 4 - row * DP;
+    if (row >= live || d >= c.dim) return;
     const int q = in.mt * rows + row0 + row, i = q / k.G;
+    const float f = vs / l;
     typename attend::Elem<T>::x4 z;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = (T)(y[e] / sum * vs);
+    for (int u = 0; u < 4; ++u) z[u] = (T)(y[u] * f);
     T* out = static_cast<T*>(a.out) + ((int64_t)in.r * a.blk + i) * a.out_stride +
              (int64_t)(h * k.G + (q - i * k.G)) * c.dim + d;
     *reinterpret_cast<typename attend::Elem<T>::x4*>(out) = z;
+  };
+  Sum sum;
+  sum.run(k, in, w, hi, row0, live, WIDE ? wave : 0, WIDE ? kJoinWaves : 1);
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int v = 0; v < Sum::NV; ++v) store(v * 64 + lane, sum.o[v], sum.l[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < Sum::NV; ++v) {
+      const int e = v * 64 + lane;
+      s_o[wave][e] = sum.o[v];
+      if (e * 4 % DP == 0) {
+        s_m[wave][e * 4 / DP] = sum.m[v];
+        s_l[wave][e * 4 / DP] = sum.l[v];
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kJoinRows * DP / 4; e += 64 * kJoinWaves) {
+      const int row = e * 4 / DP;
+      float mx = kNegBig, l = 0.0f;
+      for (int u = 0; u < kJoinWaves; ++u) mx = fmaxf(mx, s_m[u][row]);
+      f32x4 y = {0, 0, 0, 0};
+      for (int u = 0; u < kJoinWaves; ++u) {
+        const float f = __builtin_amdgcn_exp2f(s_m[u][row] - mx);
+        y += s_o[u][e] * f;
+        l += s_l[u][row] * f;
+      }
+      store(e, y, l);
+    }
   }
+}
+
+template <typename T, int DP>
+hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
+  const int rows = p.mt * 16, items = k.wgs * p.hpw * (p.prow / kJoinRows);
+  const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
+  const int status = k.a.status ? k.a.batch : 0;
+  // fewer jobs than a quarter of the shares: most are cut in many parts
+  if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.wgs)
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
+                   dim3(64 * kJoinWaves), 0, stream, k, rows, f8);
+  else
+    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, false>),
+                   dim3((unsigned)((items + kJoinWaves - 1) / kJoinWaves + status)),
+                   dim3(64 * kJoinWaves), 0, stream, k, rows, f8);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_join(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
-  const int rows = p.mt * 16, groups = p.hpw * (p.prow / kJoinRows);
-  const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
-  const dim3 grid((unsigned)(k.wgs * groups + (k.a.status ? k.a.batch : 0))), block(64 * kJoinWaves);
-  if (p.dp == 64)
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 64>), grid, block, 0, stream, k, rows, f8);
-  else if (p.dp == 128)
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 128>), grid, block, 0, stream, k, rows, f8);
-  else
-    PSISPEC_LAUNCH("attend_join", (k_attend_join<T, 256>), grid, block, 0, stream, k, rows, f8);
-  return hipGetLastError();
+  return p.dp == 64    ? launch_join_dp<T, 64>(k, p, stream)
+         : p.dp == 128 ? launch_join_dp<T, 128>(k, p, stream)
+                       : launch_join_dp<T, 256>(k, p, stream);
 }
 
 }  // namespace
@@ -216,7 +251,6 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.G = a.heads_q / a.c.heads;
   k.nmt = p.nmt;
   k.mask_words = p.mask_words;
-  const int rb = p.dp * (f8 ? 1 : 2);
   k.wgs = p.wgs;
   k.hpw = p.hpw;
   k.hgroups = a.c.heads / p.hpw;
@@ -225,9 +259,9 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
-  k.row_groups = a.c.page_size % (1024 / rb) == 0 && page_bytes < (int64_t(1) << 31) &&
-                 row_bytes * (a.c.page_size + 16) < (int64_t(1) << 31);
-  if (k.row_groups) {
+  k.halves = a.c.dim == p.dp && a.c.page_size % 16 == 0 && page_bytes < (int64_t(1) << 31) &&
+             row_bytes * (a.c.page_size + 16) < (int64_t(1) << 31);
+  if (k.halves) {
     k.page_bytes = (uint32_t)page_bytes;
     k.row_bytes = (uint32_t)row_bytes;
   }
