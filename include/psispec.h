@@ -353,7 +353,8 @@ typedef struct {
  *   positions  [batch][blk] int32 rotation position of each row (a tree's len + depth; any value),
  *              or NULL: len[r] + i
  *   len        [batch] int32 rows that the line holds already
- *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] are neither read nor written
+ *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] have no effect and are not
+ *              written
  *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when len < 0, n_new is outside [0, blk]
  *              or the rows do not fit the slots (nothing of the line is then written, q_out

@@ -43,14 +43,46 @@ __device__ inline u32x2 pack_e4m3(const float* x) {
   return w;
 }
 
-// T: element type of the inputs; F8: the cache holds 8-bit numbers, else T
+// T: element type of the inputs; F8: the cache holds 8-bit numbers, else T.  log_group: lanes of a head,
+// D/16 rounded up to a power of two.
 template <typename T, bool F8>
 __global__ __launch_bounds__(kAppendThreads) void k_qkv_append(AppendArgs a, int log_group) {
   typedef typename Vec8<T>::type V8;
   __shared__ float s_cos[kMaxHeadDim / 2], s_sin[kMaxHeadDim / 2];
+  const psispec_paged_cache& c = a.c;
   const int64_t row = blockIdx.x;
   const int r = (int)(row / a.blk), i = (int)(row - (int64_t)r * a.blk);
-  const psispec_paged_cache& c = a.c;
+  const int rot = a.p.rot, half = rot >> 1;
+  const int group = 1 << log_group;
+  const int u = threadIdx.x & (group - 1);
+  const bool lane_on = u < (c.dim >> 4);
+  // the lane's two chunks of 8 dimensions
+  const int rp = rot >> 4;               // lanes that hold rotated pairs
+  const bool rotated = u < rp;
+  const bool inter = (a.p.flags & PSISPEC_ROPE_INTERLEAVED) != 0;
+  int c0 = 2 * u, c1 = 2 * u + 1;
+  if (rotated && !inter) {
+    c0 = u;
+    c1 = u + rp;
+  }
+  const int heads = a.heads_q + 2 * c.heads, per_pass = kAppendThreads >> log_group;
+  const int hd0 = threadIdx.x >> log_group;
+
+  // The first heads and the frequency do not hang on the line's length: they are on their way during
+  // the chain length -> page -> place.
+  auto load = [&](int hd, V8& raw0, V8& raw1) {
+    const int kind = hd < a.heads_q ? 0 : hd < a.heads_q + c.heads ? 1 : 2;  // q, k, v
+    const int h = kind == 0 ? hd : kind == 1 ? hd - a.heads_q : hd - a.heads_q - c.heads;
+    const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                   row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
+                   (int64_t)h * c.dim;
+    raw0 = *reinterpret_cast<const V8*>(src + 8 * c0);
+    raw1 = *reinterpret_cast<const V8*>(src + 8 * c1);
+  };
+  V8 raw0 = {}, raw1 = {};
+  if (lane_on && hd0 < heads) load(hd0, raw0, raw1);
+  const double freq = (int)threadIdx.x < half ? a.p.inv_freq[threadIdx.x] : 0.0;
+
   int L, n;
   const bool ok = line_rows(a.len, a.n_new, r, a.blk, c.slots, c.page_size, &L, &n);
   const int32_t* tab = c.table + (int64_t)r * c.table_stride;
@@ -68,66 +100,45 @@ __global__ __launch_bounds__(kAppendThreads) void k_qkv_append(AppendArgs a, int
   const int slot = (L + i) / c.page_size, off = (L + i) - slot * c.page_size;
   const int page = tab[slot];
   if ((uint32_t)page >= (uint32_t)c.num_pages) return;
-
-  const int rot = a.p.rot, half = rot >> 1;
   const int pos = a.positions ? a.positions[row] : L + i;
-  for (int j = threadIdx.x; j < half; j += kAppendThreads) {
-    const double t = (double)pos * a.p.inv_freq[j] * 0.15915494309189533577;  // turns
+  if ((int)threadIdx.x < half) {  // half <= 128
+    const double t = (double)pos * freq * 0.15915494309189533577;  // turns
     float sn, cs;
     sincospif(2.0f * (float)(t - rint(t)), &sn, &cs);
-    s_cos[j] = cs * (float)a.p.rope_scale;
-    s_sin[j] = sn * (float)a.p.rope_scale;
+    s_cos[threadIdx.x] = cs * (float)a.p.rope_scale;
+    s_sin[threadIdx.x] = sn * (float)a.p.rope_scale;
   }
   __syncthreads();
 
   const int64_t at = (int64_t)page * c.page_stride + (int64_t)off * c.row_stride;
-  const int group = 1 << log_group;      // lanes of a head, D/16 rounded up to a power of two
-  const int u = threadIdx.x & (group - 1);
-  const bool lane_on = u < (c.dim >> 4);
-  // the lane's two chunks of 8 dimensions
-  const int rp = rot >> 4;               // lanes that hold rotated pairs
-  const bool rotated = u < rp;
-  const bool inter = (a.p.flags & PSISPEC_ROPE_INTERLEAVED) != 0;
-  int c0 = 2 * u, c1 = 2 * u + 1;
-  if (rotated && !inter) {
-    c0 = u;
-    c1 = u + rp;
-  }
-  const int heads = a.heads_q + 2 * c.heads;
   const float eps = (float)a.p.eps, inv_d = 1.0f / (float)c.dim;
-  for (int hd = threadIdx.x >> log_group; hd < heads; hd += kAppendThreads >> log_group) {
-    const int kind = hd < a.heads_q ? 0 : hd < a.heads_q + c.heads ? 1 : 2;  // q, k, v
+  for (int hd = hd0; hd < heads; hd += per_pass) {
+    if (hd != hd0 && lane_on) load(hd, raw0, raw1);
+    const int kind = hd < a.heads_q ? 0 : hd < a.heads_q + c.heads ? 1 : 2;
     const int h = kind == 0 ? hd : kind == 1 ? hd - a.heads_q : hd - a.heads_q - c.heads;
-    const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                   row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
-                   (int64_t)h * c.dim;
-    float x[2][8] = {};
-    V8 raw[2] = {};
-    if (lane_on) {
-      raw[0] = *reinterpret_cast<const V8*>(src + 8 * c0);
-      raw[1] = *reinterpret_cast<const V8*>(src + 8 * c1);
+    float x[2][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[0][e] = (float)raw[0][e];
-        x[1][e] = (float)raw[1][e];
-      }
+    for (int e = 0; e < 8; ++e) {
+      x[0][e] = (float)raw0[e];
+      x[1][e] = (float)raw1[e];
     }
     if (kind < 2) {
       const T* w = static_cast<const T*>(kind == 0 ? a.p.q_weight : a.p.k_weight);
       if (w) {
+        V8 w0 = {}, w1 = {};
+        if (lane_on) {
+          w0 = *reinterpret_cast<const V8*>(w + 8 * c0);
+          w1 = *reinterpret_cast<const V8*>(w + 8 * c1);
+        }
         float ss = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss += x[0][e] * x[0][e] + x[1][e] * x[1][e];
         for (int o = 1; o < group; o <<= 1) ss += __shfl_xor(ss, o, 64);
         const float inv = 1.0f / sqrtf(ss * inv_d + eps);
-        if (lane_on) {
-          const V8 w0 = *reinterpret_cast<const V8*>(w + 8 * c0);
-          const V8 w1 = *reinterpret_cast<const V8*>(w + 8 * c1);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[0][e] *= inv * (float)w0[e];
-            x[1][e] *= inv * (float)w1[e];
-          }
+        for (int e = 0; e < 8; ++e) {
+          x[0][e] *= inv * (float)w0[e];
+          x[1][e] *= inv * (float)w1[e];
         }
       }
       if (rotated) {
@@ -142,12 +153,10 @@ __global__ __launch_bounds__(kAppendThreads) void k_qkv_append(AppendArgs a, int
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {  // pairs 8u + e of the lane's 16 dimensions
-            float& p = x[e >> 2][(2 * e) & 7];
-            float& z = x[e >> 2][(2 * e + 1) & 7];
             const float cs = s_cos[8 * u + e], sn = s_sin[8 * u + e];
-            const float p0 = p, z0 = z;
-            p = p0 * cs - z0 * sn;
-            z = z0 * cs + p0 * sn;
+            const float p = x[e >> 2][(2 * e) & 7], z = x[e >> 2][(2 * e + 1) & 7];
+            x[e >> 2][(2 * e) & 7] = p * cs - z * sn;
+            x[e >> 2][(2 * e + 1) & 7] = z * cs + p * sn;
           }
         }
       }
@@ -162,8 +171,13 @@ __global__ __launch_bounds__(kAppendThreads) void k_qkv_append(AppendArgs a, int
         x[1][e] = clamp_e4m3(x[1][e] / s);
       }
       uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? c.k : c.v) + at + (int64_t)h * c.head_stride;
-      *reinterpret_cast<u32x2*>(dst + 8 * c0) = pack_e4m3(x[0]);
-      *reinterpret_cast<u32x2*>(dst + 8 * c1) = pack_e4m3(x[1]);
+      if (c1 == c0 + 1) {
+        const u32x2 lo = pack_e4m3(x[0]), hi = pack_e4m3(x[1]);
+        *reinterpret_cast<u32x4*>(dst + 8 * c0) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      } else {
+        *reinterpret_cast<u32x2*>(dst + 8 * c0) = pack_e4m3(x[0]);
+        *reinterpret_cast<u32x2*>(dst + 8 * c1) = pack_e4m3(x[1]);
+      }
       continue;
     }
     T* dst = kind == 0 ? static_cast<T*>(a.q_out) + row * a.q_out_stride + (int64_t)h * c.dim
@@ -171,12 +185,12 @@ __global__ __launch_bounds__(kAppendThreads) void k_qkv_append(AppendArgs a, int
     if (kind < 2) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        raw[0][e] = (T)x[0][e];
-        raw[1][e] = (T)x[1][e];
+        raw0[e] = (T)x[0][e];
+        raw1[e] = (T)x[1][e];
       }
     }
-    *reinterpret_cast<V8*>(dst + 8 * c0) = raw[0];
-    *reinterpret_cast<V8*>(dst + 8 * c1) = raw[1];
+    *reinterpret_cast<V8*>(dst + 8 * c0) = raw0;
+    *reinterpret_cast<V8*>(dst + 8 * c1) = raw1;
   }
 }
 

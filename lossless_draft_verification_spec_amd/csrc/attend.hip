@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
 constexpr int kJoinWaves = 4;
 
 // the parts first, first + stride, ... of rows row0 .. row0+3 (live of them)
-template <int DP> struct JoinSum {
+template <int DP, bool WIDE> struct JoinSum {
   static constexpr int NV = kJoinRows * DP / 4 / 64;  // 16-byte pieces per lane
   f32x4 o[NV];
   float m[NV], l[NV];
@@ -86,40 +86,34 @@ template <int DP> struct JoinSum {
       m[v] = kNegBig;
       l[v] = 0.0f;
     }
-    constexpr int kAhead = DP > 128 ? 4 : 8;  // parts loaded together
+    constexpr int kAhead = (WIDE ? 8 : 4) / (DP > 128 ? 2 : 1);  // parts loaded together
     for (int p0 = first; p0 < in.parts; p0 += stride * kAhead) {
       f32x4 y[kAhead][NV];
       float2 ml[kAhead][NV];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int p = p0 + stride * u;
-        if (p < in.parts) {
-          const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
-          const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
+      for (int u = 0; u < kAhead; ++u) {  // no branches: past the last part, the last again
+        const int p = min(p0 + stride * u, in.parts - 1);
+        const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
+        const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int e = (v * 64 + lane) * 4, row = e / DP;
-            if (row < live) {
-              ml[u][v] = k.ml[at + row];
-              y[u][v] = *reinterpret_cast<const f32x4*>(k.o + at * DP + e);
-            }
-          }
+        for (int v = 0; v < NV; ++v) {
+          const int e = (v * 64 + lane) * 4, row = e / DP, ok = min(row, live - 1);
+          ml[u][v] = k.ml[at + ok];
+          y[u][v] = *reinterpret_cast<const f32x4*>(k.o + (at + ok) * DP + (e - row * DP));
         }
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        if (p0 + stride * u < in.parts) {
+        const bool on = p0 + stride * u < in.parts;
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            if ((v * 64 + lane) * 4 / DP < live) {
-              const float mx = fmaxf(m[v], ml[u][v].x);
-              const float f0 = __builtin_amdgcn_exp2f(m[v] - mx);
-              const float f1 = __builtin_amdgcn_exp2f(ml[u][v].x - mx);
-              o[v] = o[v] * f0 + y[u][v] * f1;
-              l[v] = l[v] * f0 + ml[u][v].y * f1;
-              m[v] = mx;
-            }
-          }
+        for (int v = 0; v < NV; ++v) {
+          const float mx = fmaxf(m[v], ml[u][v].x);
+          const float f0 = __builtin_amdgcn_exp2f(m[v] - mx);
+          const float f1 = __builtin_amdgcn_exp2f(ml[u][v].x - mx);
+          // selected, not multiplied by zero: a part may hold infinities
+          o[v] = on ? o[v] * f0 + y[u][v] * f1 : o[v];
+          l[v] = on ? l[v] * f0 + ml[u][v].y * f1 : l[v];
+          m[v] = on ? mx : m[v];
         }
       }
     }
@@ -128,7 +122,7 @@ template <int DP> struct JoinSum {
 
 template <typename T, int DP, bool WIDE>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int f8) {
-  typedef JoinSum<DP> Sum;
+  typedef JoinSum<DP, WIDE> Sum;
   __shared__ f32x4 s_o[WIDE ? kJoinWaves : 1][kJoinRows * DP / 4];
   __shared__ float s_m[kJoinWaves][kJoinRows], s_l[kJoinWaves][kJoinRows];
   const AttendArgs& a = k.a;

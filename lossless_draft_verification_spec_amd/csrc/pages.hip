@@ -19,10 +19,13 @@ __device__ inline bool page_ok(int p, int num_pages) { return (uint32_t)p < (uin
 // ------------------------------------------------------------------------------------------------
 // commit: kept row i of line r moves from position len + keep[i] to len + i, keep strictly
 // increasing.  As in the contiguous commit the move is in place and safe in increasing i: a thread
-// owns a 16-byte slice of every row, and the source of every later row lies behind row i.  One
-// slice per thread; rows already in place are dropped from the list that the block builds in LDS.
+// owns a few 16-byte slices of every row, and the source of every later row lies behind row i.  Rows
+// already in place are dropped from the list that the block builds in LDS.  Bound by HBM for large
+// batches, by the chain count -> list -> pages -> rows for small ones.
 // ------------------------------------------------------------------------------------------------
 constexpr int kCommitBatch = 8;       // rows loaded before they are stored
+constexpr int kCommitSlices = 2;      // 16-byte slices of a row per thread (1 slice: 87 us for 256 lines,
+                                      // 2: 44, 4: 45, 8: 51)
 
 struct Move {
   int64_t src, dst;  // byte offsets within a plane
@@ -65,7 +68,9 @@ __device__ inline int commit_check(const PagedCommitArgs& a, int r, int* s_keep,
   return any_bad ? PSISPEC_ST_BAD_KEEP : any_page ? PSISPEC_ST_BAD_PAGE : 0;
 }
 
-__global__ __launch_bounds__(kPgThreads) void k_paged_commit(PagedCommitArgs a, int ntiles) {
+// with_len: tile 0 writes the line's status and new length, which must not be `len` itself then.
+__global__ __launch_bounds__(kPgThreads) void k_paged_commit(PagedCommitArgs a, int ntiles,
+                                                             int with_len) {
   extern __shared__ char smem[];
   __shared__ int s_cnt;
   Move* s_mv = reinterpret_cast<Move*>(smem);
@@ -73,24 +78,50 @@ __global__ __launch_bounds__(kPgThreads) void k_paged_commit(PagedCommitArgs a, 
   const int r = blockIdx.x / ntiles;
   const int tile = blockIdx.x - r * ntiles;
   int moves;
-  if (commit_check(a, r, s_keep, s_mv, &s_cnt, &moves) || moves == 0) return;
+  const int st = commit_check(a, r, s_keep, s_mv, &s_cnt, &moves);
   const int n = a.n_keep[r];
-  const int64_t per_plane = a.pool.row_bytes / 16;
-  const int64_t s = (int64_t)tile * kPgThreads + threadIdx.x;
-  if (s >= per_plane * a.pool.planes) return;
-  const int64_t w = s / per_plane;
-  char* base = static_cast<char*>(a.pool.base) + w * a.pool.plane_stride + (s - w * per_plane) * 16;
+  if (with_len && tile == 0 && threadIdx.x == 0) {
+    const int L = a.len[r];
+    a.new_len[r] = st ? L : L + n;
+    if (a.status) a.status[r] = st;
+  }
+  if (st || moves == 0) return;
+  const int64_t per_plane = a.pool.row_bytes / 16, all = per_plane * a.pool.planes;
+  int64_t s = (int64_t)tile * kPgThreads * kCommitSlices + threadIdx.x;
+  char* base[kCommitSlices];
+  bool on[kCommitSlices];
+#pragma unroll
+  for (int k = 0; k < kCommitSlices; ++k, s += kPgThreads) {
+    on[k] = s < all;
+    const int64_t w = (on[k] ? s : 0) / per_plane;
+    base[k] = static_cast<char*>(a.pool.base) + w * a.pool.plane_stride +
+              ((on[k] ? s : 0) - w * per_plane) * 16;
+  }
   for (int i0 = n - moves; i0 < n; i0 += kCommitBatch) {  // the moving rows are the last ones
-    u32x4 v[kCommitBatch] = {};
+    u32x4 v[kCommitBatch][kCommitSlices] = {};
 #pragma unroll
-    for (int u = 0; u < kCommitBatch; ++u)
-      if (i0 + u < n) v[u] = *reinterpret_cast<const u32x4*>(base + s_mv[i0 + u].src);
+    for (int u = 0; u < kCommitBatch; ++u) {
+      if (i0 + u < n) {
+        const int64_t src = s_mv[i0 + u].src;
 #pragma unroll
-    for (int u = 0; u < kCommitBatch; ++u)
-      if (i0 + u < n) *reinterpret_cast<u32x4*>(base + s_mv[i0 + u].dst) = v[u];
+        for (int k = 0; k < kCommitSlices; ++k)
+          if (on[k]) v[u][k] = *reinterpret_cast<const u32x4*>(base[k] + src);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kCommitBatch; ++u) {
+      if (i0 + u < n) {
+        const int64_t dst = s_mv[i0 + u].dst;
+#pragma unroll
+        for (int k = 0; k < kCommitSlices; ++k)
+          if (on[k]) *reinterpret_cast<u32x4*>(base[k] + dst) = v[u][k];
+      }
+    }
   }
 }
 
+// New lengths and status alone: no row moves, or the new lengths overwrite the old ones, which every
+// block of the move reads.
 __global__ __launch_bounds__(64) void k_paged_len(PagedCommitArgs a) {
   extern __shared__ char smem[];
   __shared__ int s_cnt;
@@ -110,37 +141,56 @@ __global__ __launch_bounds__(64) void k_paged_len(PagedCommitArgs a) {
 // assign: line r becomes the first new_len[r] positions of the old line src[r].
 // ------------------------------------------------------------------------------------------------
 
-// Workgroup r: the line's new entries into the workspace and the changes of the counts (integer
-// adds: the sums do not depend on their order).
-__global__ __launch_bounds__(kPgThreads) void k_assign_count(AssignArgs a, int32_t* newtab,
-                                                             int32_t* newlen) {
-  const int r = blockIdx.x;
+// Line r by `threads` threads (all of a workgroup's barriers are shared by its lines): the new entries
+// into the workspace and the changes of the counts (integer adds: the sums do not depend on their
+// order).
+struct AssignLine {
+  const int32_t *from, *old;
+  int32_t* out;
+  int cut, want;
+  bool bad;
+};
+__device__ inline AssignLine assign_begin(const AssignArgs& a, int32_t* newtab, int r, int tid,
+                                          int threads) {
+  AssignLine l;
   const int src = a.src[r];
-  const int want = src == -1 ? 0 : a.new_len[r];
-  bool bad = src < -1 || src >= a.batch || want < 0;
-  int cut = 0;
-  if (!bad && src >= 0) {
-    bad = want > a.len[src] || (int64_t)want > (int64_t)a.slots * a.page_size;
-    cut = bad ? 0 : (int)(((int64_t)want + a.page_size - 1) / a.page_size);
+  l.want = src == -1 ? 0 : a.new_len[r];
+  l.bad = src < -1 || src >= a.batch || l.want < 0;
+  l.cut = 0;
+  if (!l.bad && src >= 0) {
+    l.bad = l.want > a.len[src] || (int64_t)l.want > (int64_t)a.slots * a.page_size;
+    l.cut = l.bad ? 0 : (int)(((int64_t)l.want + a.page_size - 1) / a.page_size);
   }
-  const int32_t* from = a.table + (int64_t)(bad || src < 0 ? r : src) * a.table_stride;
-  const int32_t* old = a.table + (int64_t)r * a.table_stride;
-  for (int s = threadIdx.x; s < cut; s += kPgThreads) bad |= !page_ok(from[s], a.num_pages);
-  bad = __syncthreads_or(bad);
-  int32_t* out = newtab + (int64_t)r * a.slots;
-  for (int s = threadIdx.x; s < a.slots; s += kPgThreads) {
-    const int o = old[s];
-    const int e = bad ? o : s < cut ? from[s] : -1;
-    out[s] = e;
+  l.from = a.table + (int64_t)(l.bad || src < 0 ? r : src) * a.table_stride;
+  l.old = a.table + (int64_t)r * a.table_stride;
+  l.out = newtab + (int64_t)r * a.slots;
+  for (int s = tid; s < l.cut; s += threads) l.bad |= !page_ok(l.from[s], a.num_pages);
+  return l;
+}
+__device__ inline void assign_entries(const AssignArgs& a, const AssignLine& l, bool bad, int32_t* newlen,
+                                      int r, int tid, int threads) {
+  for (int s = tid; s < a.slots; s += threads) {
+    const int o = l.old[s];
+    const int e = bad ? o : s < l.cut ? l.from[s] : -1;
+    l.out[s] = e;
     if (e != o) {
       if (page_ok(e, a.num_pages)) atomicAdd(&a.refs[e], 1);
       if (page_ok(o, a.num_pages)) atomicSub(&a.refs[o], 1);
     }
   }
-  if (threadIdx.x == 0) {
-    newlen[r] = bad ? a.len[r] : want;
+  if (tid == 0) {
+    newlen[r] = bad ? a.len[r] : l.want;
     if (a.status) a.status[r] = bad ? PSISPEC_ST_BAD_PAGE : 0;
   }
+}
+
+// One workgroup per line, then k_assign_write: a line's old entries are read by others.
+__global__ __launch_bounds__(kPgThreads) void k_assign_count(AssignArgs a, int32_t* newtab,
+                                                             int32_t* newlen) {
+  const int r = blockIdx.x;
+  const AssignLine l = assign_begin(a, newtab, r, threadIdx.x, kPgThreads);
+  const bool bad = __syncthreads_or(l.bad);
+  assign_entries(a, l, bad, newlen, r, threadIdx.x, kPgThreads);
 }
 
 __global__ __launch_bounds__(kPgThreads) void k_assign_write(AssignArgs a, const int32_t* newtab,
@@ -149,6 +199,28 @@ __global__ __launch_bounds__(kPgThreads) void k_assign_write(AssignArgs a, const
   for (int s = threadIdx.x; s < a.slots; s += kPgThreads)
     a.table[(int64_t)r * a.table_stride + s] = newtab[(int64_t)r * a.slots + s];
   if (threadIdx.x == 0) a.len[r] = newlen[r];
+}
+
+// Few lines in one launch (4 lines: 4.5 us against 4.5 + 4.4 in two): one workgroup, a wave per line, a
+// barrier between the reads of the old tables and the writes of the new ones.  A wave with several
+// lines takes them one after the other (128 lines: 23 us against 4.3 + 4.3), so there is at most one
+// each, of a few entries per lane.
+constexpr int kOneBlock = 1024;
+constexpr int kSmallLines = kOneBlock / 64;
+constexpr int kSmallEntries = 256;
+__global__ __launch_bounds__(kOneBlock) void k_assign_small(AssignArgs a, int32_t* newtab,
+                                                            int32_t* newlen) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
+    const AssignLine l = assign_begin(a, newtab, r, lane, 64);
+    assign_entries(a, l, __any(l.bad), newlen, r, lane, 64);
+  }
+  __syncthreads();
+  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
+    for (int s = lane; s < a.slots; s += 64)
+      a.table[(int64_t)r * a.table_stride + s] = newtab[(int64_t)r * a.slots + s];
+    if (lane == 0) a.len[r] = newlen[r];
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -179,6 +251,7 @@ __device__ inline int block_excl_sum(int x, int* s, int* total) {
 
 struct ReserveWs {
   int32_t* need;   // [batch] pages that the line needs; -1: invalid
+  int32_t* first;  // [batch] pages that the lines before it need; -1: the free ones do not reach it
   int32_t* take;   // [batch][J] per slot: kNoNeed, -1 (no page there) or the shared page to replace
   int32_t* cnt;    // [chunks] free pages per chunk
   int32_t* ids;    // [batch * J] the free pages to hand out, in order
@@ -194,37 +267,46 @@ __device__ inline int block_sum_of(const int32_t* x, int n, int* s) {
   return total;
 }
 
+// What line r needs in slot j from its first touched slot on (m of them): w.take[r][j], 1 if a page.
+__device__ inline int reserve_slot(const ReserveArgs& a, const ReserveWs& w, int r, int j, int s0, int m,
+                                   int L, bool* bad) {
+  const int np = a.pool.num_pages;
+  int t = kNoNeed;
+  if (j < m) {
+    const int p = a.table[(int64_t)r * a.table_stride + s0 + j];
+    // a slot that already holds rows of the line must have its page
+    *bad |= p >= np || (p < 0 && j == 0 && L > s0 * a.pool.page_size);
+    t = p < 0 ? -1 : page_ok(p, np) && a.refs[p] > 1 ? p : kNoNeed;
+  }
+  w.take[(int64_t)r * w.J + j] = t;
+  return t != kNoNeed;
+}
+__device__ inline bool reserve_span(const ReserveArgs& a, int r, int* L, int* s0, int* m) {
+  int rows;
+  const bool ok = line_rows(a.len, a.n_new, r, a.blk, a.slots, a.pool.page_size, L, &rows);
+  *s0 = ok ? *L / a.pool.page_size : 0;
+  *m = ok && rows > 0 ? (*L + rows - 1) / a.pool.page_size - *s0 + 1 : 0;
+  return ok;
+}
+
 // Block r < batch: what line r needs.  Block batch + c: the number of free pages in chunk c.
 __global__ __launch_bounds__(kPgThreads) void k_reserve_plan(ReserveArgs a, ReserveWs w) {
   __shared__ int s_sum[4];
-  const int np = a.pool.num_pages, ps = a.pool.page_size;
   int n = 0, total;
   if ((int)blockIdx.x >= a.batch) {
     const int c = blockIdx.x - a.batch;
     for (int k = threadIdx.x; k < kScanChunk; k += kPgThreads) {
       const int p = c * kScanChunk + k;
-      n += p < np && a.refs[p] == 0;
+      n += p < a.pool.num_pages && a.refs[p] == 0;
     }
     block_excl_sum(n, s_sum, &total);
     if (threadIdx.x == 0) w.cnt[c] = total;
     return;
   }
   const int r = blockIdx.x;
-  int L, rows;
-  bool bad = !line_rows(a.len, a.n_new, r, a.blk, a.slots, ps, &L, &rows);
-  const int s0 = bad ? 0 : L / ps;
-  const int m = bad || rows == 0 ? 0 : (L + rows - 1) / ps - s0 + 1;
-  for (int j = threadIdx.x; j < w.J; j += kPgThreads) {
-    int t = kNoNeed;
-    if (j < m) {
-      const int p = a.table[(int64_t)r * a.table_stride + s0 + j];
-      // a slot that already holds rows of the line must have its page
-      bad |= p >= np || (p < 0 && j == 0 && L > s0 * ps);
-      t = p < 0 ? -1 : page_ok(p, np) && a.refs[p] > 1 ? p : kNoNeed;
-    }
-    w.take[(int64_t)r * w.J + j] = t;
-    n += t != kNoNeed;
-  }
+  int L, s0, m;
+  bool bad = !reserve_span(a, r, &L, &s0, &m);
+  for (int j = threadIdx.x; j < w.J; j += kPgThreads) n += reserve_slot(a, w, r, j, s0, m, L, &bad);
   block_excl_sum(n, s_sum, &total);
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) w.need[r] = bad ? -1 : total;
@@ -235,6 +317,17 @@ __global__ __launch_bounds__(kPgThreads) void k_reserve_ids(ReserveArgs a, Reser
   __shared__ int s_sum[4];
   const int c = blockIdx.x;
   const int want = block_sum_of(w.need, a.batch, s_sum);
+  if (c == 0) {
+    const int avail = block_sum_of(w.cnt, w.chunks, s_sum);
+    int base = 0, total;
+    for (int r0 = 0; r0 < a.batch; r0 += kPgThreads) {
+      const int r = r0 + threadIdx.x;
+      const int need = r < a.batch ? max(w.need[r], 0) : 0;
+      const int first = base + block_excl_sum(need, s_sum, &total);
+      if (r < a.batch) w.first[r] = need == 0 || first + need <= avail ? first : -1;
+      base += total;
+    }
+  }
   const int before = block_sum_of(w.cnt, c, s_sum);
   if (before >= want) return;
   int n;
@@ -257,6 +350,60 @@ __global__ __launch_bounds__(kPgThreads) void k_reserve_ids(ReserveArgs a, Reser
   }
 }
 
+// Both for a pool of one chunk and few lines in one launch: one workgroup.
+__global__ __launch_bounds__(kOneBlock) void k_reserve_small(ReserveArgs a, ReserveWs w) {
+  __shared__ int s_free[kOneBlock / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
+    int L, s0, m, n = 0;
+    bool bad = !reserve_span(a, r, &L, &s0, &m);
+    for (int j = lane; j < w.J; j += 64) n += reserve_slot(a, w, r, j, s0, m, L, &bad);
+    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+    bad = __any(bad);
+    if (lane == 0) w.need[r] = bad ? -1 : n;
+  }
+  constexpr int kPer = kScanChunk / kOneBlock;
+  const int p0 = threadIdx.x * kPer;
+  bool fr[kPer];
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    fr[k] = p0 + k < a.pool.num_pages && a.refs[p0 + k] == 0;
+    mine += fr[k];
+  }
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 63) s_free[wave] = inc;
+  __syncthreads();
+  int at = inc - mine, all = 0;
+  for (int v = 0; v < kOneBlock / 64; ++v) {
+    at += v < wave ? s_free[v] : 0;
+    all += s_free[v];
+  }
+  const int cap = a.batch * w.J;  // room in ids: no call needs more
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (fr[k]) {
+      if (at < cap) w.ids[at] = p0 + k;
+      ++at;
+    }
+  }
+  if (wave == 0) {  // batch <= 64
+    const int need = lane < a.batch ? max(w.need[lane], 0) : 0;
+    int sum = need;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += y;
+    }
+    if (lane < a.batch) w.first[lane] = need == 0 || sum <= all ? sum - need : -1;
+  }
+}
+
 // Workgroup (r, tile): tile 0 writes the line's entries, counts and status; every tile copies its
 // part of the shared tail page.
 constexpr int kCopyLoads = 4;
@@ -268,10 +415,8 @@ __global__ __launch_bounds__(kPgThreads) void k_reserve_apply(ReserveArgs a, Res
   const int tiles = tiles_per_plane * a.pool.planes;
   const int r = blockIdx.x / tiles;
   const int tile = blockIdx.x - r * tiles;
-  const int need = w.need[r];
-  const int first = block_sum_of(w.need, r, s_sum);
-  const int avail = block_sum_of(w.cnt, w.chunks, s_sum);
-  const bool served = need == 0 || (need > 0 && first + need <= avail);
+  const int need = w.need[r], first = w.first[r];
+  const bool served = first >= 0;
   if (tile == 0 && threadIdx.x == 0 && a.status)
     a.status[r] = need < 0 ? PSISPEC_ST_BAD_PAGE : served ? 0 : PSISPEC_ST_NO_PAGE;
   if (need <= 0 || !served) return;
@@ -327,20 +472,23 @@ size_t pages_workspace_bytes(int batch, int slots, int num_pages, int blk, int p
   const size_t J = reserve_slots(blk, page_size, slots);
   const size_t chunks = ((size_t)num_pages + kScanChunk - 1) / kScanChunk;
   if (chunks > kMaxChunks || batch * J > (size_t)1 << 30) return 0;
-  const size_t reserve = up256(sizeof(int32_t) * batch) +
+  const size_t reserve = 2 * up256(sizeof(int32_t) * batch) +
                          2 * up256(sizeof(int32_t) * batch * J) + up256(sizeof(int32_t) * chunks);
   return (assign > reserve ? assign : reserve) + 256;
 }
 
 hipError_t launch_paged_commit(const PagedCommitArgs& a, hipStream_t stream) {
   const int64_t slices = a.pool.planes * (a.pool.row_bytes / 16);
-  const int ntiles = (int)((slices + kPgThreads - 1) / kPgThreads);
+  const int per = kPgThreads * kCommitSlices;
+  const int ntiles = (int)((slices + per - 1) / per);
   const size_t shm = a.blk * (sizeof(Move) + sizeof(int));
+  // the two arrays of lengths apart: one launch
+  const int apart = a.new_len + a.batch <= a.len || a.len + a.batch <= a.new_len;
   if (a.keep) {  // without a list the kept rows are in place
     PSISPEC_LAUNCH("paged_commit", k_paged_commit, dim3((unsigned)((int64_t)a.batch * ntiles)),
-                   dim3(kPgThreads), shm, stream, a, ntiles);
+                   dim3(kPgThreads), shm, stream, a, ntiles, apart);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || apart) return e;
   }
   PSISPEC_LAUNCH("paged_len", k_paged_len, dim3((unsigned)a.batch), dim3(64), shm, stream, a);
   return hipGetLastError();
@@ -350,6 +498,10 @@ hipError_t launch_pages_assign(const AssignArgs& a, void* workspace, hipStream_t
   int32_t* newtab = static_cast<int32_t*>(workspace);
   int32_t* newlen = reinterpret_cast<int32_t*>(
       static_cast<char*>(workspace) + up256(sizeof(int32_t) * (size_t)a.batch * a.slots));
+  if (a.batch <= kSmallLines && a.slots <= kSmallEntries) {
+    PSISPEC_LAUNCH("assign_small", k_assign_small, dim3(1), dim3(kOneBlock), 0, stream, a, newtab, newlen);
+    return hipGetLastError();
+  }
   PSISPEC_LAUNCH("assign_count", k_assign_count, dim3((unsigned)a.batch), dim3(kPgThreads), 0, stream,
                  a, newtab, newlen);
   const hipError_t e = hipGetLastError();
@@ -370,15 +522,21 @@ hipError_t launch_pages_reserve(const ReserveArgs& a, void* workspace, hipStream
     return p;
   };
   w.need = carve(a.batch);
+  w.first = carve(a.batch);
   w.take = carve((size_t)a.batch * w.J);
   w.ids = carve((size_t)a.batch * w.J);
   w.cnt = carve(w.chunks);
-  PSISPEC_LAUNCH("reserve_plan", k_reserve_plan, dim3((unsigned)(a.batch + w.chunks)), dim3(kPgThreads), 0,
-                 stream, a, w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  PSISPEC_LAUNCH("reserve_ids", k_reserve_ids, dim3((unsigned)w.chunks), dim3(kPgThreads), 0, stream,
-                 a, w);
+  hipError_t e;
+  if (w.chunks == 1 && a.batch <= kSmallLines && w.J <= kSmallEntries) {
+    PSISPEC_LAUNCH("reserve_small", k_reserve_small, dim3(1), dim3(kOneBlock), 0, stream, a, w);
+  } else {
+    PSISPEC_LAUNCH("reserve_plan", k_reserve_plan, dim3((unsigned)(a.batch + w.chunks)),
+                   dim3(kPgThreads), 0, stream, a, w);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    PSISPEC_LAUNCH("reserve_ids", k_reserve_ids, dim3((unsigned)w.chunks), dim3(kPgThreads), 0, stream,
+                   a, w);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tpp = (int)((a.pool.page_size * a.pool.row_bytes + kCopyTile - 1) / kCopyTile);
