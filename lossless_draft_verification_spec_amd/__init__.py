@@ -9,8 +9,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -552,50 +554,84 @@ _PAGED_DTYPES = {torch.bfloat16: PSISPEC_BF16, torch.float16: PSISPEC_F16,
                  torch.float8_e4m3fn: PSISPEC_F8E4M3}
 
 
-def _on(dev, stream):
+class _On:
     """The guard under which a call on `dev` allocates and launches: `dev` current and, when a stream
-    is given, that stream (which must be one of `dev`'s)."""
-    if stream is not None:
-        if stream.device != dev:
-            raise PsispecError(f"stream is on {stream.device}, expected {dev}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != dev.index:
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    is given, that stream (which must be one of `dev`'s).  None where nothing has to change."""
+
+    @staticmethod
+    def guard(dev, stream):
+        if stream is not None:
+            if stream.device != dev:
+                raise PsispecError(f"stream is on {stream.device}, expected {dev}")
+            return torch.cuda.stream(stream)
+        if torch.cuda.current_device() != dev.index:
+            return torch.cuda.device(dev)
+        return _NOTHING
 
 
-def _int32(t: torch.Tensor, shape, dev, name: str) -> int:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise PsispecError(f"{name} must be int32 {list(shape)}")
-    _same_dev(t, dev, name)
-    return _dev(t, name)
+_NOTHING = contextlib.nullcontext()
+_CACHE_STRUCT = struct.Struct("5Q4q6i")  # psispec_paged_cache
+_PREP_STRUCT = struct.Struct("3Q2diI")   # psispec_qkv_prep
+_POOL_STRUCT = struct.Struct("Q3q4i")    # psispec_page_pool
+
+
+def _dev_stream(dev):
+    """dev's current stream as a raw pointer."""
+    return _raw_stream(dev.index) if _raw_stream is not None else _stream(None)
+
+
+def _gpu_device(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise PsispecError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    return t.device
+
+
+def _flat(t, shape, dtype, dev, name):
+    """Pointer of a contiguous tensor of exactly this shape and type on dev; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != dev.index or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise PsispecError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
+        _dev(t, name)
+        _same_dev(t, dev, name)
+    return t.data_ptr()
 
 
 def _table(table: torch.Tensor, batch: int, dev):
     """(pointer, row stride, slots) of a page table [batch][slots]; rows contiguous."""
-    if table.dim() != 2 or table.shape[0] != batch or table.dtype != torch.int32:
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch:
         raise PsispecError("table must be int32 [batch][slots]")
-    if not table.is_cuda:
-        raise PsispecError("table must be a GPU tensor (the library has no CPU path)")
-    _same_dev(table, dev, "table")
+    if table.get_device() != dev.index:
+        _gpu_device(table, "table")
+        _same_dev(table, dev, "table")
     slots = table.shape[1]
-    stride = table.stride(0) if batch > 1 else max(slots, 1)
-    if slots < 1 or (slots > 1 and table.stride(1) != 1) or stride < slots:
-        raise PsispecError("table rows must be contiguous and not overlap")
+    if table.is_contiguous():
+        stride = slots
+    else:
+        stride = table.stride(0) if batch > 1 else slots
+        if (slots > 1 and table.stride(1) != 1) or stride < slots:
+            raise PsispecError("table rows must be contiguous and not overlap")
+    if slots < 1:
+        raise PsispecError("table must have a slot at least")
     return table.data_ptr(), stride, slots
 
 
 def _token_rows(t: torch.Tensor, name: str, dtype, dev):
     """(pointer, elements from one token row to the next) of [batch][blk][heads][dim], whose heads and
     dims are contiguous within a row and whose rows are evenly spaced."""
-    if t.dim() != 4:
-        raise PsispecError(f"{name} must be [batch][blk][heads][dim]")
-    if not t.is_cuda:
-        raise PsispecError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    _same_dev(t, dev, name)
+    if t.get_device() != dev.index:
+        _gpu_device(t, name)
+        _same_dev(t, dev, name)
     if t.dtype != dtype:
         raise PsispecError(f"{name} must be {dtype}, got {t.dtype}")
-    (b, n, h, d), st = t.shape, t.stride()
+    shape = t.shape
+    if len(shape) != 4:
+        raise PsispecError(f"{name} must be [batch][blk][heads][dim]")
+    b, n, h, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
+    st = t.stride()
     rows = st[1] if n > 1 else st[0] if b > 1 else h * d
     if (st[3] != 1 or (h > 1 and st[2] != d) or (n > 1 and b > 1 and st[0] != n * rows)
             or rows < h * d):
@@ -603,56 +639,61 @@ def _token_rows(t: torch.Tensor, name: str, dtype, dev):
     return t.data_ptr(), rows
 
 
-def _scale_ptr(t, heads, dev, name):
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or tuple(t.shape) != (heads,):
-        raise PsispecError(f"{name} must be float32 [heads]")
-    _same_dev(t, dev, name)
-    return _dev(t, name)
-
-
 def _paged_cache(k_cache, v_cache, table, batch, dtype, dev, k_scale, v_scale):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    """(psispec_paged_cache as bytes, heads, dim)."""
+    shape, ct = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise PsispecError("k_cache and v_cache must be [pages][page_size][heads][dim]")
+    if v_cache.dtype != ct or (ct != dtype and ct != torch.float8_e4m3fn):
+        raise PsispecError(f"k_cache and v_cache must be {dtype} or torch.float8_e4m3fn, got {ct} and "
+                           f"{v_cache.dtype}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda:
-            raise PsispecError(f"{name} must be a GPU tensor (the library has no CPU path)")
-        _same_dev(t, dev, name)
-        if t.dtype != k_cache.dtype or t.dtype not in (dtype, torch.float8_e4m3fn):
-            raise PsispecError(f"{name} must be {dtype} or torch.float8_e4m3fn, got {t.dtype}")
-    pages, ps, heads, dim = k_cache.shape
-    # an extent of 1 has no stride of its own
-    sk, sv = ([s if n > 1 else dim for s, n in zip(t.stride(), t.shape)] for t in (k_cache, v_cache))
-    if sk != sv or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        if t.get_device() != dev.index:
+            _gpu_device(t, name)
+            _same_dev(t, dev, name)
+    pages, ps, heads, dim = shape
+    sk, sv = k_cache.stride(), v_cache.stride()
+    if 1 in shape:  # an extent of 1 has no stride of its own
+        sk, sv = ([x if n > 1 else dim if i < 3 else 1 for i, (x, n) in enumerate(zip(s, shape))]
+                  for s in (sk, sv))
+    if sk != sv or sk[3] != 1:
         raise PsispecError("k_cache and v_cache must have the same strides, the last one 1")
-    if (k_scale is not None or v_scale is not None) and k_cache.dtype != torch.float8_e4m3fn:
+    if (k_scale is not None or v_scale is not None) and ct != torch.float8_e4m3fn:
         raise PsispecError("k_scale and v_scale go with a float8_e4m3fn cache")
     tp, ts, slots = _table(table, batch, dev)
-    return psispec_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(),
-                               _scale_ptr(k_scale, heads, dev, "k_scale"),
-                               _scale_ptr(v_scale, heads, dev, "v_scale"), tp, sk[0], sk[1], sk[2],
-                               ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[k_cache.dtype])
+    return _CACHE_STRUCT.pack(k_cache.data_ptr(), v_cache.data_ptr(),
+                              _flat(k_scale, (heads,), torch.float32, dev, "k_scale"),
+                              _flat(v_scale, (heads,), torch.float32, dev, "v_scale"), tp, sk[0], sk[1],
+                              sk[2], ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[ct]), heads, dim
 
 
 def _page_pool(pool: torch.Tensor):
-    if pool.dim() < 4:
+    """(psispec_page_pool as bytes, pages, page_size)."""
+    shape = pool.shape
+    if len(shape) < 4:
         raise PsispecError("pool must be [planes][pages][page_size][...]")
-    if not pool.is_cuda:
-        raise PsispecError("pool must be a GPU tensor (the library has no CPU path)")
-    planes, pages, ps = pool.shape[:3]
-    es, row = pool.element_size(), 1
-    for n, st in zip(reversed(pool.shape[3:]), reversed(pool.stride()[3:])):
-        if n > 1 and st != row:
-            raise PsispecError("a row of pool (its dimensions after the first three) must be contiguous")
-        row *= n
-    if ps > 1 and pool.stride(2) != row:
-        raise PsispecError("the rows of a page of pool must be contiguous")
-    page = pool.stride(1) if pages > 1 else ps * row
-    plane = pool.stride(0) if planes > 1 else pages * page
-    if planes > 1 and plane < row or min(plane, page) < 0:
-        raise PsispecError("the planes of pool must not overlap")
-    return psispec_page_pool(pool.data_ptr(), plane * es, page * es, row * es, planes, pages, ps, 0)
+    _gpu_device(pool, "pool")
+    planes, pages, ps = shape[:3]
+    es = pool.element_size()
+    if pool.is_contiguous():
+        row = 1
+        for n in shape[3:]:
+            row *= n
+        page = ps * row
+        plane = pages * page
+    else:
+        row, st = 1, pool.stride()
+        for n, x in zip(reversed(shape[3:]), reversed(st[3:])):
+            if n > 1 and x != row:
+                raise PsispecError("a row of pool (its dimensions after the first three) must be contiguous")
+            row *= n
+        if ps > 1 and st[2] != row:
+            raise PsispecError("the rows of a page of pool must be contiguous")
+        page = st[1] if pages > 1 else ps * row
+        plane = st[0] if planes > 1 else pages * page
+        if min(plane, page) < row:
+            raise PsispecError("the planes and pages of pool must not overlap")
+    return _POOL_STRUCT.pack(pool.data_ptr(), plane * es, page * es, row * es, planes, pages, ps, 0), pages, ps
 
 
 def _workspace_for(workspace, need, dev, what):
@@ -660,8 +701,8 @@ def _workspace_for(workspace, need, dev, what):
         raise PsispecError(f"unsupported sizes for {what}")
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    if (not workspace.is_cuda or workspace.device != dev or workspace.dtype != torch.uint8
-            or not workspace.is_contiguous() or workspace.numel() < need):
+    if (workspace.get_device() != dev.index or workspace.dtype != torch.uint8
+            or workspace.numel() < need or not workspace.is_contiguous()):
         raise PsispecError(f"workspace must be a contiguous uint8 tensor on {dev} with at least "
                            f"{need} elements")
     return workspace
@@ -723,50 +764,43 @@ def psispec_qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cach
     rope_frequencies), positions int32 [batch][blk] or length + i.  Row i of line r goes to position
     length[r] + i; rows i >= n_new[r] (int32 [batch]) are left out.  Returns q_out (allocated when not
     given; q itself rotates in place)."""
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise PsispecError("q must be [batch][blk][heads_q][dim]")
-    batch, blk, hq, dim = q.shape
-    dev, dt = q.device, q.dtype
-    if dt not in (torch.bfloat16, torch.float16):
+    batch, blk, hq, dim = shape
+    dev, dt = _gpu_device(q, "q"), q.dtype
+    if dt != torch.bfloat16 and dt != torch.float16:
         raise PsispecError(f"q must be bfloat16 or float16, got {dt}")
     qp, qs = _token_rows(q, "q", dt, dev)
     kp, ks = _token_rows(k, "k", dt, dev)
     vp, vs = _token_rows(v, "v", dt, dev)
-    c = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
-    if k.shape != v.shape or tuple(k.shape) != (batch, blk, c.heads, dim) or c.dim != dim:
+    c, heads, cdim = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
+    if k.shape != v.shape or k.shape != (batch, blk, heads, dim) or cdim != dim:
         raise PsispecError("k and v must be [batch][blk][heads][dim] with the cache's heads and q's dim")
-    wp = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            if w.dtype != dt or tuple(w.shape) != (dim,):
-                raise PsispecError(f"{name} must be {dt} [dim]")
-            _same_dev(w, dev, name)
-        wp.append(None if w is None else _dev(w, name))
-    fp, rot = None, 0
+    fp, rot = 0, 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-            raise PsispecError("inv_freq must be float64 [rot/2]")
-        _same_dev(inv_freq, dev, "inv_freq")
-        fp, rot = _dev(inv_freq, "inv_freq"), 2 * inv_freq.numel()
-    lp = _int32(length, (batch,), dev, "length")
-    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
-    pp = None if positions is None else _int32(positions, (batch, blk), dev, "positions")
-    sp = None if status is None else _int32(status, (batch,), dev, "status")
-    prep = psispec_qkv_prep(wp[0], wp[1], fp, float(eps), float(rope_scale), rot,
-                            PSISPEC_ROPE_INTERLEAVED if interleaved else 0)
-    with _on(dev, stream):
+        rot = 2 * inv_freq.numel()
+        fp = _flat(inv_freq, (rot // 2,), torch.float64, dev, "inv_freq")
+    prep = _PREP_STRUCT.pack(_flat(q_weight, (dim,), dt, dev, "q_weight"),
+                             _flat(k_weight, (dim,), dt, dev, "k_weight"), fp, eps, rope_scale, rot,
+                             PSISPEC_ROPE_INTERLEAVED if interleaved else 0)
+    lp = _flat(length, (batch,), torch.int32, dev, "length")
+    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    pp = _flat(positions, (batch, blk), torch.int32, dev, "positions")
+    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    with _On.guard(dev, stream):
         if q_out is None:
-            q_out = torch.empty((batch, blk, hq, dim), dtype=dt, device=dev)
-        elif tuple(q_out.shape) != (batch, blk, hq, dim):
+            q_out = torch.empty(shape, dtype=dt, device=dev)
+        elif q_out.shape != shape:
             raise PsispecError("q_out must have the shape of q")
         op, os_ = _token_rows(q_out, "q_out", dt, dev)
-        rc = lib().psispec_qkv_append(ctypes.byref(c), ctypes.byref(prep), qp, qs, kp, ks, vp, vs,
-                                      _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_, op, os_, sp,
-                                      _stream(None))
+        rc = lib().psispec_qkv_append(c, prep, qp, qs, kp, ks, vp, vs, _PAGED_DTYPES[dt], batch, blk, hq,
+                                      pp, lp, np_, op, os_, sp, _dev_stream(dev))
     _check(rc, "psispec_qkv_append")
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
 def paged_attention_workspace_bytes(batch, blk, heads_q, heads_kv, dim) -> int:
     return int(lib().psispec_paged_attention_workspace(batch, blk, heads_q, heads_kv, dim))
 
@@ -784,34 +818,35 @@ def psispec_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     the rows before them.  Row i sees those, and of the block rows 0..i, or itself and its ancestors
     under parent (int32 [batch][blk], -1 = none).  Rows i >= n_new[r] of out are left as they are (a
     new out starts unspecified there).  scale defaults to dim ** -0.5."""
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise PsispecError("q must be [batch][blk][heads_q][dim]")
-    batch, blk, hq, dim = q.shape
-    dev, dt = q.device, q.dtype
-    if dt not in (torch.bfloat16, torch.float16):
+    batch, blk, hq, dim = shape
+    dev, dt = _gpu_device(q, "q"), q.dtype
+    if dt != torch.bfloat16 and dt != torch.float16:
         raise PsispecError(f"q must be bfloat16 or float16, got {dt}")
     qp, qs = _token_rows(q, "q", dt, dev)
-    c = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
-    if c.dim != dim:
+    c, heads, cdim = _paged_cache(k_cache, v_cache, table, batch, dt, dev, k_scale, v_scale)
+    if cdim != dim:
         raise PsispecError("q and the cache must have the same dim")
-    lp = _int32(length, (batch,), dev, "length")
-    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
-    pp = None if parent is None else _int32(parent, (batch, blk), dev, "parent")
-    sp = None if status is None else _int32(status, (batch,), dev, "status")
-    with _on(dev, stream):
+    lp = _flat(length, (batch,), torch.int32, dev, "length")
+    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    pp = _flat(parent, (batch, blk), torch.int32, dev, "parent")
+    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    with _On.guard(dev, stream):
         if out is None:
-            out = torch.empty((batch, blk, hq, dim), dtype=dt, device=dev)
-        elif tuple(out.shape) != (batch, blk, hq, dim):
+            out = torch.empty(shape, dtype=dt, device=dev)
+        elif out.shape != shape:
             raise PsispecError("out must have the shape of q")
         op, os_ = _token_rows(out, "out", dt, dev)
         workspace = _workspace_for(workspace,
-                                   paged_attention_workspace_bytes(batch, blk, hq, c.heads, dim), dev,
+                                   paged_attention_workspace_bytes(batch, blk, hq, heads, dim), dev,
                                    "psispec_paged_attention (blk 1..1024, heads_q a multiple of the "
                                    "cache's heads, dim a multiple of 16 up to 256)")
         rc = lib().psispec_paged_attention(
-            ctypes.byref(c), qp, qs, _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_,
-            dim ** -0.5 if scale is None else float(scale), op, os_, sp, workspace.data_ptr(),
-            workspace.numel(), _stream(None))
+            c, qp, qs, _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_,
+            dim ** -0.5 if scale is None else scale, op, os_, sp, workspace.data_ptr(),
+            workspace.numel(), _dev_stream(dev))
     _check(rc, "psispec_paged_attention")
     return out
 
@@ -825,26 +860,28 @@ def psispec_paged_commit(pool: torch.Tensor, table: torch.Tensor, length: torch.
     keep[r][:n_keep[r]] of the block at length[r] move to length[r] onwards in every plane, and
     new_length (length itself when not given) becomes length + n_keep.  Returns `status` (int32
     [batch], ST_BAD_KEEP or ST_BAD_PAGE for an invalid line, which stays as it is) when given."""
-    batch, dev = length.shape[0] if length.dim() == 1 else -1, pool.device
-    c = _page_pool(pool)
-    lp = _int32(length, (batch,), dev, "length")
+    dev = _gpu_device(pool, "pool")
+    batch = length.numel()
+    c, _, _ = _page_pool(pool)
+    lp = _flat(length, (batch,), torch.int32, dev, "length")
     tp, ts, slots = _table(table, batch, dev)
-    kp = _int32(n_keep, (batch,), dev, "n_keep")
-    np_ = lp if new_length is None else _int32(new_length, (batch,), dev, "new_length")
-    sp = None if status is None else _int32(status, (batch,), dev, "status")
-    ks, keepp = 0, None
+    kp = _flat(n_keep, (batch,), torch.int32, dev, "n_keep")
+    np_ = lp if new_length is None else _flat(new_length, (batch,), torch.int32, dev, "new_length")
+    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    ks, keepp = 0, 0
     if keep is not None:
         if keep.dim() != 2:
             raise PsispecError("keep must be int32 [batch][k]")
         ks = keep.shape[1]
-        keepp = _int32(keep, (batch, ks), dev, "keep")
-    with _on(dev, stream):
-        rc = lib().psispec_paged_commit(ctypes.byref(c), tp, ts, slots, batch, int(blk), keepp, ks, kp,
-                                        lp, np_, sp, _stream(None))
+        keepp = _flat(keep, (batch, ks), torch.int32, dev, "keep")
+    with _On.guard(dev, stream):
+        rc = lib().psispec_paged_commit(c, tp, ts, slots, batch, int(blk), keepp, ks, kp, lp, np_, sp,
+                                        _dev_stream(dev))
     _check(rc, "psispec_paged_commit")
     return status
 
 
+@functools.lru_cache(maxsize=4096)
 def pages_workspace_bytes(batch, slots, num_pages, blk, page_size) -> int:
     return int(lib().psispec_pages_workspace(batch, slots, num_pages, blk, page_size))
 
@@ -858,21 +895,21 @@ def psispec_pages_assign(table: torch.Tensor, refs: torch.Tensor, length: torch.
     [batch][slots], refs int32 [pages] (table entries that name each page; 0 = free) and length int32
     [batch] are updated in place.  Returns `status` (ST_BAD_PAGE for an invalid line, which stays as
     it is) when given."""
-    batch, dev = length.shape[0] if length.dim() == 1 else -1, table.device
-    lp = _int32(length, (batch,), dev, "length")
+    dev = _gpu_device(table, "table")
+    batch = length.numel()
+    lp = _flat(length, (batch,), torch.int32, dev, "length")
     tp, ts, slots = _table(table, batch, dev)
-    if refs.dim() != 1:
-        raise PsispecError("refs must be int32 [pages]")
-    rp = _int32(refs, tuple(refs.shape), dev, "refs")
-    srcp, nlp = _int32(src, (batch,), dev, "src"), _int32(new_length, (batch,), dev, "new_length")
-    sp = None if status is None else _int32(status, (batch,), dev, "status")
-    with _on(dev, stream):
-        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, refs.shape[0], 1,
+    pages = refs.numel()
+    rp = _flat(refs, (pages,), torch.int32, dev, "refs")
+    srcp = _flat(src, (batch,), torch.int32, dev, "src")
+    nlp = _flat(new_length, (batch,), torch.int32, dev, "new_length")
+    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    with _On.guard(dev, stream):
+        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, pages, 1,
                                                                     int(page_size)), dev,
                                    "psispec_pages_assign")
-        rc = lib().psispec_pages_assign(tp, ts, slots, rp, refs.shape[0], int(page_size), lp, srcp, nlp,
-                                        sp, batch, workspace.data_ptr(), workspace.numel(),
-                                        _stream(None))
+        rc = lib().psispec_pages_assign(tp, ts, slots, rp, pages, int(page_size), lp, srcp, nlp, sp,
+                                        batch, workspace.data_ptr(), workspace.numel(), _dev_stream(dev))
     _check(rc, "psispec_pages_assign")
     return status
 
@@ -886,19 +923,19 @@ def psispec_pages_reserve(pool: torch.Tensor, table: torch.Tensor, refs: torch.T
     [planes][pages][page_size][...], as in psispec_paged_commit).  table and refs are updated in place.
     Returns `status` when given: ST_NO_PAGE for a line that the free pages did not reach, ST_BAD_PAGE
     for an invalid one; such lines stay as they are."""
-    batch, dev = length.shape[0] if length.dim() == 1 else -1, pool.device
-    c = _page_pool(pool)
-    lp = _int32(length, (batch,), dev, "length")
+    dev = _gpu_device(pool, "pool")
+    batch = length.numel()
+    c, pages, ps = _page_pool(pool)
+    lp = _flat(length, (batch,), torch.int32, dev, "length")
     tp, ts, slots = _table(table, batch, dev)
-    rp = _int32(refs, (c.num_pages,), dev, "refs")
-    np_ = None if n_new is None else _int32(n_new, (batch,), dev, "n_new")
-    sp = None if status is None else _int32(status, (batch,), dev, "status")
-    with _on(dev, stream):
-        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, c.num_pages, int(blk),
-                                                                    c.page_size), dev,
+    rp = _flat(refs, (pages,), torch.int32, dev, "refs")
+    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    with _On.guard(dev, stream):
+        workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, pages, int(blk), ps), dev,
                                    "psispec_pages_reserve")
-        rc = lib().psispec_pages_reserve(ctypes.byref(c), tp, ts, slots, rp, lp, np_, int(blk), sp,
-                                         batch, workspace.data_ptr(), workspace.numel(), _stream(None))
+        rc = lib().psispec_pages_reserve(c, tp, ts, slots, rp, lp, np_, int(blk), sp, batch,
+                                         workspace.data_ptr(), workspace.numel(), _dev_stream(dev))
     _check(rc, "psispec_pages_reserve")
     return status
 
