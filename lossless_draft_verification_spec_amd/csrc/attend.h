@@ -52,15 +52,16 @@ constexpr int kNonTemporal = 2;
 // beside its steps.  Workgroups are dealt to the 8 XCDs in turn; each XCD gets a contiguous run of
 // shares, so that the row groups and heads that read the same pages meet in one L2.  Of the two
 // workgroups on a CU the one launched later is slower by a seventh, so the shares of the first half
-// of an XCD's workgroups are larger (34 : 30).  More, smaller shares given out as places become free
-// even out the rest, and lose more than that to joining.
+// of an XCD's workgroups are larger (34 : 30), except below two units a share, where the small ones
+// could be empty: a job's parts lie in shares one behind the other.  More, smaller shares given out as
+// places become free even out the rest, and lose more than that to joining.
 constexpr int kXcds = 8;
 __host__ __device__ inline int64_t share_of_block(int64_t shares, int R, int b) {
   return shares < R ? b : (int64_t)(b % kXcds) * (R / kXcds) + b / kXcds;
 }
 __host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int64_t w) {
   if (shares < R) return w;
-  const int64_t per = R / kXcds, h = per / 2, first = R > kAttendCUs ? 34 : 32;
+  const int64_t per = R / kXcds, h = per / 2, first = R > kAttendCUs && all >= 2 * R ? 34 : 32;
   const int64_t x = w / per, j = w - x * per;
   const int64_t at = j < h ? first * j : first * h + (64 - first) * (j - h);
   return all * (x * 64 * h + at) / (kXcds * 64 * h);

@@ -164,6 +164,20 @@ def test_attend_batch_of_one_long_line():
     _check_attend(_case([20011], 1, 8, 1, 128, 64, BF, F8, seed=12))
 
 
+@pytest.mark.parametrize("dim,dtype,cache,L", [(64, FH, FH, 67400), (128, BF, F8, 68600), (192, BF, BF, 33200)])
+def test_attend_about_one_unit_of_work_per_share(dim, dtype, cache, L):
+    """One job over a few more units than there are workgroups: a share without any would leave a part
+    that nothing wrote to the join."""
+    c = _case([L], 1, 2, 1, dim, 64, dtype, cache, seed=dim)
+    ws = torch.full((paged_attention_workspace_bytes(1, 1, 2, 1, dim),), 255, dtype=torch.uint8, device=DEV)
+    for cut in (0, 500, 1700, 2047):
+        c["lens"] = torch.tensor([L - cut], dtype=torch.int32)
+        _check_attend(c)
+        ws.fill_(255)
+        want = _attend(c)
+        assert torch.equal(_attend(c, workspace=ws), want)
+
+
 @pytest.mark.parametrize("dtype", [BF, FH])
 def test_attend_peaked_and_flat_scores(dtype):
     """Scores of +-hundreds (one position takes all the weight, the maximum rises late) and all 0."""
