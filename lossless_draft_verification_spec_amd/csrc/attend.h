@@ -99,6 +99,7 @@ struct AttendPlan {
 struct AttendKernelArgs {
   AttendArgs a;
   int G, nmt, mask_words, wgs;
+  int step_tiles;            // tiles of each wave in a step
   int job_cost;              // units of a job beside its steps
   int hpw, hgroups;          // heads per workgroup (1 or 4), groups of them
   int prow;                  // rows of a part in the workspace
@@ -147,7 +148,7 @@ template <> struct Elem<__bf16> {
   typedef __bf16 x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 x4 __attribute__((ext_vector_type(4)));
   typedef __bf16 x8 __attribute__((ext_vector_type(8)));
-  static constexpr uint32_t kExp = 0x7f80u;
+  static constexpr uint32_t kExpStep = 0x00800080u;
   __device__ static f32x4 mfma(x8 a, x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -162,7 +163,7 @@ template <> struct Elem<_Float16> {
   typedef _Float16 x2 __attribute__((ext_vector_type(2)));
   typedef _Float16 x4 __attribute__((ext_vector_type(4)));
   typedef _Float16 x8 __attribute__((ext_vector_type(8)));
-  static constexpr uint32_t kExp = 0x7c00u;
+  static constexpr uint32_t kExpStep = 0x04000400u;
   __device__ static f32x4 mfma(x8 a, x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
@@ -217,17 +218,14 @@ __device__ inline typename Elem<T>::x8 widen(uint32_t w0, uint32_t w1) {
 
 // all ones in the places of a word's finite elements, zeros in those of NaN and infinities
 template <typename T, bool F8> __device__ inline uint32_t finite_mask(uint32_t w) {
-  uint32_t m = ~0u;
+  // adding one step of the exponent (8 bits: of the whole number) carries out of all ones
   if constexpr (F8) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (((w >> (8 * b)) & 0x7fu) == 0x7fu) m &= ~(0xffu << (8 * b));
+    const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return ~((m >> 7) * 0xffu);
   } else {
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      if (((w >> (16 * b)) & Elem<T>::kExp) == Elem<T>::kExp) m &= ~(0xffffu << (16 * b));
+    const uint32_t m = ((w & 0x7fff7fffu) + Elem<T>::kExpStep) & 0x80008000u;
+    return ~((m >> 15) * 0xffffu);
   }
-  return m;
 }
 
 // Wait until at most units * UNIT loads are outstanding (units wave-uniform, at most MAX).
@@ -290,9 +288,9 @@ __device__ inline int64_t block_scan(int64_t x, int64_t* s, int64_t* total) {
   return before + inc - x;
 }
 
-// steps of job group mt of a line: a step is one tile of each wave
+// steps of job group mt of a line: a step is step_tiles tiles of each wave
 __device__ inline int job_steps(const AttendKernelArgs& k, int keys) {
-  const int step = kAttendTile * kAttendWaves / k.hpw;
+  const int step = kAttendTile * kAttendWaves / k.hpw * k.step_tiles;
   return (keys + step - 1) / step;
 }
 __device__ inline int64_t line_units(const AttendKernelArgs& k, int r, int rows) {
@@ -434,8 +432,8 @@ void k_attend(AttendKernelArgs k) {
         if (step0 >= step1) continue;
         const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
         const int splits = kAttendWaves / k.hpw;  // waves that share a head's positions
-        const int tile0 = step0 * splits;
-        const int tile1 = min(step1 * splits, ntiles);
+        const int tile0 = step0 * splits * k.step_tiles;
+        const int tile1 = min(step1 * splits * k.step_tiles, ntiles);
         const int cnt = tile1 - tile0;
         const int t0 = k.hpw == 1 ? tile0 + cnt * wave / kAttendWaves : tile0;
         const int t1 = k.hpw == 1 ? tile0 + cnt * (wave + 1) / kAttendWaves : tile1;
@@ -469,28 +467,38 @@ void k_attend(AttendKernelArgs k) {
           const int lane_row = lane / CPR;
           const int swz = is_v() ? swz_v<RB, F8>(lane_row) : swz_k<RB>(lane_row);
           const int lane_chunk = (lane % CPR) ^ swz;
-          if (k.halves && tile_pos + kAttendTile <= keys) {
-            // whole tile, each 16 positions of it in one page: two scalar addresses
+          if (k.halves) {
+            // each 16 positions of the tile lie in one page: two scalar addresses
+            const int lim = keys - 1 + 64 * ps - chunk_end;
+            const bool part = tile_pos + kAttendTile > keys;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const uint32_t rel = rel0 + 16 * half;
+              const uint32_t rel = min(rel0 + 16 * half, lim);
               const uint32_t idx = __umulhi(rel, k.ps_magic);
               const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(tab_now, idx);
               const char* const at0 =
                   from + (uint64_t)page * k.page_bytes + (rel - idx * ps) * k.row_bytes;
-              auto rows = [&](auto policy) {
+              auto rows = [&](auto policy, auto is_part) {
                 const char* at = at0;
 #pragma unroll
                 for (int i = half * NLD / 2; i < (half + 1) * NLD / 2; ++i) {
                   const int ch = lane_chunk ^ (is_v() ? swz_v<RB, F8>(i * RPI) : swz_k<RB>(i * RPI));
-                  load_lds<decltype(policy)::value>(at + (lane_ofs + (ch << 4)), to + i * 1024);
-                  at += RPI * k.row_bytes;
+                  if constexpr (decltype(is_part)::value) {
+                    const int row = min((i - half * NLD / 2) * RPI + lane_row, lim - (int)rel);
+                    load_lds<decltype(policy)::value>(at0 + ((uint32_t)row * k.row_bytes + (ch << 4)),
+                                                      to + i * 1024);
+                  } else {
+                    load_lds<decltype(policy)::value>(at + (lane_ofs + (ch << 4)), to + i * 1024);
+                    at += RPI * k.row_bytes;
+                  }
                 }
               };
-              if (k.nmt > 1)
-                rows(std::integral_constant<int, 0>{});
+              if (part)
+                rows(std::integral_constant<int, 0>{}, std::true_type{});
+              else if (k.nmt > 1)
+                rows(std::integral_constant<int, 0>{}, std::false_type{});
               else
-                rows(std::integral_constant<int, kNonTemporal>{});
+                rows(std::integral_constant<int, kNonTemporal>{}, std::false_type{});
             }
           } else {
             const int lim = keys - 1 + 64 * ps - chunk_end;
@@ -689,19 +697,19 @@ void k_attend(AttendKernelArgs k) {
             // (rare) become 0 here and are added at the end, to the rows that see them.
 #pragma unroll
             for (int i = 0; i < NLD; ++i) {
+              if (pos0 + (i + 1) * RPI <= L) continue;
               char* const at = vt + i * 1024 + lane * 16;
               const int pos = pos0 + i * RPI + lane / CPR;
-              u32x4 v = {0, 0, 0, 0};
-              if (pos < keys) v = lds_read<u32x4>(at);
-              if (pos >= L) {
+              u32x4 v = lds_read<u32x4>(at);
+              uint32_t lost = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t keep = finite_mask<T, F8>(v[e]);
-                  odd |= keep != ~0u;
-                  v[e] &= keep;
-                }
-                *reinterpret_cast<u32x4*>(at) = v;
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t keep = pos >= keys ? 0u : pos >= L ? finite_mask<T, F8>(v[e]) : ~0u;
+                lost |= pos < keys ? ~keep : 0u;
+                v[e] &= keep;
               }
+              odd |= lost != 0;
+              *reinterpret_cast<u32x4*>(at) = v;
             }
             wait_lds();
           }

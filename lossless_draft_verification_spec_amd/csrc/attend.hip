@@ -9,6 +9,14 @@ using attend::f32x4;
 
 constexpr int kJoinRows = 4;
 
+// Lines of tables up to this width (positions) are not cut: nothing is joined and the second launch goes.
+// Kernels' time uncut against cut and joined: 9 rows of 8 heads 19.1 against 22.8 us at 250 positions, 21.5
+// against 22.6 at 500, 25.0 against 22.8 at 750; 16 lines of one row 18.4 against 20.3 at 500.  One
+// line of one row is cut sooner (heads in fours leave its waves alone with their positions): 14.0
+// against 14.3 at 250, 16.3 against 15.1 at 500.
+constexpr int64_t kWholePositions = 512, kWholeFewPositions = 256;
+constexpr int kFewHeads = 64;
+
 // Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
 // the instantiated sizes allow (each group reads every key and value again), then the smallest
 // size that holds a group: rows that pad a tile cost matrix work.  The largest sizes are those with
@@ -121,14 +129,15 @@ template <int DP, bool WIDE> struct JoinSum {
 };
 
 template <typename T, int DP, bool WIDE>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int f8) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int items,
+                                                              int f8) {
   typedef JoinSum<DP, WIDE> Sum;
   __shared__ f32x4 s_o[WIDE ? kJoinWaves : 1][kJoinRows * DP / 4];
   __shared__ float s_m[kJoinWaves][kJoinRows], s_l[kJoinWaves][kJoinRows];
   const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int quads = k.prow / kJoinRows, items = k.wgs * k.hpw * quads;
+  const int quads = k.prow / kJoinRows;
   const int item_blocks = WIDE ? items : (items + kJoinWaves - 1) / kJoinWaves;
   if ((int)blockIdx.x >= item_blocks) {
     const int r = blockIdx.x - item_blocks;
@@ -207,26 +216,27 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
 }
 
 template <typename T, int DP>
-hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
-  const int rows = p.mt * 16, items = k.wgs * p.hpw * (p.prow / kJoinRows);
+hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, bool whole,
+                          hipStream_t stream) {
+  const int rows = p.mt * 16, items = whole ? 0 : k.wgs * k.hpw * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
   const int status = k.a.status ? k.a.batch : 0;
   // fewer jobs than a quarter of the shares: most are cut in many parts
   if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.wgs)
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
-                   dim3(64 * kJoinWaves), 0, stream, k, rows, f8);
+                   dim3(64 * kJoinWaves), 0, stream, k, rows, items, f8);
   else
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, false>),
                    dim3((unsigned)((items + kJoinWaves - 1) / kJoinWaves + status)),
-                   dim3(64 * kJoinWaves), 0, stream, k, rows, f8);
+                   dim3(64 * kJoinWaves), 0, stream, k, rows, items, f8);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_join(const AttendKernelArgs& k, const AttendPlan& p, hipStream_t stream) {
-  return p.dp == 64    ? launch_join_dp<T, 64>(k, p, stream)
-         : p.dp == 128 ? launch_join_dp<T, 128>(k, p, stream)
-                       : launch_join_dp<T, 256>(k, p, stream);
+hipError_t launch_join(const AttendKernelArgs& k, const AttendPlan& p, bool whole, hipStream_t stream) {
+  return p.dp == 64    ? launch_join_dp<T, 64>(k, p, whole, stream)
+         : p.dp == 128 ? launch_join_dp<T, 128>(k, p, whole, stream)
+                       : launch_join_dp<T, 256>(k, p, whole, stream);
 }
 
 }  // namespace
@@ -246,10 +256,16 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.nmt = p.nmt;
   k.mask_words = p.mask_words;
   k.wgs = p.wgs;
-  k.hpw = p.hpw;
-  k.hgroups = a.c.heads / p.hpw;
+  // Short lines: a job is one step, so no border cuts it.
+  const int64_t most = (int64_t)a.c.slots * a.c.page_size;
+  const bool few = p.hpw > 1 && (int64_t)a.batch * a.c.heads <= kFewHeads;
+  const bool whole = most <= (few ? kWholeFewPositions : kWholePositions);
+  k.hpw = whole ? 1 : p.hpw;
+  k.hgroups = a.c.heads / k.hpw;
   k.prow = p.prow;
-  k.job_cost = p.hpw > 1 ? 1 : 3;
+  const int step = kAttendTile * kAttendWaves;
+  k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
+  k.job_cost = whole ? 0 : k.hpw > 1 ? 1 : 3;
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
@@ -277,7 +293,9 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   else
     e = f8 ? launch_attend_f16_f8(k, p.dp, p.mt, stream) : launch_attend_f16(k, p.dp, p.mt, stream);
   if (e != hipSuccess) return e;
-  return dtype == PSISPEC_BF16 ? launch_join<__bf16>(k, p, stream) : launch_join<_Float16>(k, p, stream);
+  if (whole && !a.status) return hipSuccess;
+  return dtype == PSISPEC_BF16 ? launch_join<__bf16>(k, p, whole, stream)
+                               : launch_join<_Float16>(k, p, whole, stream);
 }
 
 }  // namespace psispec

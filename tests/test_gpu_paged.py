@@ -178,6 +178,47 @@ def test_attend_about_one_unit_of_work_per_share(dim, dtype, cache, L):
         assert torch.equal(_attend(c, workspace=ws), want)
 
 
+@pytest.mark.parametrize("dim,rows", [(64, 16), (64, 30), (64, 50), (64, 90), (128, 8), (128, 32), (128, 42),
+                                      (128, 60), (256, 16), (256, 26), (256, 50)])
+@pytest.mark.parametrize("hkv", [3, 4])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, F8), (FH, F8)])
+def test_attend_row_groups(dim, rows, hkv, dtype, cache):
+    """Every number of row tiles at lines of many tiles per wave, heads alone and in fours; twice the same
+    bits."""
+    c = _case([1555, 40, 777], rows // 2, 2 * hkv, hkv, dim, 16, dtype, cache, seed=rows + hkv)
+    _check_attend(c)
+    assert torch.equal(_attend(c), _attend(c))
+
+
+@pytest.mark.parametrize("slots", [15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("blk,hkv", [(1, 4), (9, 4), (9, 1)])
+def test_attend_short_tables(slots, blk, hkv):
+    """Full lines of tables about as wide as those that are not cut, with and without a status."""
+    L = slots * 16 - blk
+    c = _case([L, 0, L - 200], blk, 4 * hkv, hkv, 128, 16, BF, BF, seed=slots)
+    assert c["table"].shape[1] == slots
+    _check_attend(c)
+    st = torch.full((3,), -1, dtype=torch.int32, device=DEV)
+    assert torch.equal(_attend(c), _attend(c, status=st)) and (st == 0).all()
+
+
+@pytest.mark.parametrize("hkv", [3, 4])
+def test_attend_values_that_are_not_finite_in_cut_lines(hkv):
+    """NaN and infinities in block rows of lines that several workgroups share."""
+    c = _case([3000, 2000], 3, 2 * hkv, hkv, 128, 16, BF, BF, seed=hkv, live=[3, 2])
+    want = _attend(c).cpu()
+    for r, L in ((0, 3000), (1, 2000)):
+        for j, bad in ((1, float("inf")), (2, float("nan"))):
+            at = c["table"][r, (L + j) // 16].long(), (L + j) % 16
+            c["v"][at][..., :hkv, 7] = bad
+    got = _attend(c).cpu()
+    assert torch.equal(got[0, 0], want[0, 0]) and torch.equal(got[1, 0], want[1, 0])
+    other = [d for d in range(128) if d != 7]
+    assert torch.equal(got[0, :, :, other], want[0, :, :, other])
+    assert torch.isinf(got[0, 1, :, 7]).all() and torch.isinf(got[1, 1, :, 7]).all()
+    assert torch.isnan(got[0, 2, :, 7]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, FH])
 def test_attend_peaked_and_flat_scores(dtype):
     """Scores of +-hundreds (one position takes all the weight, the maximum rises late) and all 0."""
