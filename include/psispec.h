@@ -355,14 +355,16 @@ typedef struct {
  *   len        [batch] int32 rows that the line holds already
  *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] have no effect and are not
  *              written
- *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride
+ *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride, and
+ *              overlaps no input otherwise
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when len < 0, n_new is outside [0, blk]
  *              or the rows do not fit the slots (nothing of the line is then written, q_out
  *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a
  *              page are then not written, q_out included)
  *   blk 1..2^20;  batch >= 0 (0 launches nothing);  heads_q >= 1
- * The pages written must be the line's own (psispec_pages_reserve sees to it): rows of two lines
- * in one page position race.  Asynchronous on `stream`; no workspace.
+ * No two (page, position, head) of the cache share an element.  The pages written must be the line's
+ * own (psispec_pages_reserve sees to it): rows of two lines in one page position race.
+ * Asynchronous on `stream`; no workspace.
  */
 psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qkv_prep* p,
                                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -382,9 +384,10 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
  * Products of the matrix cores in the inputs' type with 32-bit sums; softmax statistics in 32 bits;
  * weights enter the second product as a pair of 16-bit numbers (relative error 2^-16), so out is as
  * exact as its own rounding.  A position that a row does not see has no effect on it, whatever the
- * cache holds there.
+ * cache holds there.  Infinities among what it sees give infinities or NaN.
  *   q, out     row (r, i) at (r * blk + i) * stride elements: heads_q heads of c->dim contiguous
- *              elements; dtype PSISPEC_BF16 or PSISPEC_F16; 16-byte aligned, strides multiples of 8
+ *              elements; dtype PSISPEC_BF16 or PSISPEC_F16; 16-byte aligned, strides multiples of 8;
+ *              out overlaps no input
  *   parent     [batch][blk] int32: the block row that row j follows, -1 = the line's last position;
  *              must be < j.  NULL: row j follows row j-1
  *   len, n_new as in psispec_qkv_append; rows i >= n_new[r] of out are left as they are
@@ -429,7 +432,7 @@ typedef struct {
  *   table      [batch][table_stride] int32, the first `slots` entries of a row used
  *   blk, keep, keep_stride, n_keep   as in psispec_kv_commit (blk 1..1024)
  *   len        [batch] int32 with len + blk <= slots * page_size
- *   new_len    [batch] int32; may be len itself
+ *   new_len    [batch] int32; len itself, or apart from it
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_KEEP as in psispec_kv_commit,
  *              PSISPEC_ST_BAD_PAGE when a page of the rows that move is not in 0..num_pages-1;
  *              nothing of such a line moves and its length stays

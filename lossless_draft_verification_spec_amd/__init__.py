@@ -870,8 +870,8 @@ def psispec_paged_commit(pool: torch.Tensor, table: torch.Tensor, length: torch.
     sp = _flat(status, (batch,), torch.int32, dev, "status")
     ks, keepp = 0, 0
     if keep is not None:
-        if keep.dim() != 2:
-            raise PsispecError("keep must be int32 [batch][k]")
+        if keep.dim() != 2 or keep.shape[1] < 1:
+            raise PsispecError("keep must be int32 [batch][k], k at least 1")
         ks = keep.shape[1]
         keepp = _flat(keep, (batch, ks), torch.int32, dev, "keep")
     with _On.guard(dev, stream):

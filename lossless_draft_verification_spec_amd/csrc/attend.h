@@ -389,7 +389,7 @@ void k_attend(AttendKernelArgs k) {
     s_line = tid;
     s_base = at0;
   }
-  for (int r0 = kAttendThreads; base <= x; r0 += kAttendThreads) {
+  for (int r0 = kAttendThreads; base <= x && r0 < a.batch; r0 += kAttendThreads) {
     const int64_t mine = r0 + tid < a.batch ? line_units(k, r0 + tid, ROWS) : 0;
     int64_t part;
     const int64_t at = base + block_scan(mine, s_scan, &part);
@@ -406,11 +406,11 @@ void k_attend(AttendKernelArgs k) {
   char* const my_ring = ring + wave * Sh::kRing;
   bool first_segment = true;
 
-  for (;; ++r) {  // lines of the share
+  for (; r < a.batch; ++r) {  // lines of the share
     int L, n;
     const bool live_line =
         line_rows(a.len, a.n_new, r, a.blk, c.slots, ps, &L, &n) && n > 0;
-    if (!live_line) continue;  // cannot run past the batch: units are left
+    if (!live_line) continue;
     const int32_t* const tab = c.table + (int64_t)r * c.table_stride;
     for (int hg = 0; hg < k.hgroups && x < x_end; ++hg) {
       const int h = hg * k.hpw + (k.hpw == 1 ? 0 : wave);

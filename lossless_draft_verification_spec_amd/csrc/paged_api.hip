@@ -3,6 +3,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <utility>
+
 #include "paged.h"
 
 using namespace psispec;
@@ -26,12 +28,42 @@ psispec_status check_cache(const psispec_paged_cache* c, psispec_dtype dtype) {
     return PSISPEC_EINVAL;
   if (c->heads < 1 || c->heads > kMaxHeads || c->dim < 16 || c->dim > kMaxHeadDim || c->dim % 16)
     return PSISPEC_EINVAL;
-  const int64_t es = c->dtype == PSISPEC_F8E4M3 ? 1 : 2;
-  if (c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0 || (c->page_stride * es) % 16 ||
+  const int64_t es = c->dtype == PSISPEC_F8E4M3 ? 1 : 2, most = int64_t(1) << 60;
+  if (c->page_stride > most || c->row_stride > most || c->head_stride > most || c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0 || (c->page_stride * es) % 16 ||
       (c->row_stride * es) % 16 || (c->head_stride * es) % 16)
     return PSISPEC_EINVAL;
   if (c->dtype != PSISPEC_F8E4M3 && (c->k_scale || c->v_scale)) return PSISPEC_EINVAL;
   return PSISPEC_OK;
+}
+
+// No two (page, position, head) share an element: from the smallest stride on, each is at least what
+// the ones before it span.
+bool places_apart(const psispec_paged_cache* c) {
+  int64_t stride[3] = {c->head_stride, c->row_stride, c->page_stride};
+  int64_t count[3] = {c->heads, c->page_size, c->num_pages};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (stride[j] < stride[i]) {
+        std::swap(stride[i], stride[j]);
+        std::swap(count[i], count[j]);
+      }
+  __int128 span = c->dim;
+  for (int i = 0; i < 3; ++i) {
+    if (count[i] == 1) continue;
+    if (stride[i] < span) return false;
+    span += (__int128)stride[i] * (count[i] - 1);
+  }
+  return true;
+}
+
+// Rows of `width` elements, n of them, at two places: some element is in both.  Rows of equal stride
+// may lie between each other (two parts of one packed projection).
+bool rows_overlap(const void* a, int64_t sa, const void* b, int64_t sb, int64_t n, int64_t width) {
+  const __int128 d = ((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / 2;
+  if (d >= (__int128)sa * (n - 1) + width || -d >= (__int128)sb * (n - 1) + width) return false;
+  if (sa != sb) return true;
+  const int64_t m = (int64_t)((d % sa + sa) % sa);
+  return m < width || sa - m < width;
 }
 
 bool cache_pointers_ok(const psispec_paged_cache* c) {
@@ -73,10 +105,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
   if (e != PSISPEC_OK) return e;
   if (batch < 0 || blk < 1 || blk > kMaxAppendBlock || heads_q < 1 || heads_q > kMaxHeads || !p)
     return PSISPEC_EINVAL;
-  // two rows of a line may not share their place
-  if (c->head_stride < c->dim && c->heads > 1) return PSISPEC_EINVAL;
-  if ((c->row_stride < c->dim && c->page_size > 1) || (c->page_stride < c->dim && c->num_pages > 1))
-    return PSISPEC_EINVAL;
+  if (!places_apart(c)) return PSISPEC_EINVAL;
   if (!(p->eps >= 0.0) || !isfinite(p->eps) || !isfinite(p->rope_scale) || p->rot < 0 ||
       p->rot > c->dim || p->rot % 16 || (p->flags & ~PSISPEC_ROPE_INTERLEAVED) ||
       (p->rot > 0 && !p->inv_freq) || !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16))
@@ -87,6 +116,9 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
   const int64_t wq = (int64_t)heads_q * c->dim, wk = (int64_t)c->heads * c->dim;
   if (!rows_ok(q, q_stride, wq) || !rows_ok(k, k_stride, wk) || !rows_ok(v, v_stride, wk) ||
       !rows_ok(q_out, q_out_stride, wq))
+    return PSISPEC_EINVAL;
+  const int64_t rows = (int64_t)batch * blk;
+  if (!(q_out == q && q_out_stride == q_stride) && rows_overlap(q, q_stride, q_out, q_out_stride, rows, wq))
     return PSISPEC_EINVAL;
   AppendArgs a{};
   a.c = *c;
@@ -135,7 +167,8 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
     return PSISPEC_EINVAL;
   if (batch == 0) return PSISPEC_OK;
   const int64_t wq = (int64_t)heads_q * c->dim;
-  if (!cache_pointers_ok(c) || !len || !rows_ok(q, q_stride, wq) || !rows_ok(out, out_stride, wq))
+  if (!cache_pointers_ok(c) || !len || !rows_ok(q, q_stride, wq) || !rows_ok(out, out_stride, wq) ||
+      rows_overlap(q, q_stride, out, out_stride, (int64_t)batch * blk, wq))
     return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attend_workspace_bytes(batch, blk, heads_q, c->heads, c->dim))
@@ -176,6 +209,7 @@ psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t
   if (batch == 0) return PSISPEC_OK;
   if (!pool->base || !aligned(pool->base, 16) || !table || !n_keep || !len || !new_len)
     return PSISPEC_EINVAL;
+  if (new_len != len && new_len < len + batch && len < new_len + batch) return PSISPEC_EINVAL;
   PagedCommitArgs a{};
   a.pool = *pool;
   a.table = table;
@@ -195,7 +229,7 @@ psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t
 
 static size_t pages_ws(int32_t batch, int32_t slots, int32_t num_pages, int32_t blk,
                        int32_t page_size) {
-  if (batch < 0 || batch > (1 << 24) || slots < 1 || num_pages < 1 || blk < 1 ||
+  if (batch < 0 || batch > (1 << 23) || slots < 1 || num_pages < 1 || blk < 1 ||
       blk > kMaxAppendBlock || page_size < 1 || page_size > kMaxPageSize ||
       (int64_t)slots * page_size > kMaxPositions)
     return 0;

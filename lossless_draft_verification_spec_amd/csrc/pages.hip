@@ -483,7 +483,7 @@ hipError_t launch_paged_commit(const PagedCommitArgs& a, hipStream_t stream) {
   const int ntiles = (int)((slices + per - 1) / per);
   const size_t shm = a.blk * (sizeof(Move) + sizeof(int));
   // the two arrays of lengths apart: one launch
-  const int apart = a.new_len + a.batch <= a.len || a.len + a.batch <= a.new_len;
+  const int apart = a.new_len != a.len;
   if (a.keep) {  // without a list the kept rows are in place
     PSISPEC_LAUNCH("paged_commit", k_paged_commit, dim3((unsigned)((int64_t)a.batch * ntiles)),
                    dim3(kPgThreads), shm, stream, a, ntiles, apart);

@@ -324,6 +324,26 @@ def test_attend_strided_rows_streams_and_reruns():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("ps", [16, 24])
+def test_pages_far_apart(ps):
+    """A page stride of 2^31 elements (2^32 bytes), append and attention."""
+    raw = torch.empty(3 * 2**31, dtype=BF, device=DEV)
+    k, v = (torch.as_strided(raw, (3, ps, 2, 64), (2**31, 256, 64, 1), at) for at in (0, 128))
+    c = _append_case([ps + 3], 4, 4, 2, 64, ps, BF, BF, seed=ps, rot=64, norm=False)
+    tab = torch.tensor([[2, 0]], dtype=torch.int32)
+    args = [_gpu(x) for x in (tab, c["lens"])]
+    near = [torch.empty((3, ps, 2, 64), dtype=BF, device=DEV) for _ in range(2)]
+    for kc, vc in ((k, v), near):
+        kc.copy_(torch.randn((3, ps, 2, 64), generator=_gen(1)).to(BF))
+        vc.copy_(torch.randn((3, ps, 2, 64), generator=_gen(2)).to(BF))
+    outs = []
+    for kc, vc in ((k, v), near):
+        q = psispec_qkv_append(*_gpu(c["qkv"]).split([4, 2, 2], 2), kc, vc, *args, inv_freq=_gpu(c["f"]))
+        outs.append(psispec_paged_attention(q, kc, vc, *args))
+    assert torch.equal(outs[0], outs[1])
+    assert torch.equal(k, near[0]) and torch.equal(v, near[1])
+
+
 def test_attend_pool_beyond_32_bits():
     """Pages past 2^31 elements of the pool."""
     ps, hkv, d = 16, 8, 128
@@ -805,7 +825,7 @@ def test_binding_refusals():
             (dict(q=q.transpose(2, 3)), "rows"), (dict(k_scale=torch.ones(2, device=DEV)), "float8"),
             (dict(k_cache=f8, v_cache=f8, k_scale=torch.ones(3, device=DEV)), "k_scale"),
             (dict(q=q[:, :, :3]), "unsupported"), (dict(parent=ln), "parent"),
-            (dict(scale=float("inf")), "invalid argument"), (dict(out=q.float()), "out"),
+            (dict(scale=float("inf")), "invalid argument"), (dict(out=q.float()), "out"), (dict(out=q), "invalid argument"),
             (dict(workspace=torch.empty(8, dtype=torch.uint8, device=DEV)), "workspace"),
             (dict(q=torch.zeros((1, 1025, 4, 64), dtype=BF, device=DEV)), "unsupported"),
             (dict(n_new=ln.to(torch.int64)), "n_new"), (dict(status=ln.float()), "status"),
@@ -832,7 +852,8 @@ def test_binding_refusals():
                          (dict(blk=0), "unsupported"), (dict(refs=refs[:4]), "refs")]:
         with pytest.raises(PsispecError, match=word):
             psispec_pages_reserve(**{**dict(pool=pool, table=tab, refs=refs, length=ln, blk=4), **change})
-    for change, word in [(dict(blk=0), "invalid argument"), (dict(blk=1025), "invalid argument"), (dict(keep=ln), "keep")]:
+    for change, word in [(dict(blk=0), "invalid argument"), (dict(blk=1025), "invalid argument"), (dict(keep=ln), "keep"),
+                         (dict(keep=ln[:, None][:, :0]), "keep")]:
         with pytest.raises(PsispecError, match=word):
             psispec_paged_commit(**{**dict(pool=pool, table=tab, length=ln, blk=4, n_keep=ln), **change})
     with pytest.raises(PsispecError, match="unsupported"):

@@ -28,10 +28,13 @@ def _cache(**kw):
 BAD_CACHES = [dict(num_pages=0), dict(page_size=0), dict(page_size=4097), dict(slots=0),
               dict(slots=5), dict(slots=1 << 27, table_stride=1 << 27), dict(heads=0),
               dict(dim=24), dict(dim=0), dict(dim=272), dict(row_stride=130), dict(page_stride=-16),
-              dict(head_stride=4), dict(k_scale=256), dict(v_scale=256)]
+              dict(head_stride=4), dict(page_stride=1 << 62), dict(k_scale=256), dict(v_scale=256)]
 
 
-def _attend(L, c, dtype=pkg.PSISPEC_BF16, batch=1, blk=2, hq=4, q=P, qs=256, out=P, ln=P, scale=1.0,
+FAR = ctypes.c_void_p(1 << 20)
+
+
+def _attend(L, c, dtype=pkg.PSISPEC_BF16, batch=1, blk=2, hq=4, q=P, qs=256, out=FAR, ln=P, scale=1.0,
             ws=P, wsn=BIG):
     return L.psispec_paged_attention(ctypes.byref(c) if c is not None else None, q, qs, dtype, batch,
                                      blk, hq, None, ln, None, scale, out, 256, None, ws, wsn, None)
@@ -48,6 +51,10 @@ def test_attention_checks(L):
                dict(qs=260), dict(q=None), dict(out=None), dict(ln=None), dict(scale=math.inf),
                dict(scale=math.nan), dict(scale=1e300), dict(q=ctypes.c_void_p(264))):
         assert _attend(L, _cache(), **kw) == -1, kw
+    # out over q: the same rows, a part of them, rows of other strides
+    for at in (256, 256 + 2 * 248, 256 - 2 * 128, 256 + 2 * 256):
+        assert _attend(L, _cache(), out=ctypes.c_void_p(at)) == -1
+    assert _attend(L, _cache(), qs=512, out=ctypes.c_void_p(256 + 2 * 512)) == -1
     for kw in (dict(k=None), dict(v=264), dict(table=None)):
         assert _attend(L, _cache(**kw)) == -1, kw
     assert _attend(L, _cache(), ws=None) == -3
@@ -72,6 +79,15 @@ def test_append_checks(L):
 
     for kw in BAD_CACHES + [dict(head_stride=48), dict(row_stride=0), dict(page_stride=0)]:
         assert call(c=_cache(**kw)) == -1, kw
+    # heads, positions or pages inside one another
+    for kw in (dict(row_stride=64), dict(head_stride=96, row_stride=64, page_size=2),
+               dict(page_stride=128 * 16 - 64), dict(page_stride=128, row_stride=128),
+               dict(head_stride=1 << 60, row_stride=1 << 59, page_stride=1 << 58)):
+        assert call(c=_cache(**kw)) == -1, kw
+    # q_out between the rows of q, over its end, and rows of other strides
+    for qo in (256 + 2 * 8, 256 + 2 * 248, 256 + 2 * 512):
+        assert call(qo=ctypes.c_void_p(qo)) == -1
+    assert call(qs=520) == -1
     for kw in (dict(rot=24), dict(rot=80), dict(rot=-16), dict(inv_freq=None), dict(eps=-1.0),
                dict(eps=math.nan), dict(rope_scale=math.inf), dict(flags=2), dict(q_weight=264)):
         assert call(p=prep(**kw)) == -1, kw
@@ -120,7 +136,12 @@ def test_page_calls_checks(L):
         assert f(ws=None) == -3 and f(wsn=100) == -3 and f(ws=ctypes.c_void_p(264)) == -3
         assert f(batch=0) == 0
     assert commit(batch=0) == 0
+    for at, n in ((256, 2), (260, 2), (256 + 4 * 7, 8), (256 - 4 * 7, 8)):  # partly over the old lengths
+        bad = L.psispec_paged_commit(ctypes.byref(pool()), P, 4, 4, n, 4, P, 4, P, ctypes.c_void_p(at + 4),
+                                     ctypes.c_void_p(at), None, None)
+        assert bad == -1
     assert L.psispec_pages_workspace(4, 10, 100, 9, 16) > 0
+    assert L.psispec_pages_workspace((1 << 23) + 1, 10, 100, 9, 16) == 0
     assert L.psispec_pages_workspace(4, 10, 1 << 28, 9, 16) == 0
     assert L.psispec_pages_workspace(4, 0, 100, 9, 16) == 0
 
