@@ -56,22 +56,19 @@ constexpr int kNonTemporal = 2;
 // could be empty: a job's parts lie in shares one behind the other.  More, smaller shares given out as
 // places become free even out the rest, and lose more than that to joining.
 constexpr int kXcds = 8;
-__host__ __device__ inline int64_t share_of_block(int64_t shares, int R, int b) {
-  return shares < R ? b : (int64_t)(b % kXcds) * (R / kXcds) + b / kXcds;
-}
-__host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int64_t w) {
+__host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int skew, int64_t w) {
   if (shares < R) return w;
-  const int64_t per = R / kXcds, h = per / 2, first = R > kAttendCUs && all >= 2 * R ? 34 : 32;
+  const int64_t per = R / kXcds, h = per / 2, first = all >= 2 * R ? 32 + skew : 32;
   const int64_t x = w / per, j = w - x * per;
   const int64_t at = j < h ? first * j : first * h + (64 - first) * (j - h);
   return all * (x * 64 * h + at) / (kXcds * 64 * h);
 }
 // the share that holds a unit
-__host__ __device__ inline int64_t share_of(int64_t all, int64_t shares, int R, int64_t unit) {
+__host__ __device__ inline int64_t share_of(int64_t all, int64_t shares, int R, int skew, int64_t unit) {
   int64_t lo = 0, hi = shares;  // start(lo) <= unit < start(hi)
   while (hi - lo > 1) {
     const int64_t mid = (lo + hi) / 2;
-    if (share_start(all, shares, R, mid) <= unit)
+    if (share_start(all, shares, R, skew, mid) <= unit)
       lo = mid;
     else
       hi = mid;
@@ -89,27 +86,29 @@ struct AttendPlan {
   int mt;         // 16-row tiles per job
   int nmt;        // groups of 16 mt rows per (line, head)
   int dp;         // head dimension rounded up to 64, 128 or 256
-  int wgs;        // shares
+  int wgs;        // workgroups
+  int sub;        // workgroups per share
   int mask_words; // 64-bit words of a block row's mask (tree)
-  int hpw;        // heads per workgroup
+  int hpj;        // heads per job
   int prow;       // rows of a part in the workspace: the job's, at most blk G rounded up to 4
   size_t off_ml, off_o, off_mask, total;
 };
 
 struct AttendKernelArgs {
   AttendArgs a;
-  int G, nmt, mask_words, wgs;
+  int G, nmt, mask_words;
+  int shares, skew;          // shares at most; 2: an XCD's first half of them is larger
   int step_tiles;            // tiles of each wave in a step
   int job_cost;              // units of a job beside its steps
-  int hpw, hgroups;          // heads per workgroup (1 or 4), groups of them
+  int hpj, hgroups;          // heads per job (1 or 4), groups of them
   int prow;                  // rows of a part in the workspace
   uint32_t ps_magic;         // ceil(2^32 / page_size)
   int halves;                // whole heads of DP dims, pages of 16-position multiples, strides below 2^31
   uint32_t page_bytes, row_bytes;  // the strides in bytes when halves
   float c;                   // scale log2(e)
-  AttendInfo* info;          // [wgs]
-  float2* ml;                // [2 wgs][hpw][prow]
-  float* o;                  // [2 wgs][hpw][prow][DP]
+  AttendInfo* info;          // [shares]
+  float2* ml;                // [2 shares][hpj][prow]
+  float* o;                  // [2 shares][hpj][prow][DP]
   const uint64_t* mask;      // [batch][blk][mask_words] or null
 };
 
@@ -289,10 +288,11 @@ __device__ inline int64_t block_scan(int64_t x, int64_t* s, int64_t* total) {
 }
 
 // steps of job group mt of a line: a step is step_tiles tiles of each wave
-__device__ inline int job_steps(const AttendKernelArgs& k, int keys) {
-  const int step = kAttendTile * kAttendWaves / k.hpw * k.step_tiles;
+template <bool Q_LDS> __device__ inline int job_steps(const AttendKernelArgs& k, int keys) {
+  const int step = kAttendTile * (Q_LDS ? kAttendWaves : kAttendWaves / k.hpj) * k.step_tiles;
   return (keys + step - 1) / step;
 }
+template <bool Q_LDS>
 __device__ inline int64_t line_units(const AttendKernelArgs& k, int r, int rows) {
   int L, n;
   if (!line_rows(k.a.len, k.a.n_new, r, k.a.blk, k.a.c.slots, k.a.c.page_size, &L, &n) || n == 0)
@@ -300,7 +300,7 @@ __device__ inline int64_t line_units(const AttendKernelArgs& k, int r, int rows)
   int64_t s = 0;
   for (int mt = 0; mt < k.nmt; ++mt) {
     const int keys = job_keys(L, n, k.G, mt, rows);
-    s += keys > 0 ? job_steps(k, keys) + k.job_cost : 0;
+    s += keys > 0 ? job_steps<Q_LDS>(k, keys) + k.job_cost : 0;
   }
   return s * k.hgroups;
 }
@@ -368,29 +368,31 @@ void k_attend(AttendKernelArgs k) {
 
   // ---- this workgroup's share [x, x_end) of all units, and the line that holds unit x
   // units of the lines before line `tid`, of the line, and of all lines; the first 256 lines
-  const int64_t mine0 = tid < a.batch ? line_units(k, tid, ROWS) : 0;
+  const int64_t mine0 = tid < a.batch ? line_units<kQLds>(k, tid, ROWS) : 0;
   int64_t all;
   const int64_t at0 = block_scan(mine0, s_scan, &all);
   int64_t base = all;
   if (a.batch > kAttendThreads) {
     int64_t more = 0, sum;
     for (int r0 = kAttendThreads; r0 < a.batch; r0 += kAttendThreads)
-      more += r0 + tid < a.batch ? line_units(k, r0 + tid, ROWS) : 0;
+      more += r0 + tid < a.batch ? line_units<kQLds>(k, r0 + tid, ROWS) : 0;
     block_scan(more, s_scan, &sum);
     all += sum;
   }
-  const int64_t shares = min(all, (int64_t)k.wgs);
-  const int64_t w = share_of_block(shares, k.wgs, blockIdx.x);
-  if (tid == 0) k.info[w].parts = 0;
+  const int64_t shares = min(all, (int64_t)k.shares);
+  const int nsub = kQLds ? k.hpj : 1;
+  const int nth = shares < k.shares ? blockIdx.x : blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  const int w = nth / nsub, sub = nth - w * nsub;
+  if (tid == 0 && sub == 0) k.info[w].parts = 0;
   if (w >= shares) return;
-  int64_t x = share_start(all, shares, k.wgs, w);
-  const int64_t x_end = share_start(all, shares, k.wgs, w + 1);
+  int64_t x = share_start(all, shares, k.shares, k.skew, w);
+  const int64_t x_end = share_start(all, shares, k.shares, k.skew, w + 1);
   if (at0 <= x && x < at0 + mine0) {
     s_line = tid;
     s_base = at0;
   }
   for (int r0 = kAttendThreads; base <= x && r0 < a.batch; r0 += kAttendThreads) {
-    const int64_t mine = r0 + tid < a.batch ? line_units(k, r0 + tid, ROWS) : 0;
+    const int64_t mine = r0 + tid < a.batch ? line_units<kQLds>(k, r0 + tid, ROWS) : 0;
     int64_t part;
     const int64_t at = base + block_scan(mine, s_scan, &part);
     if (at <= x && x < at + mine) {
@@ -413,10 +415,10 @@ void k_attend(AttendKernelArgs k) {
     if (!live_line) continue;
     const int32_t* const tab = c.table + (int64_t)r * c.table_stride;
     for (int hg = 0; hg < k.hgroups && x < x_end; ++hg) {
-      const int h = hg * k.hpw + (k.hpw == 1 ? 0 : wave);
+      const int h = hg * k.hpj + (kQLds ? sub : k.hpj == 1 ? 0 : wave);
       for (int mt0 = 0; mt0 < k.nmt && x < x_end; ++mt0) {
         const int keys = job_keys(L, n, G, mt0, ROWS);
-        const int steps = job_steps(k, keys);
+        const int steps = job_steps<kQLds>(k, keys);
         const int units = keys > 0 ? steps + k.job_cost : 0;
         if (off >= units) {
           off -= units;
@@ -431,12 +433,13 @@ void k_attend(AttendKernelArgs k) {
         off = 0;
         if (step0 >= step1) continue;
         const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
-        const int splits = kAttendWaves / k.hpw;  // waves that share a head's positions
+        const bool alone = !kQLds && k.hpj > 1;   // the wave has the head to itself
+        const int splits = alone ? 1 : kAttendWaves;
         const int tile0 = step0 * splits * k.step_tiles;
         const int tile1 = min(step1 * splits * k.step_tiles, ntiles);
         const int cnt = tile1 - tile0;
-        const int t0 = k.hpw == 1 ? tile0 + cnt * wave / kAttendWaves : tile0;
-        const int t1 = k.hpw == 1 ? tile0 + cnt * (wave + 1) / kAttendWaves : tile1;
+        const int t0 = alone ? tile0 : tile0 + cnt * wave / kAttendWaves;
+        const int t1 = alone ? tile1 : tile0 + cnt * (wave + 1) / kAttendWaves;
 
         // ---- loads: tile t into stage t % NST
         const int chunks = dim * ES / 16;       // real chunks of a row
@@ -751,7 +754,7 @@ void k_attend(AttendKernelArgs k) {
 
         // ---- the job's output, or its part
         const bool whole = step0 == 0 && step1 == steps;
-        const int64_t slot = 2 * w + (first_segment ? 0 : 1);
+        const int64_t slot = 2 * (int64_t)w + (first_segment ? 0 : 1);
         const float vscale = F8 && c.v_scale ? c.v_scale[h] : 1.0f;
         // dims d .. d+3 of row `row` of the job: the sums y over maximum m and weight l
         auto finish = [&](int row, int d, f32x4 y, float m, float l, bool any_odd) {
@@ -786,12 +789,12 @@ void k_attend(AttendKernelArgs k) {
             *reinterpret_cast<x4*>(static_cast<T*>(a.out) + ((int64_t)r * a.blk + i) * a.out_stride +
                                    (int64_t)(h * G + (q - i * G)) * dim + d) = z;
           } else {
-            const int64_t at = (slot * k.hpw + (h - hg * k.hpw)) * k.prow + row;
+            const int64_t at = (slot * k.hpj + (h - hg * k.hpj)) * k.prow + row;
             *reinterpret_cast<f32x4*>(k.o + at * DP + d) = y;
             if (d == 0) k.ml[at] = make_float2(m, l);
           }
         };
-        if (!kQLds && k.hpw > 1) {  // the wave has the head to itself
+        if (alone) {
           const bool any_odd = __any(odd);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -838,8 +841,8 @@ void k_attend(AttendKernelArgs k) {
             __syncthreads();
           }
         }
-        if (!whole && step0 == 0 && tid == 0) {  // the job starts here and ends in a later share
-          const int64_t wl = share_of(all, shares, k.wgs, job_x + units - 1);
+        if (!whole && step0 == 0 && tid == 0 && sub == 0) {  // the job starts here and ends in a later share
+          const int64_t wl = share_of(all, shares, k.shares, k.skew, job_x + units - 1);
           AttendInfo& o = k.info[w];
           o.r = r;
           o.h = hg;
@@ -869,8 +872,8 @@ hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
   }
-  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((unsigned)k.wgs), dim3(kAttendThreads), shm,
-                 stream, k);
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((attend_two(DP) ? 2 : 1) * kAttendCUs),
+                 dim3(kAttendThreads), shm, stream, k);
   return hipGetLastError();
 }
 

@@ -37,7 +37,8 @@ AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int d
   p.nmt = (int)((rows + p.mt * 16 - 1) / (p.mt * 16));
   p.wgs = (attend_two(p.dp) ? 2 : 1) * kAttendCUs;
   p.mask_words = (blk + 63) / 64;
-  p.hpw = !attend_q_lds(p.dp, p.mt) && heads_kv % 4 == 0 ? 4 : 1;
+  p.hpj = heads_kv % 4 == 0 ? 4 : 1;
+  p.sub = attend_q_lds(p.dp, p.mt) ? p.hpj : 1;
   p.prow = (int)((rows < p.mt * 16 ? rows : p.mt * 16) + kJoinRows - 1) / kJoinRows * kJoinRows;
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -46,8 +47,8 @@ AttendPlan make_attend_plan(int batch, int blk, int heads_q, int heads_kv, int d
     return at;
   };
   take(sizeof(AttendInfo) * p.wgs);
-  p.off_ml = take(sizeof(float2) * 2 * p.wgs * p.hpw * p.prow);
-  p.off_o = take(sizeof(float) * 2 * p.wgs * p.hpw * p.prow * (size_t)p.dp);
+  p.off_ml = take(sizeof(float2) * 2 * (p.wgs / p.sub) * p.hpj * p.prow);
+  p.off_o = take(sizeof(float) * 2 * (p.wgs / p.sub) * p.hpj * p.prow * (size_t)p.dp);
   p.off_mask = take(sizeof(uint64_t) * (size_t)batch * blk * p.mask_words);
   p.total = off;
   return p;
@@ -102,7 +103,7 @@ template <int DP, bool WIDE> struct JoinSum {
       for (int u = 0; u < kAhead; ++u) {  // no branches: past the last part, the last again
         const int p = min(p0 + stride * u, in.parts - 1);
         const int64_t slot = p == 0 ? in.slot : 2 * (int64_t)(w + p);
-        const int64_t at = (slot * k.hpw + hi) * k.prow + row0;
+        const int64_t at = (slot * k.hpj + hi) * k.prow + row0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int e = (v * 64 + lane) * 4, row = e / DP, ok = min(row, live - 1);
@@ -161,8 +162,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
   }
   const int item = WIDE ? blockIdx.x : blockIdx.x * kJoinWaves + wave;
   if (item >= items) return;
-  const int w = item / (k.hpw * quads);
-  const int hi = (item - w * k.hpw * quads) / quads;
+  const int w = item / (k.hpj * quads);
+  const int hi = (item - w * k.hpj * quads) / quads;
   const int row0 = (item % quads) * kJoinRows;
   const AttendInfo in = k.info[w];
   if (in.parts == 0) return;
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
   line_rows(a.len, a.n_new, in.r, a.blk, c.slots, c.page_size, &L, &n);
   const int live = min(n * k.G - in.mt * rows, rows) - row0;  // live rows from row0 on
   if (live <= 0) return;
-  const int h = in.h * k.hpw + hi;
+  const int h = in.h * k.hpj + hi;
   const float vs = f8 && c.v_scale ? c.v_scale[h] : 1.0f;
   auto store = [&](int e, f32x4 y, float l) {  // 16 bytes e of the four rows
     const int row = e * 4 / DP, d = e * 4 - row * DP;
@@ -218,11 +219,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
 template <typename T, int DP>
 hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, bool whole,
                           hipStream_t stream) {
-  const int rows = p.mt * 16, items = whole ? 0 : k.wgs * k.hpw * (p.prow / kJoinRows);
+  const int rows = p.mt * 16, items = whole ? 0 : k.shares * k.hpj * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
   const int status = k.a.status ? k.a.batch : 0;
   // fewer jobs than a quarter of the shares: most are cut in many parts
-  if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.wgs)
+  if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.shares)
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
                    dim3(64 * kJoinWaves), 0, stream, k, rows, items, f8);
   else
@@ -255,17 +256,18 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.G = a.heads_q / a.c.heads;
   k.nmt = p.nmt;
   k.mask_words = p.mask_words;
-  k.wgs = p.wgs;
   // Short lines: a job is one step, so no border cuts it.
   const int64_t most = (int64_t)a.c.slots * a.c.page_size;
-  const bool few = p.hpw > 1 && (int64_t)a.batch * a.c.heads <= kFewHeads;
+  const bool few = p.hpj > 1 && p.sub == 1 && (int64_t)a.batch * a.c.heads <= kFewHeads;
   const bool whole = most <= (few ? kWholeFewPositions : kWholePositions);
-  k.hpw = whole ? 1 : p.hpw;
-  k.hgroups = a.c.heads / k.hpw;
+  k.hpj = whole ? 1 : p.hpj;
+  k.hgroups = a.c.heads / k.hpj;
+  k.shares = whole ? p.wgs : p.wgs / p.sub;
+  k.skew = p.wgs > kAttendCUs ? 2 : 0;
   k.prow = p.prow;
   const int step = kAttendTile * kAttendWaves;
   k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
-  k.job_cost = whole ? 0 : k.hpw > 1 ? 1 : 3;
+  k.job_cost = whole ? 0 : p.hpj > 1 && p.sub == 1 ? 1 : 3;
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
