@@ -141,17 +141,12 @@ __global__ __launch_bounds__(64) void k_paged_len(PagedCommitArgs a) {
 // assign: line r becomes the first new_len[r] positions of the old line src[r].
 // ------------------------------------------------------------------------------------------------
 
-// Line r by `threads` threads (all of a workgroup's barriers are shared by its lines): the new entries
-// into the workspace and the changes of the counts (integer adds: the sums do not depend on their
-// order).
+// What line r becomes, but for the pages taken, which are looked at with the entries.
 struct AssignLine {
-  const int32_t *from, *old;
-  int32_t* out;
-  int cut, want;
+  int from, cut, want;  // the line that entries 0 .. cut-1 come from, the new length
   bool bad;
 };
-__device__ inline AssignLine assign_begin(const AssignArgs& a, int32_t* newtab, int r, int tid,
-                                          int threads) {
+__device__ inline AssignLine assign_begin(const AssignArgs& a, int r) {
   AssignLine l;
   const int src = a.src[r];
   l.want = src == -1 ? 0 : a.new_len[r];
@@ -161,36 +156,35 @@ __device__ inline AssignLine assign_begin(const AssignArgs& a, int32_t* newtab, 
     l.bad = l.want > a.len[src] || (int64_t)l.want > (int64_t)a.slots * a.page_size;
     l.cut = l.bad ? 0 : (int)(((int64_t)l.want + a.page_size - 1) / a.page_size);
   }
-  l.from = a.table + (int64_t)(l.bad || src < 0 ? r : src) * a.table_stride;
-  l.old = a.table + (int64_t)r * a.table_stride;
-  l.out = newtab + (int64_t)r * a.slots;
-  for (int s = tid; s < l.cut; s += threads) l.bad |= !page_ok(l.from[s], a.num_pages);
+  l.from = l.bad || src < 0 ? r : src;
   return l;
 }
-__device__ inline void assign_entries(const AssignArgs& a, const AssignLine& l, bool bad, int32_t* newlen,
-                                      int r, int tid, int threads) {
-  for (int s = tid; s < a.slots; s += threads) {
-    const int o = l.old[s];
-    const int e = bad ? o : s < l.cut ? l.from[s] : -1;
-    l.out[s] = e;
+
+// One workgroup per line: the new entries into the workspace and the changes of the counts (integer
+// adds: the sums do not depend on their order); then k_assign_write, for a line's old entries are read
+// by others.
+__global__ __launch_bounds__(kPgThreads) void k_assign_count(AssignArgs a, int32_t* newtab,
+                                                             int32_t* newlen) {
+  const int r = blockIdx.x;
+  const AssignLine l = assign_begin(a, r);
+  const int32_t* from = a.table + (int64_t)l.from * a.table_stride;
+  const int32_t* old = a.table + (int64_t)r * a.table_stride;
+  bool bad = l.bad;
+  for (int s = threadIdx.x; s < l.cut; s += kPgThreads) bad |= !page_ok(from[s], a.num_pages);
+  bad = __syncthreads_or(bad);
+  for (int s = threadIdx.x; s < a.slots; s += kPgThreads) {
+    const int o = old[s];
+    const int e = bad ? o : s < l.cut ? from[s] : -1;
+    newtab[(int64_t)r * a.slots + s] = e;
     if (e != o) {
       if (page_ok(e, a.num_pages)) atomicAdd(&a.refs[e], 1);
       if (page_ok(o, a.num_pages)) atomicSub(&a.refs[o], 1);
     }
   }
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     newlen[r] = bad ? a.len[r] : l.want;
     if (a.status) a.status[r] = bad ? PSISPEC_ST_BAD_PAGE : 0;
   }
-}
-
-// One workgroup per line, then k_assign_write: a line's old entries are read by others.
-__global__ __launch_bounds__(kPgThreads) void k_assign_count(AssignArgs a, int32_t* newtab,
-                                                             int32_t* newlen) {
-  const int r = blockIdx.x;
-  const AssignLine l = assign_begin(a, newtab, r, threadIdx.x, kPgThreads);
-  const bool bad = __syncthreads_or(l.bad);
-  assign_entries(a, l, bad, newlen, r, threadIdx.x, kPgThreads);
 }
 
 __global__ __launch_bounds__(kPgThreads) void k_assign_write(AssignArgs a, const int32_t* newtab,
@@ -201,25 +195,49 @@ __global__ __launch_bounds__(kPgThreads) void k_assign_write(AssignArgs a, const
   if (threadIdx.x == 0) a.len[r] = newlen[r];
 }
 
-// Few lines in one launch (4 lines: 4.5 us against 4.5 + 4.4 in two): one workgroup, a wave per line, a
-// barrier between the reads of the old tables and the writes of the new ones.  A wave with several
-// lines takes them one after the other (128 lines: 23 us against 4.3 + 4.3), so there is at most one
-// each, of a few entries per lane.
+// Few entries in one launch of one workgroup: each thread holds its old and new entries in registers,
+// and a barrier lies between the reads of the old tables and the writes of the new ones.  64 lines of 39
+// slots: 4.5 us against 4.7 + 4.4 in two launches; 128 of 57: 10.7 (one CU's atomics) against 4.3 + 4.3.
 constexpr int kOneBlock = 1024;
-constexpr int kSmallLines = kOneBlock / 64;
-constexpr int kSmallEntries = 256;
-__global__ __launch_bounds__(kOneBlock) void k_assign_small(AssignArgs a, int32_t* newtab,
-                                                            int32_t* newlen) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
-    const AssignLine l = assign_begin(a, newtab, r, lane, 64);
-    assign_entries(a, l, __any(l.bad), newlen, r, lane, 64);
+constexpr int kOneEntries = 4;  // per thread
+__global__ __launch_bounds__(kOneBlock) void k_assign_one(AssignArgs a) {
+  __shared__ int s_from[kOneBlock], s_cut[kOneBlock], s_bad[kOneBlock];
+  const int tid = threadIdx.x;
+  int len_new = 0;
+  if (tid < a.batch) {
+    const AssignLine l = assign_begin(a, tid);
+    s_from[tid] = l.from;
+    s_cut[tid] = l.cut;
+    s_bad[tid] = l.bad;
+    len_new = l.want;
   }
   __syncthreads();
-  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
-    for (int s = lane; s < a.slots; s += 64)
-      a.table[(int64_t)r * a.table_stride + s] = newtab[(int64_t)r * a.slots + s];
-    if (lane == 0) a.len[r] = newlen[r];
+  const int all = a.batch * a.slots;
+  int line[kOneEntries], old[kOneEntries], now[kOneEntries];
+#pragma unroll
+  for (int k = 0; k < kOneEntries; ++k) {
+    const int x = tid + k * kOneBlock;
+    line[k] = -1;
+    if (x < all) {
+      const int r = x / a.slots, t = x - r * a.slots;
+      line[k] = r;
+      old[k] = a.table[(int64_t)r * a.table_stride + t];
+      now[k] = t < s_cut[r] ? a.table[(int64_t)s_from[r] * a.table_stride + t] : -1;
+      if (t < s_cut[r] && !page_ok(now[k], a.num_pages)) s_bad[r] = 1;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kOneEntries; ++k) {
+    if (line[k] < 0 || s_bad[line[k]] || old[k] == now[k]) continue;
+    const int t = tid + k * kOneBlock - line[k] * a.slots;
+    if (page_ok(now[k], a.num_pages)) atomicAdd(&a.refs[now[k]], 1);
+    if (page_ok(old[k], a.num_pages)) atomicSub(&a.refs[old[k]], 1);
+    a.table[(int64_t)line[k] * a.table_stride + t] = now[k];
+  }
+  if (tid < a.batch) {
+    if (!s_bad[tid]) a.len[tid] = len_new;
+    if (a.status) a.status[tid] = s_bad[tid] ? PSISPEC_ST_BAD_PAGE : 0;
   }
 }
 
@@ -350,57 +368,68 @@ __global__ __launch_bounds__(kPgThreads) void k_reserve_ids(ReserveArgs a, Reser
   }
 }
 
-// Both for a pool of one chunk and few lines in one launch: one workgroup.
-__global__ __launch_bounds__(kOneBlock) void k_reserve_small(ReserveArgs a, ReserveWs w) {
-  __shared__ int s_free[kOneBlock / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int r = wave; r < a.batch; r += kOneBlock / 64) {
-    int L, s0, m, n = 0;
-    bool bad = !reserve_span(a, r, &L, &s0, &m);
-    for (int j = lane; j < w.J; j += 64) n += reserve_slot(a, w, r, j, s0, m, L, &bad);
-    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
-    bad = __any(bad);
-    if (lane == 0) w.need[r] = bad ? -1 : n;
+// Both in one launch of one workgroup for small pools and few slots: a line belongs to `group` lanes
+// (a power of two), a wave counts the free pages of its run of the pool by votes.  128 lines, 7300 pages:
+// 6.3 us against 4.4 + 6.0.
+constexpr int kOneChunks = 8;
+constexpr int kOneSlots = 4;  // slots per lane
+__global__ __launch_bounds__(kOneBlock) void k_reserve_one(ReserveArgs a, ReserveWs w, int log_group) {
+  constexpr int kWaves = kOneBlock / 64, kVotes = kOneChunks * kScanChunk / kOneBlock;
+  __shared__ int s_free[kWaves], s_need[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int group = 1 << log_group, r = tid >> log_group;
+  int n = 0, bad = 0;
+  if (r < a.batch) {
+    int L, s0, m;
+    bool b = !reserve_span(a, r, &L, &s0, &m);
+    for (int j = tid & (group - 1); j < w.J; j += group) n += reserve_slot(a, w, r, j, s0, m, L, &b);
+    bad = b;
   }
-  constexpr int kPer = kScanChunk / kOneBlock;
-  const int p0 = threadIdx.x * kPer;
-  bool fr[kPer];
+  const int votes = w.chunks * (kScanChunk / kOneBlock);
+  const int p0 = wave * votes * 64 + lane;
+  uint64_t fr[kVotes];
   int mine = 0;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    fr[k] = p0 + k < a.pool.num_pages && a.refs[p0 + k] == 0;
-    mine += fr[k];
+  for (int k = 0; k < kVotes; ++k) {
+    fr[k] = 0;
+    if (k < votes) {
+      const int p = p0 + 64 * k;
+      fr[k] = __ballot(p < a.pool.num_pages && a.refs[min(p, a.pool.num_pages - 1)] == 0);
+      mine += __popcll(fr[k]);
+    }
   }
-  int inc = mine;
+  for (int o = 1; o < group; o <<= 1) {
+    n += __shfl_xor(n, o, 64);
+    bad |= __shfl_xor(bad, o, 64);
+  }
+  const bool first_lane = (tid & (group - 1)) == 0 && r < a.batch;
+  const int need = first_lane && !bad ? n : 0;
+  int upto = need;  // what the lines up to this one need
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += y;
+    const int y = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += y;
   }
-  if (lane == 63) s_free[wave] = inc;
+  if (lane == 0) s_free[wave] = mine;
+  if (lane == 63) s_need[wave] = upto;
   __syncthreads();
-  int at = inc - mine, all = 0;
-  for (int v = 0; v < kOneBlock / 64; ++v) {
+  int at = 0, avail = 0, want = 0;
+  for (int v = 0; v < kWaves; ++v) {
     at += v < wave ? s_free[v] : 0;
-    all += s_free[v];
+    upto += v < wave ? s_need[v] : 0;
+    avail += s_free[v];
+    want += s_need[v];
   }
-  const int cap = a.batch * w.J;  // room in ids: no call needs more
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (fr[k]) {
-      if (at < cap) w.ids[at] = p0 + k;
-      ++at;
-    }
+  if (first_lane) {
+    w.need[r] = bad ? -1 : need;
+    w.first[r] = need == 0 || upto <= avail ? upto - need : -1;
   }
-  if (wave == 0) {  // batch <= 64
-    const int need = lane < a.batch ? max(w.need[lane], 0) : 0;
-    int sum = need;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += y;
-    }
-    if (lane < a.batch) w.first[lane] = need == 0 || sum <= all ? sum - need : -1;
+  for (int k = 0; k < kVotes; ++k) {
+    if (k >= votes || at >= want) break;
+    const int to = at + __popcll(fr[k] & ((1ull << lane) - 1));
+    if ((fr[k] >> lane & 1) && to < want) w.ids[to] = p0 + 64 * k;
+    at += __popcll(fr[k]);
   }
 }
 
@@ -498,8 +527,8 @@ hipError_t launch_pages_assign(const AssignArgs& a, void* workspace, hipStream_t
   int32_t* newtab = static_cast<int32_t*>(workspace);
   int32_t* newlen = reinterpret_cast<int32_t*>(
       static_cast<char*>(workspace) + up256(sizeof(int32_t) * (size_t)a.batch * a.slots));
-  if (a.batch <= kSmallLines && a.slots <= kSmallEntries) {
-    PSISPEC_LAUNCH("assign_small", k_assign_small, dim3(1), dim3(kOneBlock), 0, stream, a, newtab, newlen);
+  if (a.batch <= kOneBlock && (int64_t)a.batch * a.slots <= kOneBlock * kOneEntries) {
+    PSISPEC_LAUNCH("assign_one", k_assign_one, dim3(1), dim3(kOneBlock), 0, stream, a);
     return hipGetLastError();
   }
   PSISPEC_LAUNCH("assign_count", k_assign_count, dim3((unsigned)a.batch), dim3(kPgThreads), 0, stream,
@@ -527,8 +556,10 @@ hipError_t launch_pages_reserve(const ReserveArgs& a, void* workspace, hipStream
   w.ids = carve((size_t)a.batch * w.J);
   w.cnt = carve(w.chunks);
   hipError_t e;
-  if (w.chunks == 1 && a.batch <= kSmallLines && w.J <= kSmallEntries) {
-    PSISPEC_LAUNCH("reserve_small", k_reserve_small, dim3(1), dim3(kOneBlock), 0, stream, a, w);
+  int lg = 6;
+  while (lg > 0 && (int64_t)a.batch << lg > kOneBlock) --lg;
+  if (w.chunks <= kOneChunks && a.batch <= kOneBlock && w.J <= kOneSlots << lg) {
+    PSISPEC_LAUNCH("reserve_one", k_reserve_one, dim3(1), dim3(kOneBlock), 0, stream, a, w, lg);
   } else {
     PSISPEC_LAUNCH("reserve_plan", k_reserve_plan, dim3((unsigned)(a.batch + w.chunks)),
                    dim3(kPgThreads), 0, stream, a, w);

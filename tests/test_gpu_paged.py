@@ -679,6 +679,26 @@ def test_pages_many_chunks_of_pages():
     assert c.tab[0, :40].tolist() == free[:40].tolist()
 
 
+@pytest.mark.parametrize("batch,slots,ps,pages", [(1, 4096, 1, 4096), (1, 4097, 1, 4097), (64, 64, 4, 32768),
+                                                  (64, 65, 4, 32769), (1024, 4, 16, 9000), (1025, 4, 16, 9000),
+                                                  (17, 40, 8, 5000)])
+def test_pages_sizes_about_one_workgroup(batch, slots, ps, pages):
+    """Tables and pools just within and just beyond what one workgroup does alone."""
+    rng = np.random.default_rng(batch + slots)
+    c = _Pages(1, pages, ps, 4, batch, slots, 5)
+    blk = min(2 * ps + 1, slots * ps - 1)
+    for step in range(3):
+        n = np.minimum(rng.integers(0, blk + 1, batch), slots * ps - c.len)
+        st = c.reserve(blk, n.tolist())
+        c.grow(np.where(st == 0, n, 0))
+        src = np.where(rng.random(batch) < 0.4, rng.integers(0, batch, batch), np.arange(batch))
+        src = np.where(rng.random(batch) < 0.1, batch, src)  # refused
+        new = np.where(src < batch, c.len[np.minimum(src, batch - 1)], 0)
+        st = c.assign(src, np.maximum(new - (rng.random(batch) < 0.3), 0))
+        assert (st == np.where(src < batch, 0, ref.BAD_PAGE)).all()
+    c.reserve(max(min(300, slots * ps - int(c.len.max())), 1))  # the lines that this does not fit are refused
+
+
 # ------------------------------------------------------------------------------------- together
 
 def test_reserve_append_attend_verify_commit_loop():
