@@ -97,7 +97,8 @@ struct AttendPlan {
 struct AttendKernelArgs {
   AttendArgs a;
   int G, nmt, mask_words;
-  int shares, skew;          // shares at most; 2: an XCD's first half of them is larger
+  int shares, skew;          // shares of a full grid; 2: an XCD's first half of them is larger
+  int used;                  // shares of this grid, the others have no unit
   int step_tiles;            // tiles of each wave in a step
   int job_cost;              // units of a job beside its steps
   int hpj, hgroups;          // heads per job (1 or 4), groups of them
@@ -872,7 +873,7 @@ hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
   }
-  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((attend_two(DP) ? 2 : 1) * kAttendCUs),
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3(k.used * (Sh::kQLds ? k.hpj : 1)),
                  dim3(kAttendThreads), shm, stream, k);
   return hipGetLastError();
 }

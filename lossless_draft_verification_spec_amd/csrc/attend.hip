@@ -77,9 +77,10 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
 
 // An item is four rows of one head of the job that starts in share w and ends in a later one; its parts
 // are added in order, a lane the same 16 bytes of each.  WIDE (few jobs, many parts each): a block per
-// item, its waves take every fourth part and are added at the end.  Otherwise a wave per item.  Blocks
-// behind the items: the status of one line each.
-constexpr int kJoinWaves = 4;
+// item, its eight waves take every eighth part and are added at the end (4 lines of 130 000 8-bit positions, 64
+// parts a job: 9.0 us, with four waves 10.9).  Otherwise a wave per item.  Blocks behind the items: the
+// status of one line each.
+constexpr int join_waves(bool wide) { return wide ? 8 : 4; }
 
 // the parts first, first + stride, ... of rows row0 .. row0+3 (live of them)
 template <int DP, bool WIDE> struct JoinSum {
@@ -130,8 +131,9 @@ template <int DP, bool WIDE> struct JoinSum {
 };
 
 template <typename T, int DP, bool WIDE>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArgs k, int rows, int items,
-                                                              int f8) {
+__global__ __launch_bounds__(64 * join_waves(WIDE)) void k_attend_join(AttendKernelArgs k, int rows,
+                                                                   int items, int f8) {
+  constexpr int kJoinWaves = join_waves(WIDE);
   typedef JoinSum<DP, WIDE> Sum;
   __shared__ f32x4 s_o[WIDE ? kJoinWaves : 1][kJoinRows * DP / 4];
   __shared__ float s_m[kJoinWaves][kJoinRows], s_l[kJoinWaves][kJoinRows];
@@ -219,17 +221,17 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(AttendKernelArg
 template <typename T, int DP>
 hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, bool whole,
                           hipStream_t stream) {
-  const int rows = p.mt * 16, items = whole ? 0 : k.shares * k.hpj * (p.prow / kJoinRows);
+  const int rows = p.mt * 16, items = whole ? 0 : k.used * k.hpj * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
   const int status = k.a.status ? k.a.batch : 0;
   // fewer jobs than a quarter of the shares: most are cut in many parts
   if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.shares)
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
-                   dim3(64 * kJoinWaves), 0, stream, k, rows, items, f8);
+                   dim3(64 * join_waves(true)), 0, stream, k, rows, items, f8);
   else
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, false>),
-                   dim3((unsigned)((items + kJoinWaves - 1) / kJoinWaves + status)),
-                   dim3(64 * kJoinWaves), 0, stream, k, rows, items, f8);
+                   dim3((unsigned)((items + join_waves(false) - 1) / join_waves(false) + status)),
+                   dim3(64 * join_waves(false)), 0, stream, k, rows, items, f8);
   return hipGetLastError();
 }
 
@@ -268,6 +270,11 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   const int step = kAttendTile * kAttendWaves;
   k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
   k.job_cost = whole ? 0 : p.hpj > 1 && p.sub == 1 ? 1 : 3;
+  // no more workgroups than there can be units
+  const int tiles = (p.sub > 1 ? kAttendWaves : kAttendWaves / k.hpj) * k.step_tiles;
+  const int64_t steps = (most + tiles * kAttendTile - 1) / (tiles * kAttendTile);
+  const int64_t units = (steps + k.job_cost) * k.hgroups * k.nmt * a.batch;
+  k.used = (int)(units < k.shares ? units : k.shares);
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
