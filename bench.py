@@ -24,7 +24,8 @@ H=4096, rank-16 LoRA, MFMA roofline), the drafting step (`drafts`), the KV commi
 verifies (`kv_commit`), and the oracle timed on the host cores (`cpu_baseline`: one thread and
 request-sharded over the cores it may use).
 `--workload c2|ns|c3|c1|c4|c4s|c5|drafts|kv|peaks` prints that leg's line alone (for profiling);
-`--workload sweep` prints the linear-vs-tree batch sweep (batch 1..256).
+`--workload sweep` prints the linear-vs-tree batch sweep (batch 1..256); `--workload paged` the paged
+cache's part of a verify forward (one layer: pages, norms and rotations, attention, commit).
 """
 from __future__ import annotations
 
@@ -54,7 +55,7 @@ def parse():
                     help="calls timed one by one for the median / p10 / p90 of every leg")
     ap.add_argument("--workload", default="all",
                     choices=["all", "c2", "ns", "c3", "c1", "c4", "c4s", "c5", "drafts", "kv",
-                             "sweep", "peaks"])
+                             "paged", "sweep", "peaks"])
     ap.add_argument("--sweep-batches", default="1,2,4,8,16,32,64,128,256",
                     help="batch sizes of the linear-vs-tree sweep")
     ap.add_argument("--sweep-steps", type=int, default=40)
@@ -494,6 +495,56 @@ def run_kv(steps, warmup, ncalls, torch, pkg, workloads, peaks):
                                       peaks, read_traffic("kv_commit", "tree")))
 
 
+def run_paged(steps, warmup, ncalls, torch, pkg, peaks):
+    """Time one layer's pass of a verify forward over the paged cache: psispec_pages_reserve,
+    psispec_qkv_append, psispec_paged_attention and psispec_paged_commit of 9-row blocks (8 drafted
+    tokens and the one before them) for 64 lines of 300 to 4200 positions, 32 query and 8 key/value
+    heads of 128, bf16, pages of 16 positions in a random order.  Each call starts from a fresh copy of
+    the lengths.  HBM roofline of the attention over every key and value read once."""
+    b, blk, hq, hkv, d, ps = 64, 9, 32, 8, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(11)
+    len0 = torch.linspace(300, 4200, b, device="cuda").to(torch.int32)
+    slots = (4200 + blk + ps - 1) // ps
+    table = torch.full((b, slots), -1, dtype=torch.int32, device="cuda")
+    per = ((len0 + ps - 1) // ps).tolist()
+    pages = sum(per) + 2 * b
+    ids = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    at = 0
+    for r, n in enumerate(per):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    refs[ids[:at].long()] = 1
+    pool = torch.randn((2, pages, ps, hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    qkv = torch.randn((b, blk, hq + 2 * hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    q, k, v = qkv.split([hq, hkv, hkv], 2)
+    w = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    inv, mag = pkg.rope_frequencies(d, 1000000.0, device="cuda")
+    n_keep = torch.randint(0, blk + 1, (b,), generator=g, device="cuda", dtype=torch.int32)
+    length, status = len0.clone(), torch.zeros(b, dtype=torch.int32, device="cuda")
+    q_out, out = (torch.empty((b, blk, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def call(_):
+        length.copy_(len0)
+        pkg.psispec_pages_reserve(pool, table, refs, length, blk)
+        pkg.psispec_qkv_append(q, k, v, pool[0], pool[1], table, length, q_weight=w, k_weight=w,
+                               inv_freq=inv, rope_scale=mag, q_out=q_out)
+        pkg.psispec_paged_attention(q_out, pool[0], pool[1], table, length, out=out, status=status)
+        pkg.psispec_paged_commit(pool, table, length, blk, n_keep)
+
+    m = measure(torch, pkg, call, steps, warmup, ncalls)
+    ok = bool((length == len0 + n_keep).all().item() and (status == 0).all().item())
+    row = d * 2
+    alg = int((len0 + blk).sum().item()) * 2 * hkv * row + 2 * b * blk * hq * row
+    del pool
+    torch.cuda.empty_cache()
+    return dict(workload=f"paged: one layer of a verify forward, {b} lines of 300..4200 positions, "
+                         f"{blk}-row blocks, {hq}/{hkv} heads x {d} bf16, pages of {ps}",
+                us_per_call=round(1e3 * m["ms_per_step"], 2), lines_ok=ok, call_us=m["call_us"],
+                kernels_avg_us={n: round(t, 2) for n, t in m["kernels_us"].items()},
+                roofline=roofline_hbm("k_attend", alg, m["kernels_us"].get("attend", 0.0), peaks))
+
+
 def _time_calls(torch, pkg, call, steps, warmup):
     """Mean device time per call (torch events over `steps` calls after `warmup`), the summed
     outputs of the timed calls, and the library's per-kernel mean times (a second pass)."""
@@ -729,6 +780,7 @@ def main():
         "c4s": lambda: run_tree("c4s", L, 5, C, torch, pkg, workloads, None),
         "drafts": lambda: run_drafts(L, 5, C, torch, pkg, workloads, None),
         "kv": lambda: run_kv(min(L, 50), 3, C, torch, pkg, workloads, None),
+        "paged": lambda: run_paged(L, 5, C, torch, pkg, None),
         "ns": lambda: run_linear("ns", K, W, C, torch, pkg, workloads, None)[0],
         "c3": lambda: run_linear("c3", L, 5, C, torch, pkg, workloads, None)[0],
         "c1": lambda: run_linear("c1", K, W, C, torch, pkg, workloads, None)[0],
