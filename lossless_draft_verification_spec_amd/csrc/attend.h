@@ -84,10 +84,10 @@ __host__ __device__ inline int64_t share_of(int64_t all, int64_t shares, int R, 
   return lo;
 }
 
-// The job that starts in a workgroup's share and ends in a later one (parts == 0: none); h: head
-// group.
+// A job that starts in share w and ends in a later one (parts == 0: none); h: head group.  One per job
+// that has a step, or, with more jobs than shares, one per share.
 struct AttendInfo {
-  int32_t r, h, mt, parts, slot, pad[3];
+  int32_t r, h, mt, parts, slot, w, pad[2];
 };
 
 struct AttendPlan {
@@ -107,6 +107,7 @@ struct AttendKernelArgs {
   int G, nmt, mask_words;
   int shares, skew;          // shares of a full grid; 2: an XCD's first half of them is larger
   int used;                  // shares of this grid, the others have no unit
+  int solo;                  // a share per wave, whole jobs only (not with the queries in LDS)
   int step_tiles;            // tiles of each wave in a step
   int job_cost;              // units of a job beside its steps
   int hpj, hgroups;          // heads per job (1 or 4), groups of them
@@ -115,7 +116,8 @@ struct AttendKernelArgs {
   int halves;                // whole heads of DP dims, pages of 16-position multiples, strides below 2^31
   uint32_t page_bytes, row_bytes;  // the strides in bytes when halves
   float c;                   // scale log2(e)
-  AttendInfo* info;          // [shares]
+  int by_job;                // info per job
+  AttendInfo* info;          // [jobs or shares]
   float2* ml;                // [2 shares][hpj][prow]
   float* o;                  // [2 shares][hpj][prow][DP]
   const uint64_t* mask;      // [batch][blk][mask_words] or null
@@ -364,8 +366,8 @@ void k_attend(AttendKernelArgs k) {
   char* const q_lds = ring + Sh::kRing * kAttendWaves;
   __shared__ float s_m[kAttendWaves][ROWS], s_l[kAttendWaves][ROWS];
   __shared__ int64_t s_scan[kAttendWaves];
-  __shared__ int64_t s_base;
-  __shared__ int s_line;
+  __shared__ int64_t s_base[kAttendWaves];
+  __shared__ int s_line[kAttendWaves];
 
   const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
@@ -391,28 +393,36 @@ void k_attend(AttendKernelArgs k) {
   const int64_t shares = min(all, (int64_t)k.shares);
   const int nsub = kQLds ? k.hpj : 1;
   const int nth = shares < k.shares ? blockIdx.x : blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-  const int w = nth / nsub, sub = nth - w * nsub;
-  if (tid == 0 && sub == 0) k.info[w].parts = 0;
-  if (w >= shares) return;
-  int64_t x = share_start(all, shares, k.shares, k.skew, w);
-  const int64_t x_end = share_start(all, shares, k.shares, k.skew, w + 1);
-  if (at0 <= x && x < at0 + mine0) {
-    s_line = tid;
-    s_base = at0;
-  }
-  for (int r0 = kAttendThreads; base <= x && r0 < a.batch; r0 += kAttendThreads) {
+  const bool solo = !kQLds && k.solo;
+  const int w0 = solo ? nth * kAttendWaves : nth / nsub, sub = solo ? 0 : nth - w0 * nsub;
+  const int nw = solo ? kAttendWaves : 1;  // shares of the workgroup
+  if (tid == 0 && sub == 0 && !solo && !k.by_job) k.info[w0].parts = 0;
+  if (w0 >= shares) return;
+  auto locate = [&](int line, int64_t at, int64_t mine) {
+    for (int u = 0; u < nw; ++u) {
+      const int64_t xu = share_start(all, shares, k.shares, k.skew, min((int64_t)w0 + u, shares - 1));
+      if (at <= xu && xu < at + mine) {
+        s_line[u] = line;
+        s_base[u] = at;
+      }
+    }
+  };
+  locate(tid, at0, mine0);
+  const int64_t x_last = share_start(all, shares, k.shares, k.skew, min((int64_t)w0 + nw, shares) - 1);
+  for (int r0 = kAttendThreads; base <= x_last && r0 < a.batch; r0 += kAttendThreads) {
     const int64_t mine = r0 + tid < a.batch ? line_units<kQLds>(k, r0 + tid, ROWS) : 0;
     int64_t part;
     const int64_t at = base + block_scan(mine, s_scan, &part);
-    if (at <= x && x < at + mine) {
-      s_line = r0 + tid;
-      s_base = at;
-    }
+    locate(r0 + tid, at, mine);
     base += part;
   }
   __syncthreads();
-  int r = s_line;
-  int64_t off = x - s_base;  // unit within the line's jobs
+  const int w = w0 + (solo ? wave : 0);
+  if (w >= shares) return;  // no barrier follows in a solo wave
+  int64_t x = share_start(all, shares, k.shares, k.skew, w);
+  const int64_t x_end = share_start(all, shares, k.shares, k.skew, w + 1);
+  int r = s_line[solo ? wave : 0];
+  int64_t off = x - s_base[solo ? wave : 0];  // unit within the line's jobs
 
   char* const my_ring = ring + wave * Sh::kRing;
   bool first_segment = true;
@@ -442,7 +452,7 @@ void k_attend(AttendKernelArgs k) {
         off = 0;
         if (step0 >= step1) continue;
         const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
-        const bool alone = !kQLds && k.hpj > 1;   // the wave has the head to itself
+        const bool alone = solo || (!kQLds && k.hpj > 1);  // the wave has the head to itself
         const int splits = alone ? 1 : kAttendWaves;
         const int tile0 = step0 * splits * k.step_tiles;
         const int tile1 = min(step1 * splits * k.step_tiles, ntiles);
@@ -532,40 +542,35 @@ void k_attend(AttendKernelArgs k) {
         const float sc = fabsf(sc_signed);
         // ---- queries: row n16 of each 16-row tile, in registers, or for many rows in LDS in the
         // order of the fragments
-        x8 qf[kQLds ? 1 : MT][kQLds ? 1 : KS];
+        x8 qf[kQLds ? 1 : MT][kQLds ? 1 : KS], zq[kQLds ? MT * KS / kAttendWaves : 1];
         int irow[MT];  // block row, or -1 behind the job's last
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int m = mt0 * ROWS + mt * 16 + n16;
-          const int i = m / G;
-          irow[mt] = i < n ? i : -1;
+        auto load_q = [&](int mt, int s) {
+          const int m = mt0 * ROWS + mt * 16 + n16, i = m / G;
           const T* q = static_cast<const T*>(k.a.q) +
                        ((int64_t)r * k.a.blk + (i < n ? i : 0)) * k.a.q_stride +
                        (int64_t)(h * G + (m - i * G)) * dim;
+          // the dims of the lane's K fragment: 16-bit rows, chunk 4 s + g; 8-bit rows, half s % 2 of
+          // chunk 4 (s / 2) + g
+          const int d = F8 ? (4 * (s >> 1) + g) * 16 + (s & 1) * 8 : (4 * s + g) * 8;
+          x8 z = {};
+          if (d < dim && i < n) z = *reinterpret_cast<const x8*>(q + d);
+          return z;
+        };
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            if (kQLds && (mt * KS + s) % kAttendWaves != wave) continue;
-            // the dims of the lane's K fragment: 16-bit rows, chunk 4 s + g; 8-bit rows, half s % 2 of
-            // chunk 4 (s / 2) + g
-            const int d = F8 ? (4 * (s >> 1) + g) * 16 + (s & 1) * 8 : (4 * s + g) * 8;
-            x8 z = {};
-            if (d < dim && i < n) z = *reinterpret_cast<const x8*>(q + d);
-            if (sc_signed < 0.0f) z = -z;
-            if constexpr (kQLds)
-              *reinterpret_cast<x8*>(q_lds + ((mt * KS + s) * 64 + lane) * 16) = z;
-            else
-              qf[mt][s] = z;
+        for (int mt = 0; mt < MT; ++mt) {
+          const int i = (mt0 * ROWS + mt * 16 + n16) / G;
+          irow[mt] = i < n ? i : -1;
+          if constexpr (!kQLds) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[mt][s] = load_q(mt, s);
           }
         }
         if constexpr (kQLds) {
-          __syncthreads();
-        } else {
-          // The queries arrive before the first tile is asked for: a wait for them inside the loop
-          // would also wait for the tiles in flight.
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(qf[mt][s]));
+          for (int f = 0; f < MT * KS / kAttendWaves; ++f) {
+            const int u = f * kAttendWaves + wave;
+            zq[f] = load_q(u / KS, u % KS);
+          }
         }
 
         char* const stage0 = my_ring;
@@ -580,6 +585,23 @@ void k_attend(AttendKernelArgs k) {
             issue(t0 + s, kbase, stage0 + s * Sh::kStage, std::false_type{});
             issue(t0 + s, vbase, stage0 + s * Sh::kStage + TILE, std::true_type{});
           }
+        }
+        // the queries, asked for before the tiles: a wait for them inside the loop would also wait for the
+        // tiles in flight there
+        if constexpr (kQLds) {
+#pragma unroll
+          for (int f = 0; f < MT * KS / kAttendWaves; ++f)
+            *reinterpret_cast<x8*>(q_lds + ((f * kAttendWaves + wave) * 64 + lane) * 16) =
+                sc_signed < 0.0f ? -zq[f] : zq[f];
+          __syncthreads();
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              if (sc_signed < 0.0f) qf[mt][s] = -qf[mt][s];
+              asm volatile("" : "+v"(qf[mt][s]));
+            }
         }
 
         f32x4 acc[MT][NT];
@@ -850,14 +872,14 @@ void k_attend(AttendKernelArgs k) {
             __syncthreads();
           }
         }
-        if (!whole && step0 == 0 && tid == 0 && sub == 0) {  // the job starts here and ends in a later share
-          const int64_t wl = share_of(all, shares, k.shares, k.skew, job_x + units - 1);
-          AttendInfo& o = k.info[w];
+        if (step0 == 0 && tid == 0 && sub == 0 && (!whole || k.by_job)) {  // the job starts here
+          AttendInfo& o = k.info[k.by_job ? (r * k.hgroups + hg) * k.nmt + mt0 : w];
           o.r = r;
           o.h = hg;
           o.mt = mt0;
           o.slot = (int)slot;
-          o.parts = (int)(wl - w) + 1;
+          o.w = w;
+          o.parts = whole ? 0 : (int)(share_of(all, shares, k.shares, k.skew, job_x + units - 1) - w) + 1;
         }
         first_segment = false;
       }
@@ -881,7 +903,7 @@ hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
   }
-  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3(k.used * (Sh::kQLds ? k.hpj : 1)),
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3(k.solo ? (k.used + kAttendWaves - 1) / kAttendWaves : k.used * (Sh::kQLds ? k.hpj : 1)),
                  dim3(kAttendThreads), shm, stream, k);
   return hipGetLastError();
 }

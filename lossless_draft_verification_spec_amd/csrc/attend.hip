@@ -16,6 +16,11 @@ constexpr int kJoinRows = 4;
 // against 14.3 at 250, 16.3 against 15.1 at 500.
 constexpr int64_t kWholePositions = 512, kWholeFewPositions = 256;
 constexpr int kFewHeads = 64;
+// Many of them take a wave each, in row tiles few enough for the queries in registers (no barriers, four
+// jobs at once in a workgroup), from four jobs per workgroup on, up to kSoloPositions from two: 95 lines of
+// 16 heads, 19 rows and 10 positions 76 -> 45 us, 83 lines of one row 30 -> 21; 14 lines of 16 heads and 60
+// positions (half a job per workgroup) would take 22 instead of 16.
+constexpr int64_t kSoloPositions = 128;
 
 // Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
 // the instantiated sizes allow (each group reads every key and value again), then the smallest
@@ -75,7 +80,7 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
   }
 }
 
-// An item is four rows of one head of the job that starts in share w and ends in a later one; its parts
+// An item is four rows of one head of a job that starts in one share and ends in a later one; its parts
 // are added in order, a lane the same 16 bytes of each.  WIDE (few jobs, many parts each): a block per
 // item, its eight waves take every eighth part and are added at the end (4 lines of 130 000 8-bit positions, 64
 // parts a job: 9.0 us, with four waves 10.9).  Otherwise a wave per item.  Blocks behind the items: the
@@ -164,12 +169,16 @@ __global__ __launch_bounds__(64 * join_waves(WIDE)) void k_attend_join(AttendKer
   }
   const int item = WIDE ? blockIdx.x : blockIdx.x * kJoinWaves + wave;
   if (item >= items) return;
-  const int w = item / (k.hpj * quads);
-  const int hi = (item - w * k.hpj * quads) / quads;
+  const int at = item / (k.hpj * quads);
+  const int hi = (item - at * k.hpj * quads) / quads;
   const int row0 = (item % quads) * kJoinRows;
-  const AttendInfo in = k.info[w];
-  if (in.parts == 0) return;
   int L, n;
+  if (k.by_job && (!line_rows(a.len, a.n_new, at / (k.hgroups * k.nmt), a.blk, c.slots, c.page_size, &L,
+                              &n) ||
+                   at % k.nmt * rows >= n * k.G))
+    return;  // no step, no info
+  const AttendInfo in = k.info[at];
+  if (in.parts == 0) return;
   line_rows(a.len, a.n_new, in.r, a.blk, c.slots, c.page_size, &L, &n);
   const int live = min(n * k.G - in.mt * rows, rows) - row0;  // live rows from row0 on
   if (live <= 0) return;
@@ -188,7 +197,7 @@ __global__ __launch_bounds__(64 * join_waves(WIDE)) void k_attend_join(AttendKer
     *reinterpret_cast<typename attend::Elem<T>::x4*>(out) = z;
   };
   Sum sum;
-  sum.run(k, in, w, hi, row0, live, WIDE ? wave : 0, WIDE ? kJoinWaves : 1);
+  sum.run(k, in, in.w, hi, row0, live, WIDE ? wave : 0, WIDE ? kJoinWaves : 1);
   if constexpr (!WIDE) {
 #pragma unroll
     for (int v = 0; v < Sum::NV; ++v) store(v * 64 + lane, sum.o[v], sum.l[v]);
@@ -221,11 +230,12 @@ __global__ __launch_bounds__(64 * join_waves(WIDE)) void k_attend_join(AttendKer
 template <typename T, int DP>
 hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, bool whole,
                           hipStream_t stream) {
-  const int rows = p.mt * 16, items = whole ? 0 : k.used * k.hpj * (p.prow / kJoinRows);
+  const int64_t jobs = (int64_t)k.a.batch * k.hgroups * k.nmt;
+  const int rows = p.mt * 16, items = whole ? 0 : (k.by_job ? (int)jobs : k.used) * k.hpj * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
   const int status = k.a.status ? k.a.batch : 0;
   // fewer jobs than a quarter of the shares: most are cut in many parts
-  if ((int64_t)k.a.batch * k.hgroups * k.nmt * 4 < k.shares)
+  if (jobs * 4 < k.shares)
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
                    dim3(64 * join_waves(true)), 0, stream, k, rows, items, f8);
   else
@@ -262,12 +272,24 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   const int64_t most = (int64_t)a.c.slots * a.c.page_size;
   const bool few = p.hpj > 1 && p.sub == 1 && (int64_t)a.batch * a.c.heads <= kFewHeads;
   const bool whole = most <= (few ? kWholeFewPositions : kWholePositions);
+  int mt = p.mt;
+  if (whole) {
+    const int64_t rows = (int64_t)a.blk * k.G;
+    const int solo_mt = rows > 16 && p.dp <= 128 ? 2 : 1;
+    const int64_t solo_nmt = (rows + 16 * solo_mt - 1) / (16 * solo_mt);
+    const int64_t jobs = a.batch * a.c.heads * solo_nmt;
+    k.solo = jobs >= p.wgs * (most <= kSoloPositions ? 2 : kAttendWaves);
+    if (k.solo) {
+      mt = solo_mt;
+      k.nmt = (int)solo_nmt;
+    }
+  }
   k.hpj = whole ? 1 : p.hpj;
   k.hgroups = a.c.heads / k.hpj;
-  k.shares = whole ? p.wgs : p.wgs / p.sub;
+  k.shares = k.solo ? p.wgs * kAttendWaves : whole ? p.wgs : p.wgs / p.sub;
   k.skew = p.wgs > kAttendCUs ? 2 : 0;
   k.prow = p.prow;
-  const int step = kAttendTile * kAttendWaves;
+  const int step = kAttendTile * (k.solo ? 1 : kAttendWaves);
   k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
   k.job_cost = whole ? 0 : p.hpj > 1 && p.sub == 1 ? 1 : 3;
   // no more workgroups than there can be units
@@ -275,6 +297,7 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   const int64_t steps = (most + tiles * kAttendTile - 1) / (tiles * kAttendTile);
   const int64_t units = (steps + k.job_cost) * k.hgroups * k.nmt * a.batch;
   k.used = (int)(units < k.shares ? units : k.shares);
+  k.by_job = !whole && (int64_t)a.batch * k.hgroups * k.nmt <= k.shares;
   k.ps_magic = (uint32_t)(((uint64_t(1) << 32) + a.c.page_size - 1) / a.c.page_size);
   const int es = f8 ? 1 : 2;
   const int64_t page_bytes = a.c.page_stride * es, row_bytes = a.c.row_stride * es;
@@ -298,9 +321,9 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   }
   hipError_t e;
   if (dtype == PSISPEC_BF16)
-    e = f8 ? launch_attend_bf16_f8(k, p.dp, p.mt, stream) : launch_attend_bf16(k, p.dp, p.mt, stream);
+    e = f8 ? launch_attend_bf16_f8(k, p.dp, mt, stream) : launch_attend_bf16(k, p.dp, mt, stream);
   else
-    e = f8 ? launch_attend_f16_f8(k, p.dp, p.mt, stream) : launch_attend_f16(k, p.dp, p.mt, stream);
+    e = f8 ? launch_attend_f16_f8(k, p.dp, mt, stream) : launch_attend_f16(k, p.dp, mt, stream);
   if (e != hipSuccess) return e;
   if (whole && !a.status) return hipSuccess;
   return dtype == PSISPEC_BF16 ? launch_join<__bf16>(k, p, whole, stream)

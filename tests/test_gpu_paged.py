@@ -202,6 +202,19 @@ def test_attend_short_tables(slots, blk, hkv):
     assert torch.equal(_attend(c), _attend(c, status=st)) and (st == 0).all()
 
 
+@pytest.mark.parametrize("batch,blk,hq,hkv,dim,dtype,cache,longest", [
+    (400, 1, 6, 3, 64, BF, BF, 100), (301, 9, 12, 3, 128, BF, BF, 100), (257, 3, 4, 2, 256, BF, F8, 60),
+    (521, 1, 8, 4, 128, FH, FH, 480), (1100, 2, 1, 1, 80, FH, F8, 30), (103, 20, 20, 5, 128, BF, BF, 40)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_many_short_lines(batch, blk, hq, hkv, dim, dtype, cache, longest, tree):
+    """Enough short jobs for a wave each, idle and empty lines among them."""
+    g = _gen(batch)
+    lens = torch.randint(0, longest + 1, (batch,), generator=g).tolist()
+    live = torch.randint(0, blk + 1, (batch,), generator=g).tolist()
+    lens[3], live[3], live[7] = longest, blk, 0
+    _check_attend(_case(lens, blk, hq, hkv, dim, 16, dtype, cache, seed=batch, live=live, tree=tree))
+
+
 @pytest.mark.parametrize("hkv", [3, 4])
 def test_attend_values_that_are_not_finite_in_cut_lines(hkv):
     """NaN and infinities in block rows of lines that several workgroups share."""
