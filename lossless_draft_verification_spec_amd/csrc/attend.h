@@ -33,9 +33,9 @@
 // unnormalised output in 32 bits) in the workspace and k_attend_join adds them in order.
 //
 // Measured, 32 query and 8 key/value heads of 128 (the kernel, then the join): 64 lines of 1000-8000
-// positions, one row each, 185 us (6.4 TB/s of keys and values) + 5.5; 64 lines of 300-4200, 9 rows, 121
-// (4.7 TB/s) + 6.7; 8 lines of 3500-4500, trees of 33 rows, 71 + 7; 4 lines of 125 000 in 8 bits 162 (6.3
-// TB/s) + 9; one line of 500, 9.8 + 4.9.  The loads alone take 184 and 118 of the first two, the products
+// positions, one row each, 186 us (6.3 TB/s of keys and values) + 5.3; 64 lines of 300-4200, 9 rows, 121
+// (4.7 TB/s) + 7; 8 lines of 3500-4500, trees of 33 rows, 71 + 6; 4 lines of 125 000 in 8 bits 163 (6.3
+// TB/s) + 7; one line of 500, 9.5 + 5.2.  The loads alone take 184 and 118 of the first two, the products
 // and softmax alone 48 and 74: HBM bounds long lines, the ends of jobs (pipeline refilled, waves joined,
 // about 4 us each) short ones, and the three row groups' matrix and softmax work the trees.
 #pragma once
