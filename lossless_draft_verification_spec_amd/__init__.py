@@ -214,6 +214,7 @@ def _sampling(temperature, top_p, seed, step, request_base, flags):
 # the current device's current stream as a raw pointer (torch's own accessor when it has one:
 # torch.cuda.current_stream() builds a Stream object, a few microseconds per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
@@ -564,7 +565,7 @@ class _On:
             if stream.device != dev:
                 raise PsispecError(f"stream is on {stream.device}, expected {dev}")
             return torch.cuda.stream(stream)
-        if torch.cuda.current_device() != dev.index:
+        if _current_device() != dev.index:
             return torch.cuda.device(dev)
         return _NOTHING
 
@@ -587,9 +588,7 @@ def _gpu_device(t: torch.Tensor, name: str):
 
 
 def _flat(t, shape, dtype, dev, name):
-    """Pointer of a contiguous tensor of exactly this shape and type on dev; 0 for None."""
-    if t is None:
-        return 0
+    """Pointer of a contiguous tensor of exactly this shape and type on dev."""
     if t.get_device() != dev.index or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         if t.dtype != dtype or tuple(t.shape) != tuple(shape):
             raise PsispecError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
@@ -629,9 +628,11 @@ def _token_rows(t: torch.Tensor, name: str, dtype, dev):
     if len(shape) != 4:
         raise PsispecError(f"{name} must be [batch][blk][heads][dim]")
     b, n, h, d = shape
+    st = t.stride()
+    if n > 1 and st[3] == 1 and st[2] == d and st[1] >= h * d and (b == 1 or st[0] == n * st[1]):
+        return t.data_ptr(), st[1]
     if t.is_contiguous():
         return t.data_ptr(), h * d
-    st = t.stride()
     rows = st[1] if n > 1 else st[0] if b > 1 else h * d
     if (st[3] != 1 or (h > 1 and st[2] != d) or (n > 1 and b > 1 and st[0] != n * rows)
             or rows < h * d):
@@ -662,9 +663,11 @@ def _paged_cache(k_cache, v_cache, table, batch, dtype, dev, k_scale, v_scale):
         raise PsispecError("k_scale and v_scale go with a float8_e4m3fn cache")
     tp, ts, slots = _table(table, batch, dev)
     return _CACHE_STRUCT.pack(k_cache.data_ptr(), v_cache.data_ptr(),
+                              0 if k_scale is None else
                               _flat(k_scale, (heads,), torch.float32, dev, "k_scale"),
-                              _flat(v_scale, (heads,), torch.float32, dev, "v_scale"), tp, sk[0], sk[1],
-                              sk[2], ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[ct]), heads, dim
+                              0 if v_scale is None else
+                              _flat(v_scale, (heads,), torch.float32, dev, "v_scale"),
+                              tp, sk[0], sk[1], sk[2], ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[ct]), heads, dim
 
 
 def _page_pool(pool: torch.Tensor):
@@ -781,13 +784,13 @@ def psispec_qkv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cach
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         fp = _flat(inv_freq, (rot // 2,), torch.float64, dev, "inv_freq")
-    prep = _PREP_STRUCT.pack(_flat(q_weight, (dim,), dt, dev, "q_weight"),
-                             _flat(k_weight, (dim,), dt, dev, "k_weight"), fp, eps, rope_scale, rot,
-                             PSISPEC_ROPE_INTERLEAVED if interleaved else 0)
+    prep = _PREP_STRUCT.pack(0 if q_weight is None else _flat(q_weight, (dim,), dt, dev, "q_weight"),
+                             0 if k_weight is None else _flat(k_weight, (dim,), dt, dev, "k_weight"),
+                             fp, eps, rope_scale, rot, PSISPEC_ROPE_INTERLEAVED if interleaved else 0)
     lp = _flat(length, (batch,), torch.int32, dev, "length")
-    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
-    pp = _flat(positions, (batch, blk), torch.int32, dev, "positions")
-    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    np_ = 0 if n_new is None else _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    pp = 0 if positions is None else _flat(positions, (batch, blk), torch.int32, dev, "positions")
+    sp = 0 if status is None else _flat(status, (batch,), torch.int32, dev, "status")
     with _On.guard(dev, stream):
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=dev)
@@ -830,9 +833,9 @@ def psispec_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     if cdim != dim:
         raise PsispecError("q and the cache must have the same dim")
     lp = _flat(length, (batch,), torch.int32, dev, "length")
-    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
-    pp = _flat(parent, (batch, blk), torch.int32, dev, "parent")
-    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    np_ = 0 if n_new is None else _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    pp = 0 if parent is None else _flat(parent, (batch, blk), torch.int32, dev, "parent")
+    sp = 0 if status is None else _flat(status, (batch,), torch.int32, dev, "status")
     with _On.guard(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=dt, device=dev)
@@ -867,7 +870,7 @@ def psispec_paged_commit(pool: torch.Tensor, table: torch.Tensor, length: torch.
     tp, ts, slots = _table(table, batch, dev)
     kp = _flat(n_keep, (batch,), torch.int32, dev, "n_keep")
     np_ = lp if new_length is None else _flat(new_length, (batch,), torch.int32, dev, "new_length")
-    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    sp = 0 if status is None else _flat(status, (batch,), torch.int32, dev, "status")
     ks, keepp = 0, 0
     if keep is not None:
         if keep.dim() != 2 or keep.shape[1] < 1:
@@ -903,7 +906,7 @@ def psispec_pages_assign(table: torch.Tensor, refs: torch.Tensor, length: torch.
     rp = _flat(refs, (pages,), torch.int32, dev, "refs")
     srcp = _flat(src, (batch,), torch.int32, dev, "src")
     nlp = _flat(new_length, (batch,), torch.int32, dev, "new_length")
-    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    sp = 0 if status is None else _flat(status, (batch,), torch.int32, dev, "status")
     with _On.guard(dev, stream):
         workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, pages, 1,
                                                                     int(page_size)), dev,
@@ -929,8 +932,8 @@ def psispec_pages_reserve(pool: torch.Tensor, table: torch.Tensor, refs: torch.T
     lp = _flat(length, (batch,), torch.int32, dev, "length")
     tp, ts, slots = _table(table, batch, dev)
     rp = _flat(refs, (pages,), torch.int32, dev, "refs")
-    np_ = _flat(n_new, (batch,), torch.int32, dev, "n_new")
-    sp = _flat(status, (batch,), torch.int32, dev, "status")
+    np_ = 0 if n_new is None else _flat(n_new, (batch,), torch.int32, dev, "n_new")
+    sp = 0 if status is None else _flat(status, (batch,), torch.int32, dev, "status")
     with _On.guard(dev, stream):
         workspace = _workspace_for(workspace, pages_workspace_bytes(batch, slots, pages, int(blk), ps), dev,
                                    "psispec_pages_reserve")
