@@ -26,7 +26,7 @@ template <typename T> struct Vec8;
 template <> struct Vec8<__bf16> { typedef bf16x8 type; };
 template <> struct Vec8<_Float16> { typedef f16x8 type; };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256;  // 512, one pass over 48 heads: 8000 rows 45 us instead of 40
 
 __device__ inline float clamp_e4m3(float x) {
   const float y = fminf(fmaxf(x, -448.0f), 448.0f);

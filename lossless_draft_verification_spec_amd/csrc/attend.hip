@@ -292,6 +292,8 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   k.prow = p.prow;
   const int step = kAttendTile * (k.solo ? 1 : kAttendWaves);
   k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
+  // a job's own cost in steps (queries and page ids fetched, the waves joined): 64 lines of 9 rows 120.0 us
+  // with 3, 120.5 with 2, 121.1 with 4, 124.4 with 6; a wave that has the head to itself joins nothing
   k.job_cost = whole ? 0 : p.hpj > 1 && p.sub == 1 ? 1 : 3;
   // no more workgroups than there can be units
   const int tiles = (p.sub > 1 ? kAttendWaves : kAttendWaves / k.hpj) * k.step_tiles;
