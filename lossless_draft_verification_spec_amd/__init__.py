@@ -667,7 +667,8 @@ def _paged_cache(k_cache, v_cache, table, batch, dtype, dev, k_scale, v_scale):
                               _flat(k_scale, (heads,), torch.float32, dev, "k_scale"),
                               0 if v_scale is None else
                               _flat(v_scale, (heads,), torch.float32, dev, "v_scale"),
-                              tp, sk[0], sk[1], sk[2], ts, pages, ps, slots, heads, dim, _PAGED_DTYPES[ct]), heads, dim
+                              tp, sk[0], sk[1], sk[2], ts, pages, ps, slots, heads, dim,
+                              _PAGED_DTYPES[ct]), heads, dim
 
 
 def _page_pool(pool: torch.Tensor):

@@ -36,8 +36,9 @@
 // positions, one row each, 186 us (6.3 TB/s of keys and values) + 5.3; 64 lines of 300-4200, 9 rows, 121
 // (4.7 TB/s) + 7; 8 lines of 3500-4500, trees of 33 rows, 71 + 6; 4 lines of 125 000 in 8 bits 163 (6.3
 // TB/s) + 7; one line of 500, 9.5 + 5.2.  The loads alone take 184 and 118 of the first two, the products
-// and softmax alone 48 and 74: HBM bounds long lines, the ends of jobs (pipeline refilled, waves joined,
-// about 4 us each) short ones, and the three row groups' matrix and softmax work the trees.
+// and softmax alone 48 and 74.  HBM bounds one row (from L2 the same kernel reads 10-11 TB/s); with three
+// row tiles a tile's own time bounds the waves (5.8 TB/s at most, from L2 as well), then the ends of
+// jobs (pipeline refilled, waves joined, about 4 us each).
 #pragma once
 
 #include <type_traits>
@@ -60,9 +61,10 @@ constexpr int kNonTemporal = 2;
 // beside its steps.  Workgroups are dealt to the 8 XCDs in turn; each XCD gets a contiguous run of
 // shares, so that the row groups and heads that read the same pages meet in one L2.  Of the two
 // workgroups on a CU the one launched later is slower by a seventh, so the shares of the first half
-// of an XCD's workgroups are larger (34 : 30; 64 lines of 9 rows 120.0 us, even shares 122.7), except below two units a share, where the small ones
-// could be empty: a job's parts lie in shares one behind the other.  More, smaller shares given out as
-// places become free even out the rest, and lose more than that to joining.
+// of an XCD's workgroups are larger (34 : 30; 64 lines of 9 rows 120.0 us, even shares 122.7), except
+// below two units a share, where the small ones could be empty: a job's parts lie in shares one behind
+// the other.  More, smaller shares given out as places become free even out the rest, and lose more than
+// that to joining.
 constexpr int kXcds = 8;
 __host__ __device__ inline int64_t share_start(int64_t all, int64_t shares, int R, int skew, int64_t w) {
   if (shares < R) return w;
@@ -903,8 +905,10 @@ hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
   }
-  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3(k.solo ? (k.used + kAttendWaves - 1) / kAttendWaves : k.used * (Sh::kQLds ? k.hpj : 1)),
-                 dim3(kAttendThreads), shm, stream, k);
+  const int blocks = k.solo ? (k.used + kAttendWaves - 1) / kAttendWaves
+                            : k.used * (Sh::kQLds ? k.hpj : 1);
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((unsigned)blocks), dim3(kAttendThreads), shm,
+                 stream, k);
   return hipGetLastError();
 }
 

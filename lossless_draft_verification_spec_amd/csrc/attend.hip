@@ -82,10 +82,10 @@ __global__ __launch_bounds__(256) void k_tree_mask(AttendArgs a, uint64_t* mask,
 
 // An item is four rows of one head of a job that starts in one share and ends in a later one; its parts
 // are added in order, a lane the same 16 bytes of each.  WIDE (few jobs, many parts each): a block per
-// item, its eight waves take every eighth part and are added at the end (4 lines of 125 000 8-bit positions, 64
-// parts a job: 2 us less than with four waves).  The items are counted by jobs, where there are fewer of those
-// than shares (3 lines of 32 rows: 7 us instead of 23; most shares' items would be empty).  Otherwise a wave per item.  Blocks behind the items: the
-// status of one line each.
+// item, its eight waves take every eighth part and are added at the end (4 lines of 125 000 8-bit
+// positions, 64 parts a job: 2 us less than with four waves).  Otherwise a wave per item.  The items are
+// counted by jobs, where there are fewer of those than shares (3 lines of 32 rows: 17 us less; most
+// shares' items would be empty).  Blocks behind the items: the status of one line each.
 constexpr int join_waves(bool wide) { return wide ? 8 : 4; }
 
 // the parts first, first + stride, ... of rows row0 .. row0+3 (live of them)

@@ -29,9 +29,8 @@ psispec_status check_cache(const psispec_paged_cache* c, psispec_dtype dtype) {
   if (c->heads < 1 || c->heads > kMaxHeads || c->dim < 16 || c->dim > kMaxHeadDim || c->dim % 16)
     return PSISPEC_EINVAL;
   const int64_t es = c->dtype == PSISPEC_F8E4M3 ? 1 : 2, most = int64_t(1) << 60;
-  if (c->page_stride > most || c->row_stride > most || c->head_stride > most || c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0 || (c->page_stride * es) % 16 ||
-      (c->row_stride * es) % 16 || (c->head_stride * es) % 16)
-    return PSISPEC_EINVAL;
+  for (const int64_t s : {c->page_stride, c->row_stride, c->head_stride})
+    if (s < 0 || s > most || s * es % 16) return PSISPEC_EINVAL;
   if (c->dtype != PSISPEC_F8E4M3 && (c->k_scale || c->v_scale)) return PSISPEC_EINVAL;
   return PSISPEC_OK;
 }

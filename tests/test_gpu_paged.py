@@ -9,8 +9,8 @@ import torch
 
 import paged_ref as ref
 from lossless_draft_verification_spec_amd import (
-    PsispecError, paged_attention_workspace_bytes, pages_workspace_bytes, psispec_pages_assign, psispec_pages_reserve, psispec_paged_attention,
-    psispec_paged_commit, psispec_qkv_append, psispec_verify_tree, rope_frequencies, workloads)
+    PsispecError, paged_attention_workspace_bytes, pages_workspace_bytes, psispec_paged_attention,
+    psispec_paged_commit, psispec_pages_assign, psispec_pages_reserve, psispec_qkv_append, psispec_verify_tree, rope_frequencies, workloads)
 
 pytestmark = pytest.mark.gpu
 
