@@ -10,7 +10,8 @@ import torch
 import paged_ref as ref
 from lossless_draft_verification_spec_amd import (
     PsispecError, paged_attention_workspace_bytes, pages_workspace_bytes, psispec_paged_attention,
-    psispec_paged_commit, psispec_pages_assign, psispec_pages_reserve, psispec_qkv_append, psispec_verify_tree, rope_frequencies, workloads)
+    psispec_paged_commit, psispec_pages_assign, psispec_pages_reserve, psispec_qkv_append,
+    psispec_verify_tree, rope_frequencies, workloads)
 
 pytestmark = pytest.mark.gpu
 
@@ -371,6 +372,61 @@ def test_attend_pool_beyond_32_bits():
     got = psispec_paged_attention(_gpu(c["q"]), k, v, _gpu(c["table"] + (pages - n)), _gpu(c["lens"]),
                                   scale=c["scale"], k_scale=_gpu(c["ks"]), v_scale=_gpu(c["vs"])).cpu()
     assert torch.equal(got, want)
+
+
+def _guarded(n):
+    """A workspace of n bytes inside a buffer of 165s, and the buffer."""
+    raw = torch.full((n + 8192,), 165, dtype=torch.uint8, device=DEV)
+    return raw[4096:4096 + n], raw
+
+
+def _guards_whole(raw):
+    return bool((raw[:4096] == 165).all() and (raw[-4096:] == 165).all())
+
+
+@pytest.mark.parametrize("batch,blk,hq,hkv,dim,cache,longest,tree", [
+    (1, 1, 8, 8, 128, BF, 4000, False), (5, 9, 16, 4, 128, BF, 3000, True), (3, 50, 8, 4, 64, F8, 900, False),
+    (200, 2, 8, 8, 256, BF, 600, True), (900, 1, 4, 4, 64, BF, 700, False), (700, 3, 4, 2, 128, F8, 60, True),
+    (2, 1024, 2, 1, 64, BF, 100, True)])
+def test_attend_workspace_bounds(batch, blk, hq, hkv, dim, cache, longest, tree):
+    """Nothing outside the workspace and the outputs is written, however the work is cut."""
+    g = _gen(batch + blk)
+    lens = torch.randint(0, longest + 1, (batch,), generator=g).tolist()
+    c = _case(lens, blk, hq, hkv, dim, 16, BF, cache, seed=blk, tree=tree)
+    want = _attend(c)
+    ws, raw = _guarded(paged_attention_workspace_bytes(batch, blk, hq, hkv, dim))
+    rows = torch.full((batch + 2, blk, hq, dim), 5.0, dtype=BF, device=DEV)
+    got = _attend(c, workspace=ws, out=rows[1:-1])
+    assert torch.equal(got, want) and _guards_whole(raw)
+    assert (rows[0] == 5.0).all() and (rows[-1] == 5.0).all()
+
+
+@pytest.mark.parametrize("batch,slots,pages,blk", [(5, 9, 100, 7), (16, 256, 5000, 33), (700, 5, 9000, 1),
+                                                   (1025, 7, 33000, 20), (40, 200, 8200, 900)])
+def test_pages_workspace_bounds(batch, slots, pages, blk):
+    """Calls with guards around the workspace, the table, the counts and the lengths."""
+    ps = 4
+    ws, raw = _guarded(pages_workspace_bytes(batch, slots, pages, blk, ps))
+    held = [torch.full((n + 2048,), 0x25A5A5A5, dtype=torch.int32, device=DEV) for n in
+            (batch * slots, pages, batch, batch)]
+    tab, refs, ln, st = (x[1024:-1024] for x in held)
+    tab.fill_(-1)
+    refs.zero_()
+    ln.zero_()
+    tab = tab.view(batch, slots)
+    pool = torch.zeros((2, pages, ps, 4), dtype=torch.int32, device=DEV)
+    n = torch.full((batch,), min(blk, slots * ps // 2), dtype=torch.int32, device=DEV)
+    psispec_pages_reserve(pool, tab, refs, ln, blk, n_new=n, status=st, workspace=ws)
+    ln.copy_(torch.where(st == 0, n, 0))
+    src = torch.arange(batch, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    psispec_pages_assign(tab, refs, ln, src, ln.flip(0).contiguous(), ps, status=st, workspace=ws)
+    assert (st == 0).all()
+    psispec_pages_reserve(pool, tab, refs, ln, blk, n_new=torch.ones_like(n), status=st, workspace=ws)
+    assert _guards_whole(raw)
+    for x in held:
+        assert (x[:1024] == 0x25A5A5A5).all() and (x[-1024:] == 0x25A5A5A5).all()
+    used = tab[tab >= 0].long()
+    assert torch.equal(torch.bincount(used, minlength=pages).to(torch.int32), refs)
 
 
 # ------------------------------------------------------------------------------------- append
