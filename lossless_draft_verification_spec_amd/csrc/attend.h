@@ -109,7 +109,7 @@ struct AttendKernelArgs {
   int G, nmt, mask_words;
   int shares, skew;          // shares of a full grid; 2: an XCD's first half of them is larger
   int used;                  // shares of this grid, the others have no unit
-  int solo;                  // a share per wave, whole jobs only (not with the queries in LDS)
+  int solo;                  // a job per wave, whole jobs only (not with the queries in LDS)
   int step_tiles;            // tiles of each wave in a step
   int job_cost;              // units of a job beside its steps
   int hpj, hgroups;          // heads per job (1 or 4), groups of them
@@ -368,8 +368,8 @@ void k_attend(AttendKernelArgs k) {
   char* const q_lds = ring + Sh::kRing * kAttendWaves;
   __shared__ float s_m[kAttendWaves][ROWS], s_l[kAttendWaves][ROWS];
   __shared__ int64_t s_scan[kAttendWaves];
-  __shared__ int64_t s_base[kAttendWaves];
-  __shared__ int s_line[kAttendWaves];
+  __shared__ int64_t s_base;
+  __shared__ int s_line;
 
   const AttendArgs& a = k.a;
   const psispec_paged_cache& c = a.c;
@@ -395,36 +395,29 @@ void k_attend(AttendKernelArgs k) {
   const int64_t shares = min(all, (int64_t)k.shares);
   const int nsub = kQLds ? k.hpj : 1;
   const int nth = shares < k.shares ? blockIdx.x : blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-  const bool solo = !kQLds && k.solo;
-  const int w0 = solo ? nth * kAttendWaves : nth / nsub, sub = solo ? 0 : nth - w0 * nsub;
-  const int nw = solo ? kAttendWaves : 1;  // shares of the workgroup
-  if (tid == 0 && sub == 0 && !solo && !k.by_job) k.info[w0].parts = 0;
-  if (w0 >= shares) return;
-  auto locate = [&](int line, int64_t at, int64_t mine) {
-    for (int u = 0; u < nw; ++u) {
-      const int64_t xu = share_start(all, shares, k.shares, k.skew, min((int64_t)w0 + u, shares - 1));
-      if (at <= xu && xu < at + mine) {
-        s_line[u] = line;
-        s_base[u] = at;
-      }
-    }
-  };
-  locate(tid, at0, mine0);
-  const int64_t x_last = share_start(all, shares, k.shares, k.skew, min((int64_t)w0 + nw, shares) - 1);
-  for (int r0 = kAttendThreads; base <= x_last && r0 < a.batch; r0 += kAttendThreads) {
+  const int w = nth / nsub, sub = nth - w * nsub;
+  if (tid == 0 && sub == 0 && !k.by_job) k.info[w].parts = 0;
+  if (w >= shares) return;
+  int64_t x = share_start(all, shares, k.shares, k.skew, w);
+  const int64_t x0 = x, x_end = share_start(all, shares, k.shares, k.skew, w + 1);
+  if (at0 <= x && x < at0 + mine0) {
+    s_line = tid;
+    s_base = at0;
+  }
+  for (int r0 = kAttendThreads; base <= x && r0 < a.batch; r0 += kAttendThreads) {
     const int64_t mine = r0 + tid < a.batch ? line_units<kQLds>(k, r0 + tid, ROWS) : 0;
     int64_t part;
     const int64_t at = base + block_scan(mine, s_scan, &part);
-    locate(r0 + tid, at, mine);
+    if (at <= x && x < at + mine) {
+      s_line = r0 + tid;
+      s_base = at;
+    }
     base += part;
   }
   __syncthreads();
-  const int w = w0 + (solo ? wave : 0);
-  if (w >= shares) return;  // no barrier follows in a solo wave
-  int64_t x = share_start(all, shares, k.shares, k.skew, w);
-  const int64_t x_end = share_start(all, shares, k.shares, k.skew, w + 1);
-  int r = s_line[solo ? wave : 0];
-  int64_t off = x - s_base[solo ? wave : 0];  // unit within the line's jobs
+  int r = s_line;
+  int64_t off = x - s_base;  // unit within the line's jobs
+  const bool solo = !kQLds && k.solo;
 
   char* const my_ring = ring + wave * Sh::kRing;
   bool first_segment = true;
@@ -450,9 +443,12 @@ void k_attend(AttendKernelArgs k) {
         const int take = (int)min((int64_t)units - off, x_end - x);
         const int step0 = max((int)off - k.job_cost, 0);
         const int step1 = max((int)off + take - k.job_cost, 0);
+        // solo: a job is one unit, and the waves take the share's in turn, so that neighbours in time are
+        // neighbouring heads and row groups of the same positions
+        const bool skip = step0 >= step1 || (solo && (int)(x - x0) % kAttendWaves != wave);
         x += take;
         off = 0;
-        if (step0 >= step1) continue;
+        if (skip) continue;
         const int ntiles = (keys + kAttendTile - 1) / kAttendTile;
         const bool alone = solo || (!kQLds && k.hpj > 1);  // the wave has the head to itself
         const int splits = alone ? 1 : kAttendWaves;
@@ -905,10 +901,8 @@ hipError_t launch_one(const AttendKernelArgs& k, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
   }
-  const int blocks = k.solo ? (k.used + kAttendWaves - 1) / kAttendWaves
-                            : k.used * (Sh::kQLds ? k.hpj : 1);
-  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((unsigned)blocks), dim3(kAttendThreads), shm,
-                 stream, k);
+  PSISPEC_LAUNCH("attend", (k_attend<T, F8, DP, MT>), dim3((unsigned)(k.used * (Sh::kQLds ? k.hpj : 1))),
+                 dim3(kAttendThreads), shm, stream, k);
   return hipGetLastError();
 }
 

@@ -16,11 +16,12 @@ constexpr int kJoinRows = 4;
 // against 14.3 at 250, 16.3 against 15.1 at 500.
 constexpr int64_t kWholePositions = 512, kWholeFewPositions = 256;
 constexpr int kFewHeads = 64;
-// Many of them take a wave each, in row tiles few enough for the queries in registers (no barriers, four
-// jobs at once in a workgroup), from four jobs per workgroup on, up to kSoloPositions from two: 95 lines of
-// 16 heads, 19 rows and 10 positions 76 -> 45 us, 83 lines of one row 30 -> 21; 14 lines of 16 heads and 60
-// positions (half a job per workgroup) would take 22 instead of 16.
-constexpr int64_t kSoloPositions = 128;
+// Many of them (two per workgroup and more) take a wave each, in row tiles few enough for the queries in
+// registers: no barriers, four jobs at once in a workgroup.  95 lines of 16 heads, 19 rows and 10
+// positions 76 -> 46 us, 83 lines of one row 30 -> 23; 128 lines of 8 heads, one row of 450 positions 52 -> 48.
+// Where that needs more row groups than the plan has, only up to kSoloPositions: 256 lines of 8 heads and 9
+// rows 79 -> 58 us at 200 positions, but 110 -> 117 at 450.
+constexpr int64_t kSoloPositions = 256;
 
 // Row tiles of a job and jobs per (line, key/value head) for M = blk G query rows.  As few groups as
 // the instantiated sizes allow (each group reads every key and value again), then the smallest
@@ -279,7 +280,7 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
     const int solo_mt = rows > 16 && p.dp <= 128 ? 2 : 1;
     const int64_t solo_nmt = (rows + 16 * solo_mt - 1) / (16 * solo_mt);
     const int64_t jobs = a.batch * a.c.heads * solo_nmt;
-    k.solo = jobs >= p.wgs * (most <= kSoloPositions ? 2 : kAttendWaves);
+    k.solo = jobs >= 2 * p.wgs && (most <= kSoloPositions || solo_nmt == p.nmt);
     if (k.solo) {
       mt = solo_mt;
       k.nmt = (int)solo_nmt;
@@ -287,8 +288,8 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
   }
   k.hpj = whole ? 1 : p.hpj;
   k.hgroups = a.c.heads / k.hpj;
-  k.shares = k.solo ? p.wgs * kAttendWaves : whole ? p.wgs : p.wgs / p.sub;
-  k.skew = p.wgs > kAttendCUs ? 2 : 0;
+  k.shares = whole ? p.wgs : p.wgs / p.sub;
+  k.skew = p.wgs > kAttendCUs && !whole ? 2 : 0;  // whole jobs do not divide so: 119 -> 110 us for that case
   k.prow = p.prow;
   const int step = kAttendTile * (k.solo ? 1 : kAttendWaves);
   k.step_tiles = whole ? (int)((most + step - 1) / step) : 1;
