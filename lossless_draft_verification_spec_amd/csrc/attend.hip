@@ -236,8 +236,9 @@ hipError_t launch_join_dp(const AttendKernelArgs& k, const AttendPlan& p, bool w
   const int rows = p.mt * 16, items = whole ? 0 : (k.by_job ? (int)jobs : k.used) * k.hpj * (p.prow / kJoinRows);
   const int f8 = k.a.c.dtype == PSISPEC_F8E4M3;
   const int status = k.a.status ? k.a.batch : 0;
-  // fewer jobs than a quarter of the shares: most are cut in many parts
-  if (jobs * 4 < k.shares)
+  // Many parts per job, and no more items than CUs: 16 lines of one row (128 items of 16 parts) 5.4 us wide,
+  // 7.3 otherwise; 8 lines of 9 rows (576 items of 8 parts) 9.8 and 4.8, 4 lines (288 of 16) 7.7 and 4.9.
+  if (jobs * 8 <= k.shares && items <= kAttendCUs)
     PSISPEC_LAUNCH("attend_join", (k_attend_join<T, DP, true>), dim3((unsigned)(items + status)),
                    dim3(64 * join_waves(true)), 0, stream, k, rows, items, f8);
   else
