@@ -1,0 +1,99 @@
+"""The paged-cache calls at the borders of their numbers and sizes: small softmax weights under a large
+one, values that are not finite, and the largest sizes."""
+import pytest
+import torch
+
+import paged_ref as ref
+from test_gpu_paged import BF, DEV, F8, FH, _attend, _case, _check_attend, _gen
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [(BF, BF), (FH, FH), (BF, F8), (FH, F8)]
+
+
+# ------------------------------------------------------------------ small weights under a large one
+
+def _sink(c, r, at, depth, mag):
+    """Position at[r] of line r scores `depth` above what it scored and has the value 0; every other
+    value is between mag / 2 and 3 mag / 2, so that nothing cancels in the sums.  (Dimension 0 of the
+    queries is 8 and the scale 1 / 8: dimension 0 of a key is added to its scores.)"""
+    page, off = int(c["table"][r, at // 16]), at % 16
+    c["k"][page, off, :, 0] = torch.tensor(float(depth)).to(c["k"].dtype)
+    c["v"][page, off] = torch.zeros(()).to(c["v"].dtype)
+
+
+def _sink_case(lens, ats, blk, hq, hkv, dim, dtype, cache, depth, spread, mag=1.0, seed=1, **kw):
+    c = _case(lens, blk, hq, hkv, dim, 16, dtype, cache, seed=seed, spread=1.0, **kw)
+    g = _gen(seed + 1)
+    shape = c["k"].shape
+    k = torch.randn(shape, generator=g) * (spread * 8 / (dim - 1) ** 0.5)
+    k[..., 0] = 0.0
+    c["k"] = k.to(cache)
+    c["v"] = (mag * (0.5 + torch.rand(shape, generator=g))).to(cache)
+    c["q"][..., 0] = 8.0
+    c["scale"] = 0.125
+    if cache == F8:
+        c["ks"] = torch.ones(hkv)
+    for r, at in enumerate(ats):
+        if at is not None:
+            _sink(c, r, at, depth, mag)
+    return c
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("L,at", [(8000, 0), (300, 0), (300, 299), (37, 5)])
+@pytest.mark.parametrize("depth", [8, 14, 16, 18, 26, 40])
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+def test_attend_small_weights_under_one_large(dtype, cache, L, at, depth, spread):
+    """One position `depth` nats above all others, with the value 0: the output is what the small
+    weights give."""
+    _check_attend(_sink_case([L], [at], 1, 4, 1, 64, dtype, cache, depth, spread, seed=L + depth))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("dim,blk,hq,hkv,tree", [(64, 9, 8, 2, False), (64, 15, 8, 2, False),
+                                                 (128, 9, 8, 4, True), (128, 3, 12, 4, False),
+                                                 (256, 9, 4, 1, False), (80, 5, 6, 3, True)])
+def test_attend_small_weights_in_row_tiles(dtype, cache, dim, blk, hq, hkv, tree):
+    """The same for every number of row tiles, in cut and uncut lines; values of some hundreds."""
+    lens = [2500, 700, 90, 3, 0]
+    live = [blk, 1, blk, blk // 2, blk]
+    _check_attend(_sink_case(lens, [1, 699, 88, 0, 0], blk, hq, hkv, dim, dtype, cache, 18, 1.0, mag=200.0,
+                             live=live, tree=tree, seed=dim + blk))
+
+
+@pytest.mark.parametrize("dtype,cache", [(FH, FH), (FH, F8)])
+def test_attend_small_weights_in_many_short_lines(dtype, cache):
+    """The same with a wave per line and head."""
+    lens = torch.randint(30, 200, (300,), generator=_gen(3)).tolist()
+    ats = [L // 2 if r % 3 else None for r, L in enumerate(lens)]
+    _check_attend(_sink_case(lens, ats, 1, 4, 4, 128, dtype, cache, 16, 1.0))
+
+
+@pytest.mark.parametrize("dtype,cache", [(FH, FH), (FH, F8)])
+@pytest.mark.parametrize("steps", [[0.0, -12.0, -24.0, -12.0, 0.0], [0.0, -20.0, 6.0, -26.0, 12.0],
+                                   [-30.0, 0.0, -30.0, 30.0, -30.0], [0.0, -44.0, -60.0, -30.0, -50.0]])
+def test_attend_scores_in_steps(dtype, cache, steps):
+    """Runs of positions whose scores lie apart by more than f16's range, up and down; all values of the
+    highest run are 0, so the next one gives the output."""
+    L = 640
+    c = _sink_case([L], [None], 2, 4, 1, 64, dtype, cache, 0, 0.5)
+    for i, s in enumerate(steps):
+        t = torch.arange(i * 128, (i + 1) * 128)
+        page, off = c["table"][0][t // 16].long(), t % 16
+        c["k"][page, off, :, 0] = torch.tensor(s).to(cache)
+        if s == max(steps):
+            c["v"][page, off] = torch.zeros(()).to(cache)
+    # the block's rows as low as the lowest run
+    t = torch.arange(L, L + 2)
+    c["k"][c["table"][0][t // 16].long(), t % 16, :, 0] = torch.tensor(min(steps)).to(cache)
+    _check_attend(c)
+
+
+@pytest.mark.parametrize("cache", [FH, F8])
+def test_attend_tail_of_131072_equal_scores(cache):
+    """A position of value 1 with 131,072 others 18 nats below it, whose sum is 0.2% of its weight."""
+    c = _sink_case([131072], [7], 1, 2, 1, 64, FH, cache, 18, 0.0)
+    page, off = int(c["table"][0, 0]), 7
+    c["v"][page, off] = torch.ones(()).to(cache)
+    _check_attend(c)
