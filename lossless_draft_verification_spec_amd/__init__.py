@@ -740,9 +740,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
         # pair j turns original_length * base^(-2j/rot) / (2 pi) times
         def border(turns):
             return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
-        lo = max(math.floor(border(fast)), 0)
-        hi = min(math.ceil(border(slow)), rot // 2 - 1)
-        mix = ((j - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        # either may lie before the first pair or behind the last: the ramp keeps its slope
+        lo, hi = math.floor(border(fast)), math.ceil(border(slow))
+        mix = ((j - lo) / (hi - lo)).clamp(0, 1)
         f = f * (1 - mix) + f / factor * mix
         mag = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
     elif scaling not in ("none", "base"):

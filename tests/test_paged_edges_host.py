@@ -1,0 +1,46 @@
+"""Host side of the paged-cache calls at the borders of what they take (no GPU: every call here is refused
+or empty), and the frequency tables for long and short original lengths."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import lossless_draft_verification_spec_amd as pkg
+
+P = ctypes.c_void_p(256)
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    return pkg.lib()
+
+
+@pytest.mark.parametrize("rot,base", [(128, 10000.0), (64, 10000.0), (128, 500000.0)])
+@pytest.mark.parametrize("original", [4, 64, 200, 4096, 65536, 131072, 10**7])
+@pytest.mark.parametrize("factor", [4.0, 40.0])
+def test_by_parts_borders(rot, base, original, factor):
+    """Pairs on either side of the borders, and the ramp between them, also where a border lies before the
+    first pair or behind the last."""
+    f, _ = pkg.rope_frequencies(rot, base)
+    got, _ = pkg.rope_frequencies(rot, base, "by_parts", factor, original)
+    j_of = lambda turns: rot * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))
+    lo, hi = math.floor(j_of(32.0)), math.ceil(j_of(1.0))
+    for j in range(rot // 2):
+        turns = original * float(f[j]) / (2 * math.pi)
+        part = min(max((j - lo) / (hi - lo), 0.0), 1.0)  # of the divided frequency
+        want = float(f[j]) * ((1 - part) + part / factor)
+        assert math.isclose(float(got[j]), want, rel_tol=1e-12), j
+        if turns >= 1.0 and j < hi:
+            assert got[j] > f[j] / factor * (1 + 1e-9), "turns more than `slow` times, divided in full"
+        if turns < 32.0 and j > lo:
+            assert got[j] < f[j], "turns less than `fast` times, as it was"
+
+
+def test_by_parts_last_pair():
+    """rot 128, base 10000: the last pair turns 1.2 times in 65536 positions, so it is mixed."""
+    f, _ = pkg.rope_frequencies(128, 10000.0)
+    assert 1.1 < 65536 * float(f[-1]) / (2 * math.pi) < 1.3
+    got, _ = pkg.rope_frequencies(128, 10000.0, "by_parts", 4.0, 65536)
+    assert f[-1] / 4 * 1.01 < got[-1] < f[-1]
