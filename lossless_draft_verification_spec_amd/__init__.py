@@ -722,7 +722,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
                   slower, the fastest as before
       "by_parts"  pairs that turn more than `fast` times within original_length positions as they
                   are, those that turn less than `slow` times divided by factor, in between mixed
-                  linearly in j between the (rounded) borders; values times 0.1 ln(factor) + 1"""
+                  linearly in j between the (rounded) borders; values times 0.1 ln(factor) + 1; base
+                  above 1"""
     if rot < 2 or rot % 2 or not base > 0 or not factor > 0:
         raise PsispecError("rot must be even and positive, base and factor positive")
     j = torch.arange(rot // 2, dtype=torch.float64)
@@ -735,8 +736,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
     if scaling == "linear":
         f = f / factor
     elif scaling == "by_parts":
-        if original_length < 1 or not fast > slow > 0 or base == 1:
-            raise PsispecError("by_parts needs original_length, fast > slow > 0 and a base other than 1")
+        if original_length < 1 or not fast > slow > 0 or not base > 1:  # later pairs turn slower
+            raise PsispecError("by_parts needs original_length, fast > slow > 0 and a base above 1")
         # pair j turns original_length * base^(-2j/rot) / (2 pi) times
         def border(turns):
             return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))

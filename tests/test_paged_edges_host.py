@@ -44,3 +44,10 @@ def test_by_parts_last_pair():
     assert 1.1 < 65536 * float(f[-1]) / (2 * math.pi) < 1.3
     got, _ = pkg.rope_frequencies(128, 10000.0, "by_parts", 4.0, 65536)
     assert f[-1] / 4 * 1.01 < got[-1] < f[-1]
+
+
+def test_by_parts_base_below_one():
+    """Later pairs would turn faster: the borders would stand the wrong way round."""
+    for base in (0.5, 1.0):
+        with pytest.raises(pkg.PsispecError, match="base above 1"):
+            pkg.rope_frequencies(64, base, "by_parts", 4.0, 4096)
