@@ -431,8 +431,10 @@ typedef struct {
  * to positions len[r] .. len[r]+n_keep[r]-1 of line r, in every plane, and new_len[r] becomes
  * len[r] + n_keep[r].  Pages that the block needed stay with the line for its next block.
  *   table      [batch][table_stride] int32, the first `slots` entries of a row used
- *   blk, keep, keep_stride, n_keep   as in psispec_kv_commit (blk 1..1024)
- *   len        [batch] int32 with len + blk <= slots * page_size
+ *   blk, keep, keep_stride, n_keep   as in psispec_kv_commit (blk 1..1024); of a line whose block was
+ *              shorter (n_new) keep names rows of that block: which rows were written is not known here
+ *   len        [batch] int32; the line's first len rows and the kept ones lie within slots * page_size
+ *              positions (all blk rows need not: a short block may end where the table does)
  *   new_len    [batch] int32; len itself, or apart from it
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_KEEP as in psispec_kv_commit,
  *              PSISPEC_ST_BAD_PAGE when a page of the rows that move is not in 0..num_pages-1;

@@ -42,14 +42,14 @@ __device__ inline int commit_check(const PagedCommitArgs& a, int r, int* s_keep,
   if (threadIdx.x == 0) *s_cnt = 0;
   __syncthreads();
   const int ps = a.pool.page_size;
-  bool bad = n < 0 || n > a.blk || L < 0 || (int64_t)L + a.blk > (int64_t)a.slots * ps ||
-             (a.keep && n > a.keep_stride);
+  const int64_t most = (int64_t)a.slots * ps;  // a short block may end at the table's end: blk need not fit
+  bool bad = n < 0 || n > a.blk || L < 0 || (int64_t)L + n > most || (a.keep && n > a.keep_stride);
   bool badpage = false;
   if (!bad && a.keep) {
     const int32_t* tab = a.table + (int64_t)r * a.table_stride;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
       const int k = s_keep[i], kp = i == 0 ? -1 : s_keep[i - 1];
-      if (k < 0 || k >= a.blk || k <= kp) {
+      if (k < 0 || k >= a.blk || k <= kp || (int64_t)L + k >= most) {
         bad = true;
       } else if (k != i) {
         // keep is strictly increasing from keep[0] >= 0, so once keep[i] > i every later row moves

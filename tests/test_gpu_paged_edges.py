@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import paged_ref as ref
+from lossless_draft_verification_spec_amd import (
+    psispec_paged_attention, psispec_paged_commit, psispec_pages_reserve, psispec_qkv_append)
 from test_gpu_paged import BF, DEV, F8, FH, _attend, _case, _check_attend, _gen
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +99,73 @@ def test_attend_tail_of_131072_equal_scores(cache):
     page, off = int(c["table"][0, 0]), 7
     c["v"][page, off] = torch.ones(()).to(cache)
     _check_attend(c)
+
+
+# ------------------------------------------------------------------ the end of a table
+
+def test_short_blocks_at_the_end_of_the_table():
+    """Lines whose short block ends with the last slot, and a full idle line, through reserve, append,
+    attention and commit."""
+    ps, slots, blk, hq, hkv, dim = 16, 3, 9, 4, 2, 64
+    lens, live, kept = [44, 48, 40, 46, 10], [4, 0, 8, 2, 9], [4, 0, 3, 2, 5]
+    g, batch = _gen(5), 5
+    pages = batch * slots
+    pool = torch.randn((2, pages, ps, hkv, dim), generator=g).to(BF).to(DEV)
+    tab = torch.full((batch, slots), -1, dtype=torch.int32)
+    for r, L in enumerate(lens):
+        tab[r, :-(-L // ps)] = torch.arange(r * slots, r * slots - (-L // ps))
+    refs = torch.zeros(pages, dtype=torch.int32)
+    refs[tab[tab >= 0].long()] = 1
+    tab, refs = tab.to(DEV), refs.to(DEV)
+    ln, n = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, live))
+    st = torch.full((batch,), -1, dtype=torch.int32, device=DEV)
+
+    def fine():
+        ok = (st == 0).all()
+        st.fill_(-1)
+        return ok
+
+    psispec_pages_reserve(pool, tab, refs, ln, blk, n_new=n, status=st)
+    assert fine()
+    qkv = torch.randn((batch, blk, hq + 2 * hkv, dim), generator=g).to(BF).to(DEV)
+    q = psispec_qkv_append(*qkv.split([hq, hkv, hkv], 2), pool[0], pool[1], tab, ln, n_new=n, status=st)
+    assert fine()
+    out = psispec_paged_attention(q, pool[0], pool[1], tab, ln, n_new=n, status=st)
+    assert fine()
+    want, bound = ref.attention(q.cpu(), pool[0].cpu(), pool[1].cpu(), tab.cpu(), lens, live, None, dim**-0.5)
+    for r in range(batch):
+        assert ((out.cpu().double() - want)[r, :live[r]].abs() <= bound[r, :live[r]]).all()
+    nk = torch.tensor(kept, dtype=torch.int32, device=DEV)
+    new = torch.full_like(ln, -9)
+    psispec_paged_commit(pool, tab, ln, blk, nk, new_length=new, status=st)  # a prefix
+    assert fine() and torch.equal(new, ln + nk)
+    keep = torch.full((batch, 5), -1, dtype=torch.int32)
+    for r, rows in enumerate([[0, 1, 2, 3], [], [1, 6, 7], [0, 1], [0, 2, 3, 5, 8]]):
+        keep[r, :len(rows)] = torch.tensor(rows, dtype=torch.int32)
+    before, tabc = pool.cpu(), tab.cpu()
+    psispec_paged_commit(pool, tab, ln, blk, nk, keep=keep.to(DEV), status=st)  # a path, lengths in place
+    assert fine() and ln.cpu().tolist() == [L + k for L, k in zip(lens, kept)]
+    after = pool.cpu()
+    for r, L in enumerate(lens):
+        for i in range(kept[r]):
+            s, d = L + int(keep[r, i]), L + i
+            assert torch.equal(after[:, tabc[r, d // ps], d % ps], before[:, tabc[r, s // ps], s % ps])
+
+
+def test_commit_rows_behind_the_table():
+    """A kept row, or a kept count, that the table has no position for."""
+    pool = torch.zeros((1, 8, 4, 4), dtype=torch.int32, device=DEV)
+    tab = torch.arange(8, dtype=torch.int32, device=DEV).view(4, 2)
+    ln = torch.tensor([4, 5, 8, 2**31 - 1], dtype=torch.int32, device=DEV)
+    st = torch.full((4,), -1, dtype=torch.int32, device=DEV)
+    nk = torch.tensor([1, 4, 0, 1], dtype=torch.int32, device=DEV)
+    new = torch.zeros_like(ln)
+    psispec_paged_commit(pool, tab, ln, 6, nk, new_length=new, status=st)
+    assert st.tolist() == [0, ref.BAD_KEEP, 0, ref.BAD_KEEP] and new.tolist() == [5, 5, 8, 2**31 - 1]
+    keep = torch.tensor([[4], [3], [0], [0]], dtype=torch.int32, device=DEV)
+    nk.fill_(1)
+    psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=new, status=st)
+    assert st.tolist() == [ref.BAD_KEEP] * 4 and torch.equal(new, ln)
+    keep[:2, 0] = torch.tensor([3, 2])
+    psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=new, status=st)
+    assert st.tolist() == [0, 0, ref.BAD_KEEP, ref.BAD_KEEP] and new.tolist() == [5, 6, 8, 2**31 - 1]
