@@ -356,7 +356,7 @@ typedef struct {
  *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] have no effect and are not
  *              written
  *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride, and
- *              overlaps no input otherwise
+ *              overlaps no input otherwise (PSISPEC_EINVAL when it lies over q, k or v)
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when len < 0, n_new is outside [0, blk]
  *              or the rows do not fit the slots (nothing of the line is then written, q_out
  *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a

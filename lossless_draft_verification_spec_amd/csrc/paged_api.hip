@@ -55,14 +55,25 @@ bool places_apart(const psispec_paged_cache* c) {
   return true;
 }
 
-// Rows of `width` elements, n of them, at two places: some element is in both.  Rows of equal stride
+// n rows of wa elements, sa apart, and n of wb, sb apart: some element is in both.  Rows of equal stride
 // may lie between each other (two parts of one packed projection).
-bool rows_overlap(const void* a, int64_t sa, const void* b, int64_t sb, int64_t n, int64_t width) {
+bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t n) {
   const __int128 d = ((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / 2;
-  if (d >= (__int128)sa * (n - 1) + width || -d >= (__int128)sb * (n - 1) + width) return false;
-  if (sa != sb) return true;
-  const int64_t m = (int64_t)((d % sa + sa) % sa);
-  return m < width || sa - m < width;
+  if (d >= (__int128)sa * (n - 1) + wa || -d >= (__int128)sb * (n - 1) + wb) return false;
+  if (sa == sb) {
+    const int64_t m = (int64_t)((d % sa + sa) % sa);
+    return m < wa || sa - m < wb;
+  }
+  for (int64_t i = 0, j = 0; i < n && j < n;) {  // one within the other: rare
+    const __int128 at = (__int128)sa * i, bt = d + (__int128)sb * j;
+    if (at + wa <= bt)
+      ++i;
+    else if (bt + wb <= at)
+      ++j;
+    else
+      return true;
+  }
+  return false;
 }
 
 bool cache_pointers_ok(const psispec_paged_cache* c) {
@@ -117,7 +128,11 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
       !rows_ok(q_out, q_out_stride, wq))
     return PSISPEC_EINVAL;
   const int64_t rows = (int64_t)batch * blk;
-  if (!(q_out == q && q_out_stride == q_stride) && rows_overlap(q, q_stride, q_out, q_out_stride, rows, wq))
+  if (!(q_out == q && q_out_stride == q_stride) &&
+      rows_overlap(q, q_stride, wq, q_out, q_out_stride, wq, rows))
+    return PSISPEC_EINVAL;
+  if (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
+      rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows))
     return PSISPEC_EINVAL;
   AppendArgs a{};
   a.c = *c;
@@ -167,7 +182,7 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
   if (batch == 0) return PSISPEC_OK;
   const int64_t wq = (int64_t)heads_q * c->dim;
   if (!cache_pointers_ok(c) || !len || !rows_ok(q, q_stride, wq) || !rows_ok(out, out_stride, wq) ||
-      rows_overlap(q, q_stride, out, out_stride, (int64_t)batch * blk, wq))
+      rows_overlap(q, q_stride, wq, out, out_stride, wq, (int64_t)batch * blk))
     return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attend_workspace_bytes(batch, blk, heads_q, c->heads, c->dim))

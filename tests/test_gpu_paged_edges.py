@@ -5,8 +5,8 @@ import torch
 
 import paged_ref as ref
 from lossless_draft_verification_spec_amd import (
-    psispec_paged_attention, psispec_paged_commit, psispec_pages_reserve, psispec_qkv_append)
-from test_gpu_paged import BF, DEV, F8, FH, _attend, _case, _check_attend, _gen
+    PsispecError, psispec_paged_attention, psispec_paged_commit, psispec_pages_reserve, psispec_qkv_append)
+from test_gpu_paged import (BF, DEV, F8, FH, _append_case, _attend, _case, _check_attend, _gen, _gpu)
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,41 @@ def test_commit_rows_behind_the_table():
     keep[:2, 0] = torch.tensor([3, 2])
     psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=new, status=st)
     assert st.tolist() == [0, 0, ref.BAD_KEEP, ref.BAD_KEEP] and new.tolist() == [5, 6, 8, 2**31 - 1]
+
+
+# ------------------------------------------------------------------ where outputs may lie
+
+def test_append_output_beside_its_inputs():
+    """q, k, v and q_out as parts of one packed buffer, q_out within the gaps of other rows, and refused
+    over k and v."""
+    c = _append_case([40, 20], 3, 4, 2, 64, 16, BF, BF, seed=3, rot=64)
+    kw = dict(q_weight=_gpu(c["qw"]), k_weight=_gpu(c["kw"]), inv_freq=_gpu(c["f"]))
+
+    def run(q, k, v, out):
+        kc, vc = _gpu(c["kc"]), _gpu(c["vc"])
+        psispec_qkv_append(q, k, v, kc, vc, _gpu(c["table"]), _gpu(c["lens"]), q_out=out, **kw)
+        return out, kc, vc
+
+    qkv = _gpu(c["qkv"])
+    want = run(*qkv.split([4, 2, 2], 2), torch.empty((2, 3, 4, 64), dtype=BF, device=DEV))
+    raw = torch.zeros((2, 3, 12, 64), dtype=BF, device=DEV)
+    raw[:, :, :8] = qkv
+    q, k, v, out = raw.split([4, 2, 2, 4], 2)
+    for got, x in zip(run(q, k, v, out), want):
+        assert torch.equal(got, x)
+    raw[:, :, :8] = qkv
+    for got, x in zip(run(q, k, v, q), want):  # in place
+        assert torch.equal(got, x)
+    # k's six rows with gaps, all rows of q_out in the first of them
+    raw = torch.zeros((2, 3, 2 + 6 * 4, 64), dtype=BF, device=DEV)
+    k = raw[:, :, :2]
+    k.copy_(qkv[:, :, 4:6])
+    out = raw[0, 0, 2:].view(2, 3, 4, 64)
+    for got, x in zip(run(qkv[:, :, :4], k, qkv[:, :, 6:], out), want):
+        assert torch.equal(got, x)
+    raw = qkv.clone()
+    q, k, v = raw.split([4, 2, 2], 2)
+    for out in (raw[:, :, 2:6], raw[:, :, 4:8]):
+        with pytest.raises(PsispecError, match="invalid argument"):
+            run(qkv[:, :, :4].clone(), k, v, out)
+    assert torch.equal(raw, qkv)

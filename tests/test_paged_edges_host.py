@@ -51,3 +51,31 @@ def test_by_parts_base_below_one():
     for base in (0.5, 1.0):
         with pytest.raises(pkg.PsispecError, match="base above 1"):
             pkg.rope_frequencies(64, base, "by_parts", 4.0, 4096)
+
+
+def _cache(**kw):
+    """8 pages of 16 positions of 2 heads of 64 at 2^30 (K) and 2^31 (V)."""
+    return pkg.psispec_paged_cache(**{**dict(
+        k=1 << 30, v=1 << 31, k_scale=None, v_scale=None, table=256, page_stride=16 * 2 * 64,
+        row_stride=128, head_stride=64, table_stride=4, num_pages=8, page_size=16, slots=4, heads=2, dim=64,
+        dtype=pkg.PSISPEC_BF16), **kw})
+
+
+def _append(L, c=None, batch=1, blk=2, hq=4, q=1 << 20, qs=512, k=2 << 20, ks=512, v=3 << 20, vs=512, qo=4 << 20,
+            os=512, ln=256, nn=None, pos=None, st=None):
+    """One row of q is 256 elements, one of k or v 128."""
+    p = pkg.psispec_qkv_prep(q_weight=None, k_weight=None, inv_freq=256, eps=1e-6, rope_scale=1.0, rot=64,
+                             flags=0)
+    return L.psispec_qkv_append(ctypes.byref(c or _cache()), ctypes.byref(p), q, qs, k, ks, v, vs,
+                                pkg.PSISPEC_BF16, batch, blk, hq, pos, ln, nn, qo, os, st, None)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_append_output_over_keys_or_values(L, which):
+    """q_out over the rows of k or v: from the same place, ends that meet, other strides."""
+    at = 4 << 20  # q_out: rows of 512 bytes at 4 MiB, 1024 bytes apart
+    for off in (0, 256, -240, 496, 1024, 1024 - 240, 1024 + 496):
+        assert _append(L, **{which: at + off}) == -1, off
+    for off, s in ((0, 136), (-272, 136), (512, 264)):
+        assert _append(L, **{which: at + off, which + "s": s}) == -1, off
+    assert _append(L, **{which: 1 << 20, "qo": 1 << 20}) == -1  # in place, with k or v over q
