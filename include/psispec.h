@@ -356,7 +356,7 @@ typedef struct {
  *   n_new      [batch] int32 in [0, blk], or NULL: rows i >= n_new[r] have no effect and are not
  *              written
  *   q_out      row (r, i) at (r * blk + i) * q_out_stride; may be q itself with q_stride, and
- *              overlaps no input otherwise (PSISPEC_EINVAL when it lies over q, k or v)
+ *              overlaps no input otherwise (PSISPEC_EINVAL when it lies over q, k, v or the cache)
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE when len < 0, n_new is outside [0, blk]
  *              or the rows do not fit the slots (nothing of the line is then written, q_out
  *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a
@@ -388,7 +388,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
  * cache holds there.  Infinities among what it sees give infinities or NaN.
  *   q, out     row (r, i) at (r * blk + i) * stride elements: heads_q heads of c->dim contiguous
  *              elements; dtype PSISPEC_BF16 or PSISPEC_F16; 16-byte aligned, strides multiples of 8;
- *              out overlaps no input
+ *              out overlaps no input (PSISPEC_EINVAL when it lies over q or the cache)
  *   parent     [batch][blk] int32: the block row that row j follows, -1 = the line's last position;
  *              must be < j.  NULL: row j follows row j-1
  *   len, n_new as in psispec_qkv_append; rows i >= n_new[r] of out are left as they are

@@ -35,9 +35,16 @@ psispec_status check_cache(const psispec_paged_cache* c, psispec_dtype dtype) {
   return PSISPEC_OK;
 }
 
-// No two (page, position, head) share an element: from the smallest stride on, each is at least what
-// the ones before it span.
-bool places_apart(const psispec_paged_cache* c) {
+// The places of a cache's heads in bytes: the three strides (pages, positions, heads) in increasing
+// order, those of one only left out; span[i]: what the first i of them reach over, span[0] a head.
+struct Places {
+  int levels;
+  bool apart;  // no two places share a byte: every stride is at least the span of the ones before it
+  int64_t stride[3], count[3];
+  __int128 span[4];
+};
+Places cache_places(const psispec_paged_cache* c) {
+  const int64_t es = c->dtype == PSISPEC_F8E4M3 ? 1 : 2;
   int64_t stride[3] = {c->head_stride, c->row_stride, c->page_stride};
   int64_t count[3] = {c->heads, c->page_size, c->num_pages};
   for (int i = 0; i < 3; ++i)
@@ -46,13 +53,45 @@ bool places_apart(const psispec_paged_cache* c) {
         std::swap(stride[i], stride[j]);
         std::swap(count[i], count[j]);
       }
-  __int128 span = c->dim;
+  Places p{};
+  p.apart = true;
+  p.span[0] = c->dim * es;
   for (int i = 0; i < 3; ++i) {
     if (count[i] == 1) continue;
-    if (stride[i] < span) return false;
-    span += (__int128)stride[i] * (count[i] - 1);
+    p.stride[p.levels] = stride[i] * es;
+    p.count[p.levels] = count[i];
+    p.apart &= p.stride[p.levels] >= p.span[p.levels];
+    p.span[p.levels + 1] = p.span[p.levels] + (__int128)p.stride[p.levels] * (count[i] - 1);
+    ++p.levels;
   }
-  return true;
+  return p;
+}
+
+// Bytes [lo, hi) behind the first place, of the first n levels: some place has one of them.
+bool bytes_in_places(const Places& p, int n, __int128 lo, __int128 hi) {
+  if (hi <= 0 || lo >= p.span[n]) return false;
+  if (n == 0 || !p.apart) return true;  // places within each other (read-only caches): their whole range
+  const __int128 s = p.stride[n - 1], below = p.span[n - 1];
+  const __int128 c0 = lo < below ? 0 : (lo - below) / s + 1;  // the first part that ends behind lo
+  const __int128 c1 = (hi - 1) / s < p.count[n - 1] ? (hi - 1) / s : p.count[n - 1] - 1;
+  if (c1 - c0 > 1) return true;  // a whole part in between
+  for (__int128 c = c0; c <= c1; ++c)
+    if (bytes_in_places(p, n - 1, lo - c * s, hi - c * s)) return true;
+  return false;
+}
+
+// n rows of `width` 2-byte elements, `stride` elements apart: some byte is the cache's (K or V).
+bool rows_in_cache(const psispec_paged_cache* c, const void* rows, int64_t stride, int64_t width, int64_t n) {
+  const Places p = cache_places(c);
+  for (const void* base : {c->k, c->v}) {
+    const __int128 at = (__int128)(uintptr_t)rows - (__int128)(uintptr_t)base;
+    if (at >= p.span[p.levels] || at + 2 * ((__int128)stride * (n - 1) + width) <= 0) continue;
+    for (int64_t i = 0; i < n; ++i) {  // within the cache's range: rare
+      const __int128 lo = at + 2 * (__int128)stride * i;
+      if (bytes_in_places(p, p.levels, lo, lo + 2 * width)) return true;
+    }
+  }
+  return false;
 }
 
 // n rows of wa elements, sa apart, and n of wb, sb apart: some element is in both.  Rows of equal stride
@@ -115,7 +154,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
   if (e != PSISPEC_OK) return e;
   if (batch < 0 || blk < 1 || blk > kMaxAppendBlock || heads_q < 1 || heads_q > kMaxHeads || !p)
     return PSISPEC_EINVAL;
-  if (!places_apart(c)) return PSISPEC_EINVAL;
+  if (!cache_places(c).apart) return PSISPEC_EINVAL;
   if (!(p->eps >= 0.0) || !isfinite(p->eps) || !isfinite(p->rope_scale) || p->rot < 0 ||
       p->rot > c->dim || p->rot % 16 || (p->flags & ~PSISPEC_ROPE_INTERLEAVED) ||
       (p->rot > 0 && !p->inv_freq) || !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16))
@@ -132,7 +171,8 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
       rows_overlap(q, q_stride, wq, q_out, q_out_stride, wq, rows))
     return PSISPEC_EINVAL;
   if (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
-      rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows))
+      rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows) ||
+      rows_in_cache(c, q_out, q_out_stride, wq, rows))
     return PSISPEC_EINVAL;
   AppendArgs a{};
   a.c = *c;
@@ -182,7 +222,8 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
   if (batch == 0) return PSISPEC_OK;
   const int64_t wq = (int64_t)heads_q * c->dim;
   if (!cache_pointers_ok(c) || !len || !rows_ok(q, q_stride, wq) || !rows_ok(out, out_stride, wq) ||
-      rows_overlap(q, q_stride, wq, out, out_stride, wq, (int64_t)batch * blk))
+      rows_overlap(q, q_stride, wq, out, out_stride, wq, (int64_t)batch * blk) ||
+      rows_in_cache(c, out, out_stride, wq, (int64_t)batch * blk))
     return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attend_workspace_bytes(batch, blk, heads_q, c->heads, c->dim))

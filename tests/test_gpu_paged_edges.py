@@ -207,3 +207,30 @@ def test_append_output_beside_its_inputs():
         with pytest.raises(PsispecError, match="invalid argument"):
             run(qkv[:, :, :4].clone(), k, v, out)
     assert torch.equal(raw, qkv)
+
+
+def test_outputs_in_the_gaps_of_a_cache():
+    """Pages with a gap behind each: outputs there are taken, over a page they are refused."""
+    c = _append_case([40, 20], 3, 4, 2, 64, 16, BF, BF, seed=4, rot=64)
+    tab, ln = _gpu(c["table"]), _gpu(c["lens"])
+    q, k, v = _gpu(c["qkv"]).split([4, 2, 2], 2)
+    kw = dict(inv_freq=_gpu(c["f"]))
+    near = [_gpu(c["kc"]), _gpu(c["vc"])]
+    want_q = psispec_qkv_append(q, k, v, *near, tab, ln, **kw)
+    want = psispec_paged_attention(want_q, *near, tab, ln)
+    pages = near[0].shape[0]
+    raw = torch.zeros((2, pages, 40, 2, 64), dtype=BF, device=DEV)  # 16 positions and a gap of 24
+    far = [raw[0, :, :16], raw[1, :, :16]]
+    for x, y in zip(far, (c["kc"], c["vc"])):
+        x.copy_(y)
+    gap = raw[0, 1, 16:].flatten()
+    q_out, out = gap[:1536].view(2, 3, 4, 64), gap[1536:3072].view(2, 3, 4, 64)
+    psispec_qkv_append(q, k, v, *far, tab, ln, q_out=q_out, **kw)
+    psispec_paged_attention(q_out, *far, tab, ln, out=out)
+    assert torch.equal(q_out, want_q) and torch.equal(out, want)
+    assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+    over = raw.flatten()[5120 - 8:5120 + 1536 - 8].view(2, 3, 4, 64)  # up to the next page and into it
+    for call in (lambda: psispec_qkv_append(q, k, v, *far, tab, ln, q_out=over, **kw),
+                 lambda: psispec_paged_attention(want_q, *far, tab, ln, out=over)):
+        with pytest.raises(PsispecError, match="invalid argument"):
+            call()

@@ -79,3 +79,44 @@ def test_append_output_over_keys_or_values(L, which):
     for off, s in ((0, 136), (-272, 136), (512, 264)):
         assert _append(L, **{which: at + off, which + "s": s}) == -1, off
     assert _append(L, **{which: 1 << 20, "qo": 1 << 20}) == -1  # in place, with k or v over q
+
+
+def _attend(L, c, out, os=256, batch=1, blk=2, hq=4, **kw):
+    a = dict(parent=None, ln=256, nn=None, st=None, scale=1.0, ws=None, dtype=pkg.PSISPEC_BF16)
+    a.update(kw)
+    return L.psispec_paged_attention(ctypes.byref(c), 1 << 20, 512, a["dtype"], batch, blk, hq, a["parent"],
+                                     a["ln"], a["nn"], a["scale"], out, os, a["st"], a["ws"], BIG, None)
+
+
+def test_outputs_over_the_cache(L):
+    """Rows of 256 elements over places of K and V, at their ends, and in the gaps between places: only
+    the missing workspace is then left to refuse."""
+    K, V = 1 << 30, 1 << 31
+    page = 16 * 2 * 64 * 2  # bytes
+    for base in (K, V):
+        for at in (base, base - 1024, base - 496, base + 8 * page - 16, base + page + 32, base - 512):
+            meets = at + 1024 > base  # two rows of 512 bytes
+            assert _attend(L, _cache(), at) == (-1 if meets else -3), at - base
+            if meets:
+                assert _append(L, qo=at, os=256) == -1
+        assert _attend(L, _cache(), base + 8 * page) == -3
+        assert _attend(L, _cache(), base - 512, os=1 << 20) == -3  # the second row far behind the cache
+        assert _attend(L, _cache(), base - page, os=page // 2) == -1
+    # pages with a gap of their size behind each; heads with gaps
+    wide = _cache(page_stride=2 * 16 * 2 * 64)
+    for at, rc in ((0, -1), (page, -3), (2 * page - 1024, -3), (2 * page - 512, -1), (2 * page, -1),
+                   (page - 16, -1), (15 * page, -3)):
+        assert _attend(L, wide, K + at) == rc, at
+    heads = _cache(head_stride=1024, row_stride=2048, page_stride=16 * 2048)
+    for at, rc in ((0, -1), (128, -3), (2048 - 512, -3), (2048 - 496, -1)):
+        assert _attend(L, heads, K + at, blk=1) == rc, at
+    # positions before pages before heads (any order), and 8-bit places of half the bytes
+    mixed = _cache(page_stride=64, row_stride=8 * 64, head_stride=1 << 16)
+    assert _attend(L, mixed, K + 16 * 8 * 128) == -3 and _attend(L, mixed, K + (1 << 17)) == -1
+    f8 = _cache(dtype=pkg.PSISPEC_F8E4M3)
+    assert _attend(L, f8, K + 4 * page) == -3 and _attend(L, f8, K + 4 * page - 16) == -1
+    # a cache whose pages are one page: read-only, its whole range counts
+    assert _attend(L, _cache(page_stride=0), K + page) == -3
+    assert _attend(L, _cache(page_stride=0), K + page - 16) == -1
+    far = _cache(page_stride=1 << 59, num_pages=1 << 30)
+    assert _attend(L, far, K + page) == -3 and _attend(L, far, K) == -1
