@@ -362,8 +362,10 @@ typedef struct {
  *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a
  *              page are then not written, q_out included)
  *   blk 1..2^20;  batch >= 0 (0 launches nothing);  heads_q >= 1
- * No two (page, position, head) of the cache share an element.  The pages written must be the line's
- * own (psispec_pages_reserve sees to it): rows of two lines in one page position race.
+ * No two (page, position, head) of the cache share an element, nor do K and V (PSISPEC_EINVAL).  The
+ * pages written must be the line's own (psispec_pages_reserve sees to it): rows of two lines in one
+ * page position race.  The inputs q, k and v lie outside the cache, but for rows of k or v that are
+ * already in the very places that they go to, in a cache of their type.
  * Asynchronous on `stream`; no workspace.
  */
 psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qkv_prep* p,

@@ -80,6 +80,17 @@ bool bytes_in_places(const Places& p, int n, __int128 lo, __int128 hi) {
   return false;
 }
 
+// Places `d` bytes behind each other of the first n levels (which lie apart): some two share a byte.
+bool shifted_places_meet(const Places& p, int n, __int128 d) {
+  if (d >= p.span[n] || -d >= p.span[n]) return false;
+  if (n == 0) return true;
+  const __int128 s = p.stride[n - 1], most = p.count[n - 1] - 1;
+  const __int128 c = d >= 0 ? d / s : -((-d + s - 1) / s);  // d lies between c and c + 1 parts
+  for (const __int128 x : {c, c + 1})
+    if (x >= -most && x <= most && shifted_places_meet(p, n - 1, d - x * s)) return true;
+  return false;
+}
+
 // n rows of `width` 2-byte elements, `stride` elements apart: some byte is the cache's (K or V).
 bool rows_in_cache(const psispec_paged_cache* c, const void* rows, int64_t stride, int64_t width, int64_t n) {
   const Places p = cache_places(c);
@@ -173,6 +184,9 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
   if (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
       rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows) ||
       rows_in_cache(c, q_out, q_out_stride, wq, rows))
+    return PSISPEC_EINVAL;
+  const Places places = cache_places(c);
+  if (shifted_places_meet(places, places.levels, (__int128)(uintptr_t)c->v - (__int128)(uintptr_t)c->k))
     return PSISPEC_EINVAL;
   AppendArgs a{};
   a.c = *c;

@@ -234,3 +234,49 @@ def test_outputs_in_the_gaps_of_a_cache():
                  lambda: psispec_paged_attention(want_q, *far, tab, ln, out=over)):
         with pytest.raises(PsispecError, match="invalid argument"):
             call()
+
+
+@pytest.mark.parametrize("order", ["rows", "halves", "turns", "heads"])
+def test_append_keys_beside_values(order):
+    """K and V side by side in each position, in halves of a page, in pages in turn, and in heads in turn; one
+    over the other is refused."""
+    c = _append_case([40, 20], 3, 4, 2, 64, 16, BF, BF, seed=5, rot=64)
+    tab, ln = _gpu(c["table"]), _gpu(c["lens"])
+    q, k, v = _gpu(c["qkv"]).split([4, 2, 2], 2)
+    near = [_gpu(c["kc"]), _gpu(c["vc"])]
+    want = psispec_qkv_append(q, k, v, *near, tab, ln, inv_freq=_gpu(c["f"]))
+    n = near[0].shape[0]
+    if order == "rows":
+        raw = torch.zeros((n, 16, 2, 2, 64), dtype=BF, device=DEV)
+        far = [raw[:, :, 0], raw[:, :, 1]]
+    elif order == "halves":
+        raw = torch.zeros((n, 2, 2, 16, 64), dtype=BF, device=DEV)
+        far = [raw[:, 0].transpose(1, 2), raw[:, 1].transpose(1, 2)]
+    elif order == "turns":
+        raw = torch.zeros((n, 2, 16, 2, 64), dtype=BF, device=DEV)
+        far = [raw[:, 0], raw[:, 1]]
+    else:
+        raw = torch.zeros((n, 16, 2, 2, 64), dtype=BF, device=DEV)
+        far = [raw[:, :, :, 0], raw[:, :, :, 1]]
+    for x, y in zip(far, (c["kc"], c["vc"])):
+        x.copy_(y)
+    got = psispec_qkv_append(q, k, v, *far, tab, ln, inv_freq=_gpu(c["f"]))
+    assert torch.equal(got, want) and torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+    with pytest.raises(PsispecError, match="invalid argument"):
+        psispec_qkv_append(q, k, v, far[0], far[0], tab, ln, inv_freq=_gpu(c["f"]))
+
+
+def test_append_rows_in_their_places():
+    """Keys and values that a projection left in the cache itself are prepared there."""
+    c = _append_case([0], 40, 4, 2, 128, 16, BF, BF, seed=6, rot=64)
+    tab = torch.arange(3, dtype=torch.int32, device=DEV)[None]
+    ln, f, kw = _gpu(c["lens"]), _gpu(c["f"]), _gpu(c["kw"])
+    q, k, v = _gpu(c["qkv"]).split([4, 2, 2], 2)
+    want = [torch.zeros((3, 16, 2, 128), dtype=BF, device=DEV) for _ in range(2)]
+    want_q = psispec_qkv_append(q, k, v, *want, tab, ln, k_weight=kw, inv_freq=f)
+    got = [torch.zeros_like(x) for x in want]
+    rows = [x.view(1, 48, 2, 128)[:, :40] for x in got]
+    rows[0].copy_(k)
+    rows[1].copy_(v)
+    got_q = psispec_qkv_append(q, *rows, *got, tab, ln, k_weight=kw, inv_freq=f)
+    assert torch.equal(got_q, want_q) and all(torch.equal(x, y) for x, y in zip(got, want))

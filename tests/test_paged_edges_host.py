@@ -120,3 +120,15 @@ def test_outputs_over_the_cache(L):
     assert _attend(L, _cache(page_stride=0), K + page - 16) == -1
     far = _cache(page_stride=1 << 59, num_pages=1 << 30)
     assert _attend(L, far, K + page) == -3 and _attend(L, far, K) == -1
+
+
+def test_append_keys_over_values(L):
+    """K and V in one place, and parts of a head, a head, some positions or pages apart."""
+    K, head, row, page = 1 << 30, 128, 256, 4096
+    wide = dict(row_stride=256, page_stride=16 * 256)  # rows with room for V's beside K's
+    turns = dict(page_stride=2 * 16 * 128)             # pages with room for V's behind each
+    mixed = dict(page_stride=64, row_stride=512, head_stride=1 << 14)
+    for kw, shift in [({}, 0), ({}, head), ({}, -3 * row), ({}, 5 * page), ({}, -16), ({}, 8 * page - 16),
+                      (wide, row - 16), (wide, 512 * 3 - head), (turns, page + 16), (mixed, 1 << 15),
+                      (mixed, 128), (mixed, -1024 * 15)]:
+        assert _append(L, _cache(k=K, v=K + shift, **kw)) == -1, (kw, shift)
