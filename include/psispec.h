@@ -437,7 +437,7 @@ typedef struct {
  *              shorter (n_new) keep names rows of that block: which rows were written is not known here
  *   len        [batch] int32; the line's first len rows and the kept ones lie within slots * page_size
  *              positions (all blk rows need not: a short block may end where the table does)
- *   new_len    [batch] int32; len itself, or apart from it
+ *   new_len    [batch] int32; len itself, or apart from every input (PSISPEC_EINVAL otherwise)
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_KEEP as in psispec_kv_commit,
  *              PSISPEC_ST_BAD_PAGE when a page of the rows that move is not in 0..num_pages-1;
  *              nothing of such a line moves and its length stays

@@ -863,7 +863,7 @@ def psispec_paged_commit(pool: torch.Tensor, table: torch.Tensor, length: torch.
     """psispec_kv_commit for lines in pages.  pool [planes][pages][page_size][...] (any dtype, rows of
     16-byte multiples; e.g. layers x K and V as planes); table int32 [batch][slots].  The kept rows
     keep[r][:n_keep[r]] of the block at length[r] move to length[r] onwards in every plane, and
-    new_length (length itself when not given) becomes length + n_keep.  Returns `status` (int32
+    new_length (length itself when not given, never n_keep or keep) becomes length + n_keep.  Returns `status` (int32
     [batch], ST_BAD_KEEP or ST_BAD_PAGE for an invalid line, which stays as it is) when given.  Kept
     rows must lie within the table; where n_new made a block shorter, keep names rows of it."""
     dev = _gpu_device(pool, "pool")

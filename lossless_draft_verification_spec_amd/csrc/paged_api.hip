@@ -126,6 +126,14 @@ bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t 
   return false;
 }
 
+// The first na numbers at a and the first nb at b (either may be NULL): some number is in both.
+bool ints_overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
+}
+// numbers from the first to the last of a table
+int64_t table_extent(int64_t batch, int64_t stride, int64_t slots) { return (batch - 1) * stride + slots; }
+
 bool cache_pointers_ok(const psispec_paged_cache* c) {
   return c->k && c->v && c->table && aligned(c->k, 16) && aligned(c->v, 16);
 }
@@ -278,7 +286,11 @@ psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t
   if (batch == 0) return PSISPEC_OK;
   if (!pool->base || !aligned(pool->base, 16) || !table || !n_keep || !len || !new_len)
     return PSISPEC_EINVAL;
-  if (new_len != len && new_len < len + batch && len < new_len + batch) return PSISPEC_EINVAL;
+  if (new_len != len && ints_overlap(new_len, batch, len, batch)) return PSISPEC_EINVAL;
+  if (ints_overlap(new_len, batch, n_keep, batch) ||
+      ints_overlap(new_len, batch, keep, (int64_t)batch * keep_stride) ||
+      ints_overlap(new_len, batch, table, table_extent(batch, table_stride, slots)))
+    return PSISPEC_EINVAL;
   PagedCommitArgs a{};
   a.pool = *pool;
   a.table = table;

@@ -280,3 +280,17 @@ def test_append_rows_in_their_places():
     rows[1].copy_(v)
     got_q = psispec_qkv_append(q, *rows, *got, tab, ln, k_weight=kw, inv_freq=f)
     assert torch.equal(got_q, want_q) and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_commit_refuses_lengths_over_its_inputs():
+    pool = torch.zeros((1, 8, 4, 4), dtype=torch.int32, device=DEV)
+    raw = torch.zeros(24, dtype=torch.int32, device=DEV)
+    tab = torch.arange(8, dtype=torch.int32, device=DEV).view(4, 2)
+    ln, nk, keep = raw[:4], raw[4:8], raw[8:16].view(4, 2)
+    for new in (nk, keep[:2].flatten(), raw[5:9], tab[:2].flatten()):
+        with pytest.raises(PsispecError, match="invalid argument"):
+            psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=new)
+    st = torch.full((4,), -1, dtype=torch.int32, device=DEV)
+    nk.fill_(1)
+    psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=raw[16:20], status=st)
+    assert (st == 0).all() and raw[16:20].tolist() == [1] * 4 and (raw[20:] == 0).all()

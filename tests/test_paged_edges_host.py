@@ -132,3 +132,18 @@ def test_append_keys_over_values(L):
                       (wide, row - 16), (wide, 512 * 3 - head), (turns, page + 16), (mixed, 1 << 15),
                       (mixed, 128), (mixed, -1024 * 15)]:
         assert _append(L, _cache(k=K, v=K + shift, **kw)) == -1, (kw, shift)
+
+
+def _commit(L, batch=8, blk=4, tab=1 << 12, keep=2 << 12, n_keep=3 << 12, ln=4 << 12, new=5 << 12, st=None):
+    pool = pkg.psispec_page_pool(base=1 << 30, plane_stride=1 << 20, page_stride=16 * 64, row_bytes=64, planes=2,
+                                 num_pages=8, page_size=16, reserved=0)
+    return L.psispec_paged_commit(ctypes.byref(pool), tab, 6, 4, batch, blk, keep, 5, n_keep, ln, new, st, None)
+
+
+def test_commit_lengths_over_inputs(L):
+    """New lengths over the counts, the kept rows or the table: tiles of a line still read those when the
+    first writes its new length."""
+    for at in (3 << 12, (3 << 12) + 28, (3 << 12) - 28, 2 << 12, (2 << 12) + 4 * 39, 1 << 12, (1 << 12) + 4 * 45):
+        assert _commit(L, new=at) == -1, at
+        assert _commit(L, new=at, ln=at) == -1, at
+    assert _commit(L, new=(4 << 12) + 4) == -1
