@@ -296,7 +296,8 @@ psispec_status psispec_lmhead_verify(const void* h_ar, const void* h_draft, cons
  * path over it: psispec_pages_reserve gives every line pages for its next block,
  * psispec_qkv_append writes the block's rows at positions len[r] .. len[r]+n-1,
  * psispec_paged_attention reads them, psispec_paged_commit keeps the accepted ones and advances
- * len, psispec_pages_assign forks, cuts and frees lines.
+ * len, psispec_pages_assign forks, cuts and frees lines.  A status lies apart from the lengths, counts
+ * and tables that its call reads (PSISPEC_EINVAL otherwise).
  *
  * One layer's keys and values as the append and the attention see them.  Element (page p, offset o,
  * head h, dimension d) of K is k[p * page_stride + o * row_stride + h * head_stride + d], of V the

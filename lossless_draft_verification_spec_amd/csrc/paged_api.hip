@@ -3,6 +3,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include <initializer_list>
 #include <utility>
 
 #include "paged.h"
@@ -131,6 +132,13 @@ bool ints_overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return a && b && x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
 }
+// What a call reads of [batch] numbers lies apart from its status, which some workgroups write while others
+// still read.
+bool status_apart(const int32_t* status, int64_t batch, std::initializer_list<const int32_t*> read) {
+  for (const int32_t* x : read)
+    if (ints_overlap(status, batch, x, batch)) return false;
+  return true;
+}
 // numbers from the first to the last of a table
 int64_t table_extent(int64_t batch, int64_t stride, int64_t slots) { return (batch - 1) * stride + slots; }
 
@@ -193,6 +201,9 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
       rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows) ||
       rows_in_cache(c, q_out, q_out_stride, wq, rows))
     return PSISPEC_EINVAL;
+  if (!status_apart(status, batch, {len, n_new}) || ints_overlap(status, batch, positions, rows) ||
+      ints_overlap(status, batch, c->table, table_extent(batch, c->table_stride, c->slots)))
+    return PSISPEC_EINVAL;
   const Places places = cache_places(c);
   if (shifted_places_meet(places, places.levels, (__int128)(uintptr_t)c->v - (__int128)(uintptr_t)c->k))
     return PSISPEC_EINVAL;
@@ -247,6 +258,9 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
       rows_overlap(q, q_stride, wq, out, out_stride, wq, (int64_t)batch * blk) ||
       rows_in_cache(c, out, out_stride, wq, (int64_t)batch * blk))
     return PSISPEC_EINVAL;
+  if (!status_apart(status, batch, {len, n_new}) || ints_overlap(status, batch, parent, (int64_t)batch * blk) ||
+      ints_overlap(status, batch, c->table, table_extent(batch, c->table_stride, c->slots)))
+    return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attend_workspace_bytes(batch, blk, heads_q, c->heads, c->dim))
     return PSISPEC_EWORKSPACE;
@@ -291,6 +305,10 @@ psispec_status psispec_paged_commit(const psispec_page_pool* pool, const int32_t
       ints_overlap(new_len, batch, keep, (int64_t)batch * keep_stride) ||
       ints_overlap(new_len, batch, table, table_extent(batch, table_stride, slots)))
     return PSISPEC_EINVAL;
+  if (!status_apart(status, batch, {len, n_keep, new_len}) ||
+      ints_overlap(status, batch, keep, (int64_t)batch * keep_stride) ||
+      ints_overlap(status, batch, table, table_extent(batch, table_stride, slots)))
+    return PSISPEC_EINVAL;
   PagedCommitArgs a{};
   a.pool = *pool;
   a.table = table;
@@ -331,6 +349,9 @@ psispec_status psispec_pages_assign(int32_t* table, int64_t table_stride, int32_
   if (need == 0 || table_stride < slots) return PSISPEC_EINVAL;
   if (batch == 0) return PSISPEC_OK;
   if (!table || !refs || !len || !src || !new_len) return PSISPEC_EINVAL;
+  if (!status_apart(status, batch, {len, src, new_len}) || ints_overlap(status, batch, refs, num_pages) ||
+      ints_overlap(status, batch, table, table_extent(batch, table_stride, slots)))
+    return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PSISPEC_EWORKSPACE;
   AssignArgs a{};
   a.table = table;
@@ -365,6 +386,9 @@ psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* tab
     return PSISPEC_EINVAL;
   if (batch == 0) return PSISPEC_OK;
   if (!pool->base || !aligned(pool->base, 16) || !table || !refs || !len) return PSISPEC_EINVAL;
+  if (!status_apart(status, batch, {len, n_new}) || ints_overlap(status, batch, refs, pool->num_pages) ||
+      ints_overlap(status, batch, table, table_extent(batch, table_stride, slots)))
+    return PSISPEC_EINVAL;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PSISPEC_EWORKSPACE;
   ReserveArgs a{};
   a.pool = *pool;

@@ -147,3 +147,22 @@ def test_commit_lengths_over_inputs(L):
         assert _commit(L, new=at) == -1, at
         assert _commit(L, new=at, ln=at) == -1, at
     assert _commit(L, new=(4 << 12) + 4) == -1
+
+
+def test_status_over_inputs(L):
+    """A status over the lengths, counts, positions, parents, kept rows or table that the call reads."""
+    A, B, C, T = 1 << 14, 2 << 14, 3 << 14, 4 << 14
+    c = _cache(table=T)
+    for st in (A, A + 28, A - 28, B, C, C + 4 * 15, T, T + 4 * 31):
+        assert _append(L, c, batch=8, ln=A, nn=B, pos=C, st=st) == -1, st
+        assert _attend(L, c, 1 << 26, batch=8, ln=A, nn=B, parent=C, st=st) == -1, st
+    assert _attend(L, c, 1 << 26, batch=8, ln=A, nn=B, parent=C, st=5 << 14) == -3
+    for st in (3 << 12, 4 << 12, 5 << 12, (2 << 12) + 4 * 39, (1 << 12) + 4 * 45):
+        assert _commit(L, st=st) == -1, st
+    pool = pkg.psispec_page_pool(base=1 << 30, plane_stride=1 << 20, page_stride=16 * 64, row_bytes=64, planes=2,
+                                 num_pages=50, page_size=16, reserved=0)
+    R = 5 << 14
+    for st, rc in ((A, -1), (B, -1), (C, -1), (T, -1), (T + 4 * 45, -1), (R + 4 * 49, -1), (6 << 14, -3)):
+        assert L.psispec_pages_assign(T, 6, 4, R, 50, 16, A, B, C, st, 8, None, BIG, None) == rc, st
+        if st != C:
+            assert L.psispec_pages_reserve(ctypes.byref(pool), T, 6, 4, R, A, B, 4, st, 8, None, BIG, None) == rc
