@@ -362,7 +362,7 @@ typedef struct {
  *              or the rows do not fit the slots (nothing of the line is then written, q_out
  *              included), or when a page of the rows is not in 0..num_pages-1 (the rows on such a
  *              page are then not written, q_out included)
- *   blk 1..2^20;  batch >= 0 (0 launches nothing);  heads_q >= 1
+ *   blk 1..2^20;  batch >= 0 (0 launches nothing), batch * blk < 2^24;  heads_q 1..1024
  * No two (page, position, head) of the cache share an element, nor do K and V (PSISPEC_EINVAL).  The
  * pages written must be the line's own (psispec_pages_reserve sees to it): rows of two lines in one
  * page position race.  The inputs q, k and v lie outside the cache, but for rows of k or v that are
@@ -399,7 +399,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE as in psispec_qkv_append, for every page
  *              of the line's first len + n_new positions; PSISPEC_ST_BAD_PARENT.  Out rows of such a
  *              line are unspecified, other lines are not affected
- *   blk 1..1024;  batch >= 0 (0 launches nothing);  heads_q a multiple of c->heads, at most 1024
+ *   blk 1..1024;  batch 0..2^24-1 (0 launches nothing);  heads_q a multiple of c->heads, at most 1024
  * The work is cut into equal shares over the whole batch by the lines' lengths, read on the device,
  * and rows cut by a share's border are joined in a fixed order: reruns are bitwise identical.
  */

@@ -847,7 +847,7 @@ def psispec_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         workspace = _workspace_for(workspace,
                                    paged_attention_workspace_bytes(batch, blk, hq, heads, dim), dev,
                                    "psispec_paged_attention (blk 1..1024, heads_q a multiple of the "
-                                   "cache's heads, dim a multiple of 16 up to 256)")
+                                   "cache's heads and at most 1024, dim a multiple of 16 up to 256)")
         rc = lib().psispec_paged_attention(
             c, qp, qs, _PAGED_DTYPES[dt], batch, blk, hq, pp, lp, np_,
             dim ** -0.5 if scale is None else scale, op, os_, sp, workspace.data_ptr(),

@@ -233,7 +233,15 @@ static bool attend_sizes_ok(int32_t batch, int32_t blk, int32_t heads_q, int32_t
                             int32_t dim) {
   return batch >= 0 && blk >= 1 && blk <= kMaxAttendBlock && heads_kv >= 1 && heads_q >= heads_kv &&
          heads_q <= kMaxHeads && heads_q % heads_kv == 0 && dim >= 16 && dim <= kMaxHeadDim &&
-         dim % 16 == 0 && grid_ok((int64_t)batch * blk * heads_q);
+         dim % 16 == 0 && grid_ok(batch);  // a workgroup per line at most (masks, status)
+}
+
+// The units of work that the kernel's shares are cut from, at most: their product with the 2^14 parts of a
+// share's border stays below 2^63.
+static bool attend_units_ok(const psispec_paged_cache* c, int32_t batch, int32_t blk, int32_t heads_q) {
+  const int64_t groups = (int64_t)blk * (heads_q / c->heads) / 16 + 1;
+  const int64_t steps = (int64_t)c->slots * c->page_size / 32 + 4;
+  return (__int128)batch * c->heads * groups * steps < (__int128)1 << 49;
 }
 
 size_t psispec_paged_attention_workspace(int32_t batch, int32_t blk, int32_t heads_q,
@@ -250,7 +258,8 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
                                        size_t workspace_bytes, void* stream) {
   const psispec_status e = check_cache(c, dtype);
   if (e != PSISPEC_OK) return e;
-  if (!attend_sizes_ok(batch, blk, heads_q, c->heads, c->dim) || !isfinite((float)scale))
+  if (!attend_sizes_ok(batch, blk, heads_q, c->heads, c->dim) || !attend_units_ok(c, batch, blk, heads_q) ||
+      !isfinite((float)scale))
     return PSISPEC_EINVAL;
   if (batch == 0) return PSISPEC_OK;
   const int64_t wq = (int64_t)heads_q * c->dim;

@@ -6,7 +6,8 @@ import torch
 import paged_ref as ref
 from lossless_draft_verification_spec_amd import (
     PsispecError, psispec_paged_attention, psispec_paged_commit, psispec_pages_reserve, psispec_qkv_append)
-from test_gpu_paged import (BF, DEV, F8, FH, _append_case, _attend, _case, _check_attend, _gen, _gpu)
+from test_gpu_paged import (BF, DEV, F8, FH, _append_case, _attend, _case, _check_attend, _gen, _gpu,
+                            _make_table)
 
 pytestmark = pytest.mark.gpu
 
@@ -294,3 +295,33 @@ def test_commit_refuses_lengths_over_its_inputs():
     nk.fill_(1)
     psispec_paged_commit(pool, tab, ln, 6, nk, keep=keep, new_length=raw[16:20], status=st)
     assert (st == 0).all() and raw[16:20].tolist() == [1] * 4 and (raw[20:] == 0).all()
+
+
+# ------------------------------------------------------------------ sizes
+
+def test_attend_large_batch_of_large_blocks():
+    """256 lines of 1024 rows and 64 query heads (2^24 rows): rows of a few lines against the reference, and
+    against calls of those lines alone."""
+    batch, blk, hq, hkv, dim, ps = 256, 1024, 64, 8, 16, 16
+    g = torch.Generator(device=DEV).manual_seed(7)
+    lens = [0 if r % 7 == 3 else (r * 37) % 150 for r in range(batch)]
+    live = [0 if r % 11 == 5 else 5 if r in (0, 128, 255) else blk for r in range(batch)]
+    tab, pages = _make_table(lens, blk, ps, _gen(7))
+    k, v = (torch.randn((pages, ps, hkv, dim), generator=g, device=DEV).to(BF) for _ in range(2))
+    q = torch.randn((batch, blk, hq, dim), generator=g, device=DEV, dtype=BF)
+    tab, ln, n = tab.to(DEV), *(torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, live))
+    st = torch.full((batch,), -1, dtype=torch.int32, device=DEV)
+    out = torch.full_like(q, 7.0)
+    psispec_paged_attention(q, k, v, tab, ln, n_new=n, out=out, status=st)
+    assert (st == 0).all()
+    for r in (0, 128, 255, 5):
+        assert (out[r, live[r]:] == 7.0).all()
+    few = [0, 128, 255]
+    want, bound = ref.attention(q[few, :5].cpu(), k.cpu(), v.cpu(), tab[few].cpu(), ln[few].cpu(), [5] * 3, None,
+                                dim**-0.5)
+    assert ((out[few, :5].cpu().double() - want).abs() <= bound).all()
+    for r in (1, 77, 254):
+        alone = psispec_paged_attention(q[r:r + 1], k, v, tab[r:r + 1], ln[r:r + 1], n_new=n[r:r + 1])[0].float()
+        both = out[r].float()
+        # each within half a step of its own rounding, 2^-8, and the arithmetic's 2^-13 of values up to 6
+        assert ((both - alone).abs() <= 2.0**-7 * alone.abs() + 2 * 6 * 2.0**-13).all()

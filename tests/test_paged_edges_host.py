@@ -166,3 +166,16 @@ def test_status_over_inputs(L):
         assert L.psispec_pages_assign(T, 6, 4, R, 50, 16, A, B, C, st, 8, None, BIG, None) == rc, st
         if st != C:
             assert L.psispec_pages_reserve(ctypes.byref(pool), T, 6, 4, R, A, B, 4, st, 8, None, BIG, None) == rc
+
+
+def test_attention_sizes(L):
+    """Batch, block and heads each at their limits, and several of them large at once."""
+    size = L.psispec_paged_attention_workspace
+    for a in ((256, 1024, 64, 8, 128), (64, 1024, 1024, 1, 256), (1 << 20, 1, 64, 8, 128), ((1 << 24) - 1, 1, 1, 1, 16)):
+        assert size(*a) > 0, a
+    for a in ((1 << 24, 1, 1, 1, 16), (1, 1025, 1, 1, 16), (1, 1, 1025, 1, 16), (1, 1, 1088, 17, 16)):
+        assert size(*a) == 0, a
+    assert _attend(L, _cache(), 1 << 40, batch=256, blk=1024, hq=2) == -3
+    # more work than the shares can be cut from: 2^23 lines of 2^30 positions
+    c = _cache(page_size=4096, slots=1 << 18, table_stride=1 << 18, page_stride=4096 * 128)
+    assert _attend(L, c, 1 << 40, batch=1 << 23, blk=1) == -1
