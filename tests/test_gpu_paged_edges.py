@@ -325,3 +325,75 @@ def test_attend_large_batch_of_large_blocks():
         both = out[r].float()
         # each within half a step of its own rounding, 2^-8, and the arithmetic's 2^-13 of values up to 6
         assert ((both - alone).abs() <= 2.0**-7 * alone.abs() + 2 * 6 * 2.0**-13).all()
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+def _odd_case(kind, dtype, cache, tree):
+    if kind == "cut":          # a workgroup per share, lines cut and joined
+        return _case([1500, 0, 733], 9, 8, 4, 128, 16, dtype, cache, seed=50, live=[9, 5, 7], tree=tree)
+    if kind == "rows":         # three row tiles, the queries in LDS
+        return _case([600, 0, 333], 20, 8, 4, 128, 16, dtype, cache, seed=51, live=[20, 5, 7], tree=tree)
+    if kind == "padded":       # heads and pages of no round size
+        return _case([75, 0, 33], 9, 6, 3, 80, 24, dtype, cache, seed=52, live=[9, 5, 7], tree=tree)
+    if kind == "wide":
+        return _case([75, 0, 333], 9, 4, 2, 208, 8, dtype, cache, seed=53, live=[9, 5, 7], tree=tree)
+    lens = [75, 0, 33] + torch.randint(0, 40, (260,), generator=_gen(4)).tolist()  # a wave per job
+    live = [9, 5, 7] + torch.randint(0, 3, (260,), generator=_gen(5)).tolist()
+    return _case(lens, 9, 4, 4, 64, 16, dtype, cache, seed=54, live=live, tree=tree)
+
+
+@pytest.mark.parametrize("kind", ["cut", "rows", "padded", "wide", "short"])
+@pytest.mark.parametrize("dtype,cache,bad", [(d, c, b) for d, c in TYPES for b in ("nan", "inf", "-inf")
+                                             if c != F8 or b == "nan"])  # 8 bits have no infinities
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_unseen_values_of_every_type(kind, dtype, cache, bad, tree):
+    """What a row does not see (free pages, the rest of a line's last page, block rows of other branches) has
+    no effect on it, whatever it holds; values that are not finite reach exactly the rows that see them."""
+    c = _odd_case(kind, dtype, cache, tree)
+    lens, live, ps = c["lens"], c["live"], c["k"].shape[1]
+    n0, dim = int(live[0]), c["q"].shape[3]
+
+    def place(r, pos):
+        return int(c["table"][r, pos // ps]), pos % ps
+
+    fill = torch.tensor(float(bad)).to(cache)
+    used = torch.zeros(c["k"].shape[:2], dtype=torch.bool)
+    for r in range(len(lens)):
+        t = torch.arange(int(lens[r] + live[r]))
+        used[c["table"][r][t // ps].long(), t % ps] = True
+    raw = torch.uint8 if cache == F8 else torch.int16
+    for x in (c["k"], c["v"]):
+        x.view(raw)[~used] = fill.view(raw)
+    _check_attend(c)
+    want = _attend(c).cpu()
+    sees = ref.seen_rows(n0, n0, c["parent"][0] if tree else None)
+
+    def clean_rows_kept(got, rows):
+        clean = [i for i in range(n0) if not any(sees[i, j] for j in rows)]
+        assert clean
+        assert torch.equal(got[0, clean].view(torch.int16), want[0, clean].view(torch.int16))
+        for r in range(1, len(lens)):
+            assert torch.equal(got[r, :live[r]].view(torch.int16), want[r, :live[r]].view(torch.int16))
+        return [i for i in range(n0) if i not in clean]
+
+    # one dimension of two values
+    spot = (3, dim - 5)
+    old = {}
+    for j in spot[:1] + (6,):
+        at = place(0, int(lens[0]) + j)
+        old[at] = c["v"][at].clone()
+        c["v"].view(raw)[at[0], at[1], :, spot[1]] = fill.view(raw)
+    got = _attend(c).cpu()
+    for i in clean_rows_kept(got, (3, 6)):
+        x = got[0, i].float()
+        assert (torch.isnan(x[:, spot[1]]) | torch.isinf(x[:, spot[1]])).all()
+        others = [d for d in range(dim) if d != spot[1]]
+        assert torch.equal(got[0, i][:, others].view(torch.int16), want[0, i][:, others].view(torch.int16))
+    # whole keys and values of the same rows
+    for at in old:
+        c["k"].view(raw)[at] = fill.view(raw)
+        c["v"].view(raw)[at] = fill.view(raw)
+    got = _attend(c).cpu()
+    for i in clean_rows_kept(got, (3, 6)):
+        assert not torch.isfinite(got[0, i].float()).any()
