@@ -500,7 +500,9 @@ def run_paged(steps, warmup, ncalls, torch, pkg, peaks):
     psispec_qkv_append, psispec_paged_attention and psispec_paged_commit of 9-row blocks (8 drafted
     tokens and the one before them) for 64 lines of 300 to 4200 positions, 32 query and 8 key/value
     heads of 128, bf16, pages of 16 positions in a random order.  Each call starts from a fresh copy of
-    the lengths.  HBM roofline of the attention over every key and value read once."""
+    lengths, table and page counts (its time is part of the call's), so that each reserves the pages of
+    its blocks; pages are the lines' own (none is copied), and the commit keeps a prefix of each block, as
+    a linear verify does: no row moves.  HBM roofline of the attention over every key and value read once."""
     b, blk, hq, hkv, d, ps = 64, 9, 32, 8, 128, 16
     g = torch.Generator(device="cuda").manual_seed(11)
     len0 = torch.linspace(300, 4200, b, device="cuda").to(torch.int32)
@@ -522,10 +524,11 @@ def run_paged(steps, warmup, ncalls, torch, pkg, peaks):
     inv, mag = pkg.rope_frequencies(d, 1000000.0, device="cuda")
     n_keep = torch.randint(0, blk + 1, (b,), generator=g, device="cuda", dtype=torch.int32)
     length, status = len0.clone(), torch.zeros(b, dtype=torch.int32, device="cuda")
+    table0, refs0 = table.clone(), refs.clone()
     q_out, out = (torch.empty((b, blk, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
 
     def call(_):
-        length.copy_(len0)
+        torch._foreach_copy_([length, table, refs], [len0, table0, refs0])
         pkg.psispec_pages_reserve(pool, table, refs, length, blk)
         pkg.psispec_qkv_append(q, k, v, pool[0], pool[1], table, length, q_weight=w, k_weight=w,
                                inv_freq=inv, rope_scale=mag, q_out=q_out)
@@ -533,7 +536,9 @@ def run_paged(steps, warmup, ncalls, torch, pkg, peaks):
         pkg.psispec_paged_commit(pool, table, length, blk, n_keep)
 
     m = measure(torch, pkg, call, steps, warmup, ncalls)
-    ok = bool((length == len0 + n_keep).all().item() and (status == 0).all().item())
+    held = int(((len0 + blk + ps - 1) // ps).sum().item())  # pages of the lines and their blocks
+    ok = bool((length == len0 + n_keep).all().item() and (status == 0).all().item()
+              and held > int(refs0.sum().item()) and int(refs.sum().item()) == held)
     row = d * 2
     alg = int((len0 + blk).sum().item()) * 2 * hkv * row + 2 * b * blk * hq * row
     del pool
