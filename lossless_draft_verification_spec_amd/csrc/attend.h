@@ -25,8 +25,8 @@
 // f16 V: f16 ends at 2^-24, and weights below 2^-9 would lose bits of the pair, those below 2^-25 all,
 // while the sum l keeps them (a position far above the others with a value of 0 shows it).  There the
 // weights are taken times 2^14 and relative to a reference that follows the tiles down too: it is
-// raised by scores 2^1 above it and lowered when a tile has nothing within 2^8 of it, at most 2^64 below
-// the maximum (what lies deeper is below f16's range).  A weight is then off by 2^-16 of itself or
+// raised by scores 2^1 above it and lowered when a tile has nothing within 2^8 of it, at most by 2^64
+// (what lies deeper is below f16's range).  A weight is then off by 2^-16 of itself or
 // 2^-39 of the reference's; over all positions at most 2^-26 of the largest |v|.  Cost, f16 caches
 // alone (the measured lines below): 64 lines of one row 185.8 -> 186.5 us, of 9 rows 119.0 -> 121.2, trees 67.1 ->
 // 67.8.
@@ -363,7 +363,7 @@ void k_attend(AttendKernelArgs k) {
   typedef typename Elem<P>::x8 p8;
   constexpr bool kFollow = std::is_same<P, _Float16>::value;
   constexpr float kSlack = kFollow ? 1.0f : 8.0f;   // powers of two that a weight may exceed 1 by
-  constexpr float kBias = kFollow ? 14.0f : 0.0f;   // all weights times 2^kBias (up to 2^15: f16 holds them)
+  constexpr float kBias = kFollow ? 14.0f : 0.0f;   // the reference lies 2^kBias below (weights up to 2^15)
   constexpr float kDrop = 8.0f, kDeepest = 64.0f;
   constexpr int ES = F8 ? 1 : 2;
   constexpr int RB = DP * ES;                 // bytes of a row in LDS
@@ -619,7 +619,7 @@ void k_attend(AttendKernelArgs k) {
         }
 
         f32x4 acc[MT][NT];
-        float m_run[MT], l_run[MT], top[kFollow ? MT : 1];  // the reference, the sum; the maximum
+        float m_run[MT], l_run[MT], top[kFollow ? MT : 1];  // the reference, the sum; the highest reference
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           m_run[mt] = kNegBig;
@@ -706,36 +706,46 @@ void k_attend(AttendKernelArgs k) {
             }
             float mx = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
                              fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
-            mx *= sc;  // sc >= 0: a negative scale is in the queries' signs
-            bool move = __any(mx > m_run[mt] + kSlack);
-            if constexpr (kFollow) {  // rows that see something here, and nothing near the reference
-              uint64_t seen = __ballot(mx > -INFINITY), near = __ballot(mx > m_run[mt] - kDrop);
+            // sc >= 0: a negative scale is in the queries' signs
+            bool move;
+            float m_new;
+            if constexpr (kFollow) {
+              // minus the largest exponent, rounded as the weight's own, so that no weight is too large
+              const float x = fmaf(-mx, sc, m_run[mt]);
+              // rows that see something here, and nothing near the reference
+              uint64_t seen = __ballot(x < INFINITY), near = __ballot(x < kDrop - kBias);
               seen |= seen >> 32;
               near |= near >> 32;
-              move |= ((seen | seen >> 16) & ~(near | near >> 16) & 0xffffu) != 0;
+              move = __any(x < -kBias - kSlack) || ((seen | seen >> 16) & ~(near | near >> 16) & 0xffffu) != 0;
+            } else {
+              mx *= sc;
+              move = __any(mx > m_run[mt] + kSlack);
             }
             if (move) {
               mx = group_max(mx);
               if constexpr (kFollow) {
-                top[mt] = fmaxf(top[mt], mx);
-                mx = mx > -INFINITY ? fmaxf(mx, top[mt] - kDeepest) : m_run[mt];
+                const float g = mx * sc;
+                m_new = g > -INFINITY ? fmaxf(g - kBias, top[mt] - kDeepest) : m_run[mt];
+                // where 32 bits hold the reference in steps of 1 and more
+                const float x = fmaf(-mx, sc, m_new);
+                if (x < -kBias - kSlack) m_new += fmaxf(-x - kBias, fabsf(m_new) * 0x1p-23f);
+                top[mt] = fmaxf(top[mt], m_new);
               } else {
-                mx = fmaxf(mx, m_run[mt]);
+                m_new = fmaxf(mx, m_run[mt]);
               }
-              const float f = __builtin_amdgcn_exp2f(m_run[mt] - mx);
-              m_run[mt] = mx;
+              const float f = __builtin_amdgcn_exp2f(m_run[mt] - m_new);
+              m_run[mt] = m_new;
               l_run[mt] *= f;
 #pragma unroll
               for (int d = 0; d < NT; ++d) acc[mt][d] *= f;
             }
             float sum = 0.0f;
-            const float base = kFollow ? kBias - m_run[mt] : -m_run[mt];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               f32x2 p;
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                p[u] = __builtin_amdgcn_exp2f(fmaf(s[mt][(e + u) >> 2][(e + u) & 3], sc, base));
+                p[u] = __builtin_amdgcn_exp2f(fmaf(s[mt][(e + u) >> 2][(e + u) & 3], sc, -m_run[mt]));
                 if constexpr (TAIL) p[u] = (see >> (16 * (e >> 2) + ((e + u) & 3))) & 1u ? p[u] : 0.0f;
               }
               sum += p[0] + p[1];
@@ -811,7 +821,7 @@ void k_attend(AttendKernelArgs k) {
         int t = t0;
         for (const int tm = min(t1, L / kAttendTile); t < tm; ++t) tile(t, std::false_type{});
         for (; t < t1; ++t) tile(t, std::true_type{});
-        if constexpr (kFollow) {  // from here on relative to the maximum again
+        if constexpr (kFollow) {  // from here on relative to the highest reference
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             if (!__any(m_run[mt] < top[mt])) continue;

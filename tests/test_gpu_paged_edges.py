@@ -397,3 +397,26 @@ def test_attend_unseen_values_of_every_type(kind, dtype, cache, bad, tree):
     got = _attend(c).cpu()
     for i in clean_rows_kept(got, (3, 6)):
         assert not torch.isfinite(got[0, i].float()).any()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("power", [12, 18, 21, 22, 23, 24, 25, 26])
+def test_attend_very_large_scores(dtype, cache, power):
+    """Scores of about +-2^power, which 32 bits hold in steps of up to 8 and more: one position with all the
+    weight, runs of equal scores, and rows that see only the lowest."""
+    L = 300
+    c = _case([L], 3, 2, 1, 64, 16, dtype, cache, seed=power)
+    page, off = (c["table"][0][torch.arange(L + 3) // 16].long(), torch.arange(L + 3) % 16)
+    if cache == F8:
+        c["ks"], c["vs"] = torch.ones(1), torch.ones(1)
+    c["scale"] = 1.0
+    k = torch.zeros(L + 3)
+    k[10:20], k[130], k[200:232] = -1.0, 0.875, -0.75
+    c["k"][page, off, 0] = (k[:, None] * 2.0 ** 7).to(cache).expand(L + 3, 64)
+    c["q"].copy_(torch.tensor([1.0, -1.0, 0.8125]).view(3, 1, 1) * 2.0 ** (power - 13))
+    got = _attend(c).cpu().double()
+    v = c["v"].double()[page, off, 0]
+    top = (v[130], v[10:20].mean(0), v[130])
+    for i in range(3):
+        err = (got[0, i] - top[i]).abs()
+        assert (err <= (ref.half_step(dtype) + 2.0**-14) * top[i].abs() + 2.0**-14).all(), (i, err.max())
