@@ -330,8 +330,8 @@ typedef struct {
   const void* k_weight;   /* the same for the key heads */
   const double* inv_freq; /* device [rot/2]: angle per position of pair j (the long-context scalings
                              are other frequencies, and rope_scale); NULL only when rot = 0 */
-  double eps;             /* >= 0: added to the mean square */
-  double rope_scale;      /* finite: the rotated pairs are multiplied by it */
+  double eps;             /* >= 0, finite in 32 bits: added to the mean square */
+  double rope_scale;      /* finite in 32 bits: the rotated pairs are multiplied by it */
   int32_t rot;            /* leading dimensions that are rotated: a multiple of 16, 0..dim */
   uint32_t flags;         /* PSISPEC_ROPE_INTERLEAVED or 0 */
 } psispec_qkv_prep;
@@ -395,7 +395,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
  *   parent     [batch][blk] int32: the block row that row j follows, -1 = the line's last position;
  *              must be < j.  NULL: row j follows row j-1
  *   len, n_new as in psispec_qkv_append; rows i >= n_new[r] of out are left as they are
- *   scale      finite
+ *   scale      finite, in 32 bits and times log2 e
  *   status     [batch] int32, nullable: PSISPEC_ST_BAD_PAGE as in psispec_qkv_append, for every page
  *              of the line's first len + n_new positions; PSISPEC_ST_BAD_PARENT.  Out rows of such a
  *              line are unspecified, other lines are not affected

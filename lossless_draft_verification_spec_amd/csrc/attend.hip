@@ -312,7 +312,7 @@ hipError_t launch_attend(const AttendArgs& a, psispec_dtype dtype, void* workspa
     k.page_bytes = (uint32_t)page_bytes;
     k.row_bytes = (uint32_t)row_bytes;
   }
-  k.c = a.scale * 1.4426950408889634f;
+  k.c = a.scale * kLog2e;
   k.info = reinterpret_cast<AttendInfo*>(ws);
   k.ml = reinterpret_cast<float2*>(ws + p.off_ml);
   k.o = reinterpret_cast<float*>(ws + p.off_o);

@@ -9,6 +9,7 @@ constexpr int kMaxPageSize = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxAttendBlock = 1024;   // rows of a block that the attention takes
 constexpr int kMaxAppendBlock = 1 << 20;
+constexpr float kLog2e = 1.4426950408889634f;  // the scores are in powers of two
 
 // append.hip
 struct AppendArgs {

@@ -182,7 +182,7 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
   if (batch < 0 || blk < 1 || blk > kMaxAppendBlock || heads_q < 1 || heads_q > kMaxHeads || !p)
     return PSISPEC_EINVAL;
   if (!cache_places(c).apart) return PSISPEC_EINVAL;
-  if (!(p->eps >= 0.0) || !isfinite(p->eps) || !isfinite(p->rope_scale) || p->rot < 0 ||
+  if (!(p->eps >= 0.0) || !isfinite((float)p->eps) || !isfinite((float)p->rope_scale) || p->rot < 0 ||
       p->rot > c->dim || p->rot % 16 || (p->flags & ~PSISPEC_ROPE_INTERLEAVED) ||
       (p->rot > 0 && !p->inv_freq) || !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16))
     return PSISPEC_EINVAL;
@@ -259,7 +259,7 @@ psispec_status psispec_paged_attention(const psispec_paged_cache* c, const void*
   const psispec_status e = check_cache(c, dtype);
   if (e != PSISPEC_OK) return e;
   if (!attend_sizes_ok(batch, blk, heads_q, c->heads, c->dim) || !attend_units_ok(c, batch, blk, heads_q) ||
-      !isfinite((float)scale))
+      !isfinite((float)scale * kLog2e))
     return PSISPEC_EINVAL;
   if (batch == 0) return PSISPEC_OK;
   const int64_t wq = (int64_t)heads_q * c->dim;

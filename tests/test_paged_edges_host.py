@@ -179,3 +179,15 @@ def test_attention_sizes(L):
     # more work than the shares can be cut from: 2^23 lines of 2^30 positions
     c = _cache(page_size=4096, slots=1 << 18, table_stride=1 << 18, page_stride=4096 * 128)
     assert _attend(L, c, 1 << 40, batch=1 << 23, blk=1) == -1
+
+
+def test_numbers_that_32_bits_do_not_hold(L):
+    for scale in (3e38, -3e38, 1e39):
+        assert _attend(L, _cache(), 1 << 26, scale=scale) == -1, scale
+    for scale in (2e38, -2e38, 0.0, 1e-40):
+        assert _attend(L, _cache(), 1 << 26, scale=scale) == -3, scale
+    for kw in (dict(eps=1e39), dict(rope_scale=1e39), dict(rope_scale=-1e300)):
+        p = pkg.psispec_qkv_prep(**{**dict(q_weight=None, k_weight=None, inv_freq=256, eps=1e-6, rope_scale=1.0,
+                                           rot=64, flags=0), **kw})
+        assert L.psispec_qkv_append(ctypes.byref(_cache()), ctypes.byref(p), 1 << 20, 512, 2 << 20, 512, 3 << 20, 512,
+                                    pkg.PSISPEC_BF16, 1, 2, 4, None, 256, None, 4 << 20, 512, None, None) == -1, kw
