@@ -385,10 +385,11 @@ psispec_status psispec_qkv_append(const psispec_paged_cache* c, const psispec_qk
  *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * q . k_t)   over the positions t that it sees
  * Query heads share key/value heads in groups: head h reads key/value head h / (heads_q / heads).
  * Products of the matrix cores in the inputs' type with 32-bit sums; softmax statistics in 32 bits;
- * weights enter the second product as a pair of 16-bit numbers (relative error 2^-16; in an F16 cache
- * also up to 2^-26 of the largest |v| over all positions, half of F16's smallest number for values up
- * to 2), so out is as exact as its own rounding, however small the weights.  A position that a row does not see has no effect on it, whatever the
- * cache holds there.  Infinities among what it sees give infinities or NaN.
+ * weights enter the second product as a pair of 16-bit numbers with a relative error of 2^-16, so out
+ * is as exact as its own rounding.  What the pairs' range leaves out is at most 2^-26 of the largest
+ * |v| for an F16 cache (half of F16's smallest number for values up to 2), 2^-96 of it otherwise.  A
+ * position that a row does not see has no effect on it, whatever the cache holds there.  Infinities
+ * among what it sees give infinities or NaN.
  *   q, out     row (r, i) at (r * blk + i) * stride elements: heads_q heads of c->dim contiguous
  *              elements; dtype PSISPEC_BF16 or PSISPEC_F16; 16-byte aligned, strides multiples of 8;
  *              out overlaps no input (PSISPEC_EINVAL when it lies over q or the cache)

@@ -28,8 +28,8 @@
 // raised by scores 2^1 above it and lowered when a tile has nothing within 2^8 of it, at most by 2^64
 // (what lies deeper is below f16's range).  A weight is then off by 2^-16 of itself or
 // 2^-39 of the reference's; over all positions at most 2^-26 of the largest |v|.  Cost, f16 caches
-// alone (the measured lines below): 64 lines of one row 185.8 -> 186.5 us, of 9 rows 119.0 -> 121.2, trees 67.1 ->
-// 67.8.
+// alone (the measured lines below): 64 lines of one row 185.8 -> 186.8 us, of 9 rows 118.7 -> 121.8, trees 68.9 ->
+// 69.7.
 //
 // Memory.  K and V go from HBM to LDS by 16-byte direct loads (no registers), each wave into a
 // ring of its own (no barrier in the loop): K and V of a tile have separate places, each refilled as
@@ -62,7 +62,8 @@ constexpr int kAttendThreads = 64 * kAttendWaves;
 constexpr int kAttendTile = 32;                          // positions per tile
 // Cache policy of the tiles: nontemporal when each is read once (64 lines of 1000-8000 positions:
 // 210 us without, 187 with); kept when several row groups of a job read them (33-row trees: 89 us
-// nontemporal, 79 kept).
+// nontemporal, 79 kept).  The path for heads and pages of any size is nontemporal throughout (not
+// measured kept).
 constexpr int kNonTemporal = 2;
 
 // The shares: one per workgroup that runs at once (R of them), or one per unit of work if there are
