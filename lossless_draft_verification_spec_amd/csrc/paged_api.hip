@@ -97,8 +97,9 @@ bool rows_in_cache(const psispec_paged_cache* c, const void* rows, int64_t strid
   const Places p = cache_places(c);
   for (const void* base : {c->k, c->v}) {
     const __int128 at = (__int128)(uintptr_t)rows - (__int128)(uintptr_t)base;
-    if (at >= p.span[p.levels] || at + 2 * ((__int128)stride * (n - 1) + width) <= 0) continue;
-    for (int64_t i = 0; i < n; ++i) {  // within the cache's range: rare
+    if (!bytes_in_places(p, p.levels, at, at + 2 * ((__int128)stride * (n - 1) + width))) continue;
+    if (stride == width) return true;
+    for (int64_t i = 0; i < n; ++i) {  // places in the rows' range, perhaps between the rows: rare
       const __int128 lo = at + 2 * (__int128)stride * i;
       if (bytes_in_places(p, p.levels, lo, lo + 2 * width)) return true;
     }

@@ -220,17 +220,18 @@ def test_outputs_in_the_gaps_of_a_cache():
     want_q = psispec_qkv_append(q, k, v, *near, tab, ln, **kw)
     want = psispec_paged_attention(want_q, *near, tab, ln)
     pages = near[0].shape[0]
-    raw = torch.zeros((2, pages, 40, 2, 64), dtype=BF, device=DEV)  # 16 positions and a gap of 24
+    raw = torch.zeros((2, pages, 46, 2, 64), dtype=BF, device=DEV)  # 16 positions and a gap of 30
     far = [raw[0, :, :16], raw[1, :, :16]]
     for x, y in zip(far, (c["kc"], c["vc"])):
         x.copy_(y)
     gap = raw[0, 1, 16:].flatten()
-    q_out, out = gap[:1536].view(2, 3, 4, 64), gap[1536:3072].view(2, 3, 4, 64)
+    q_out, out = (x.view(2, 3, 4, 64) for x in gap[:2 * 1536].chunk(2))
     psispec_qkv_append(q, k, v, *far, tab, ln, q_out=q_out, **kw)
     psispec_paged_attention(q_out, *far, tab, ln, out=out)
     assert torch.equal(q_out, want_q) and torch.equal(out, want)
     assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
-    over = raw.flatten()[5120 - 8:5120 + 1536 - 8].view(2, 3, 4, 64)  # up to the next page and into it
+    page = raw[0, 0].numel()
+    over = raw.flatten()[page - 8:page + 1536 - 8].view(2, 3, 4, 64)  # from the gap into the next page
     for call in (lambda: psispec_qkv_append(q, k, v, *far, tab, ln, q_out=over, **kw),
                  lambda: psispec_paged_attention(want_q, *far, tab, ln, out=over)):
         with pytest.raises(PsispecError, match="invalid argument"):
