@@ -43,7 +43,7 @@
 //
 // Measured, 32 query and 8 key/value heads of 128 (the kernel, then the join): 64 lines of 1000-8000
 // positions, one row each, 186 us (6.3 TB/s of keys and values) + 5.3; 64 lines of 300-4200, 9 rows, 121
-// (4.7 TB/s) + 7; 8 lines of 3500-4500, trees of 33 rows, 71 + 6; 4 lines of 125 000 in 8 bits 163 (6.3
+// (4.7 TB/s; three idle and every fifth with 5 rows, all with 9: 128, the same rate) + 7; 8 lines of 3500-4500, trees of 33 rows, 71 + 6; 4 lines of 125 000 in 8 bits 163 (6.3
 // TB/s) + 7; one line of 500, 9.5 + 5.2.  The loads alone take 184 and 118 of the first two, the products
 // and softmax alone 48 and 74.  HBM bounds one row (from L2 the same kernel reads 10-11 TB/s); with three
 // row tiles a tile's own time bounds the waves (5.8 TB/s at most, from L2 as well), then the ends of
