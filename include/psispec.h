@@ -59,12 +59,14 @@ typedef enum {
 } psispec_status;
 
 /* Logits are F32 or BF16.  The paged-cache calls take queries, keys and values in BF16 or F16 and
-   caches in their type or in F8E4M3 (8 bits: 4 exponent, 3 mantissa; no infinities, largest 448). */
+   caches in their type or in F8E4M3 (8 bits: 4 exponent, 3 mantissa; no infinities, largest 448).
+   E8M0 is a power of two as a scale: byte e stands for 2^(e - 127), 255 for NaN. */
 typedef enum {
   PSISPEC_F32 = 0,
   PSISPEC_BF16 = 1,
   PSISPEC_F16 = 2,
-  PSISPEC_F8E4M3 = 3
+  PSISPEC_F8E4M3 = 3,
+  PSISPEC_E8M0 = 4
 } psispec_dtype;
 
 /* flags */
@@ -498,6 +500,105 @@ psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* tab
                                      const int32_t* len, const int32_t* n_new, int32_t blk,
                                      int32_t* status, int32_t batch, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/*
+ * The layers around the paged attention: the norm of the residual stream and linear layers with frozen
+ * weights of 4 bits, for the rows of a draft or verify forward (one token of one line up to a block of
+ * every line; prompts too).
+ *
+ * psispec_add_rmsnorm, in one pass over the rows:
+ *   h = x + residual;  residual_out = h;  y = h / sqrt(mean(h^2) + eps) * weight
+ * in 32 bits; h is normalised as the 32-bit sum, y and residual_out are rounded once.  out holds y, or
+ * 8-bit numbers q = y / s (clamped to +-448, to nearest) with
+ *   scale_dtype F32   one s per row: the row's largest |y| / 448
+ *   scale_dtype E8M0  one s per 32 columns: the smallest power of two (from 2^-127) with |y| <= 448 s in
+ *                     the block; what psispec_w4_linear and psispec_w4_gated take
+ * A row (block) of zeros has q = 0; one with an infinity or a NaN has an infinite or NaN scale, its q are
+ * unspecified.
+ *   x             rows of dim elements, x_stride elements apart; dtype PSISPEC_BF16 or PSISPEC_F16
+ *   residual      rows of residual_dtype (dtype or PSISPEC_F32), or NULL: h = x
+ *   residual_out  rows of residual_dtype, or NULL: h is not written
+ *   weight        [dim] of dtype, or NULL: 1
+ *   eps           >= 0, finite in 32 bits
+ *   rows 0..2^24-1 (0 launches nothing);  dim 1..32768, a multiple of 32 with E8M0 scales
+ *   out           rows of out_dtype: dtype or PSISPEC_F8E4M3
+ *   scale         with F8E4M3 only (NULL otherwise): [rows] f32, or rows of dim / 32 bytes, scale_stride apart
+ * Rows may start anywhere (those 16-byte aligned are read and written 16 bytes at a time).  residual_out and
+ * out may each be the rows of x or of residual themselves; every other overlap of an output with an input or
+ * another output is refused (PSISPEC_EINVAL).  Asynchronous on `stream`; no workspace.
+ */
+psispec_status psispec_add_rmsnorm(const void* x, int64_t x_stride, psispec_dtype dtype,
+                                   const void* residual, int64_t residual_stride,
+                                   void* residual_out, int64_t residual_out_stride,
+                                   psispec_dtype residual_dtype, const void* weight, double eps,
+                                   int32_t rows, int32_t dim, void* out, int64_t out_stride,
+                                   psispec_dtype out_dtype, void* scale, int64_t scale_stride,
+                                   psispec_dtype scale_dtype, void* stream);
+
+/*
+ * Weights of 4 bits: w[n][k] = code[n][k] * scale[n][k / group], n outputs, k inputs.
+ *   PSISPEC_W4_INT  codes are two's complement, -8..7; scales BF16 or F16, group 32, 64 or a multiple of 128
+ *   PSISPEC_W4_MX   codes are floats of sign, 2 bits of exponent, 1 of mantissa (0, 0.5, 1, 1.5, 2, 3, 4,
+ *                   6 and their negatives from code 8 on); scales E8M0, group 32
+ * psispec_w4_pack writes a layer's codes and scales, as a checkpoint holds them, in the order in which the
+ * products read them into `packed` (device, 256-byte aligned, psispec_w4_packed_bytes, the caller's for as long
+ * as the layer is used).  Once per layer; the codes and scales are not needed afterwards.
+ *   codes      row n at n * codes_stride bytes: k / 2 bytes, the even input's code in the low four bits
+ *   scales     row n at n * scales_stride elements: ceil(k / group) of scale_dtype (a last group may be short)
+ */
+typedef enum { PSISPEC_W4_INT = 0, PSISPEC_W4_MX = 1 } psispec_w4_format;
+typedef enum { PSISPEC_W4_SILU = 0, PSISPEC_W4_GELU = 1, PSISPEC_W4_GELU_TANH = 2 } psispec_w4_activation;
+typedef struct {
+  void* packed;        /* device; the products only read it */
+  int32_t n;           /* outputs, 1..2^20 */
+  int32_t k;           /* inputs, a multiple of 32, 32..2^20 */
+  int32_t group;       /* inputs per scale */
+  int32_t format;      /* psispec_w4_format */
+  int32_t scale_dtype; /* PSISPEC_BF16 or PSISPEC_F16 (INT), PSISPEC_E8M0 (MX) */
+  int32_t reserved;    /* must be 0 */
+} psispec_w4_weight;
+
+size_t psispec_w4_packed_bytes(int32_t n, int32_t k, int32_t group, int32_t format);
+
+psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const void* scales,
+                               int64_t scales_stride, const psispec_w4_weight* w,
+                               size_t packed_bytes, void* stream);
+
+/*
+ * A linear layer, and the two projections of a gated feed-forward block with their activation and product:
+ *   psispec_w4_linear  out = x w^T + bias
+ *   psispec_w4_gated   out = act(x gate^T) * (x up^T),  act(a) = a / (1 + exp(-a))   (PSISPEC_W4_SILU)
+ *                      or a (1 + erf(a / sqrt 2)) / 2                                 (PSISPEC_W4_GELU)
+ *                      or a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2           (PSISPEC_W4_GELU_TANH)
+ * Codes and rows enter the matrix cores as they are, the sums are of 32 bits, INT scales are applied to the
+ * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  (F16 rows with MX weights:
+ * exact for scales down to 2^-36 of the output's largest, smaller ones give weights off by at most 2^-38 of
+ * that largest scale.)  Infinities in x give infinities or NaN.
+ *   x        rows of k elements, x_stride elements apart, 16-byte aligned, strides of 16-byte multiples: dtype
+ *            PSISPEC_BF16, PSISPEC_F16, or (MX weights) PSISPEC_F8E4M3 with x_scale: rows of k / 32 E8M0 bytes,
+ *            x_scale_stride apart (NULL for the other types).  8-bit rows go through the scaled matrix
+ *            instruction at twice the 16-bit rate
+ *   bias     [n] of out_dtype, or NULL
+ *   out      rows of n elements, out_stride elements apart, of dtype (8-bit x: BF16 or F16); overlaps no input
+ *            (PSISPEC_EINVAL)
+ *   rows     0..2^24-1 (0 launches nothing), ceil(rows / 16) * ceil(n / 16) < 2^23
+ *   gate, up of the same n, k, group and format
+ * The workspace is psispec_w4_workspace(rows, n, k, 1) bytes, (.., 2) for a gated call; 0: none is needed and
+ * NULL will do.  Sums are taken in a fixed order: reruns are bitwise identical.
+ */
+size_t psispec_w4_workspace(int32_t rows, int32_t n, int32_t k, int32_t mats);
+
+psispec_status psispec_w4_linear(const psispec_w4_weight* w, const void* x, int64_t x_stride,
+                                 psispec_dtype dtype, const void* x_scale, int64_t x_scale_stride,
+                                 int32_t rows, const void* bias, void* out, int64_t out_stride,
+                                 psispec_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+psispec_status psispec_w4_gated(const psispec_w4_weight* gate, const psispec_w4_weight* up,
+                                int32_t activation, const void* x, int64_t x_stride,
+                                psispec_dtype dtype, const void* x_scale, int64_t x_scale_stride,
+                                int32_t rows, void* out, int64_t out_stride, psispec_dtype out_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Message for a return code (static string). */
 const char* psispec_strerror(psispec_status code);

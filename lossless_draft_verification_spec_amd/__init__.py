@@ -19,12 +19,14 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpsispec.so")
 
-PSISPEC_F32, PSISPEC_BF16, PSISPEC_F16, PSISPEC_F8E4M3 = 0, 1, 2, 3
+PSISPEC_F32, PSISPEC_BF16, PSISPEC_F16, PSISPEC_F8E4M3, PSISPEC_E8M0 = 0, 1, 2, 3, 4
 PSISPEC_FIRST_FROM_TARGET = 1
 PSISPEC_MAX_CHILDREN_SHIFT = 4  # flags bits 4..7: bound on children per node (sampled tree)
 ST_NONFINITE, ST_BAD_TOKEN, ST_Q_ZERO, ST_RESID_ZERO, ST_BAD_PARENT = 1, 2, 4, 8, 16
 ST_BAD_KEEP, ST_BAD_PAGE, ST_NO_PAGE = 32, 64, 128
 PSISPEC_ROPE_INTERLEAVED = 1
+PSISPEC_W4_INT, PSISPEC_W4_MX = 0, 1
+PSISPEC_W4_SILU, PSISPEC_W4_GELU, PSISPEC_W4_GELU_TANH = 0, 1, 2
 
 EXPORTS = ("psispec_verify_linear_workspace", "psispec_verify_linear",
            "psispec_verify_linear_noalloc",
@@ -32,7 +34,9 @@ EXPORTS = ("psispec_verify_linear_workspace", "psispec_verify_linear",
            "psispec_lmhead_verify", "psispec_sample_drafts_workspace", "psispec_sample_drafts",
            "psispec_kv_commit", "psispec_qkv_append", "psispec_paged_attention_workspace",
            "psispec_paged_attention", "psispec_paged_commit", "psispec_pages_workspace",
-           "psispec_pages_assign", "psispec_pages_reserve", "psispec_strerror", "psispec_timing_enable",
+           "psispec_pages_assign", "psispec_pages_reserve", "psispec_add_rmsnorm",
+           "psispec_w4_packed_bytes", "psispec_w4_pack", "psispec_w4_workspace", "psispec_w4_linear",
+           "psispec_w4_gated", "psispec_strerror", "psispec_timing_enable",
            "psispec_timing_read", "psispec_peak_read", "psispec_peak_mfma")
 
 
@@ -67,6 +71,11 @@ class psispec_page_pool(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int64),
                 ("planes", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class psispec_w4_weight(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+        "n", "k", "group", "format", "scale_dtype", "reserved")]
 
 
 _lib = None
@@ -123,6 +132,19 @@ def lib():
         L.psispec_pages_assign.restype = i32
         L.psispec_pages_reserve.argtypes = [P, P, i64, i32, P, P, P, i32, P, i32, P, sz, P]
         L.psispec_pages_reserve.restype = i32
+        L.psispec_add_rmsnorm.argtypes = [P, i64, i32, P, i64, P, i64, i32, P, ctypes.c_double, i32, i32,
+                                          P, i64, i32, P, i64, i32, P]
+        L.psispec_add_rmsnorm.restype = i32
+        L.psispec_w4_packed_bytes.argtypes = [i32, i32, i32, i32]
+        L.psispec_w4_packed_bytes.restype = sz
+        L.psispec_w4_pack.argtypes = [P, i64, P, i64, P, sz, P]
+        L.psispec_w4_pack.restype = i32
+        L.psispec_w4_workspace.argtypes = [i32, i32, i32, i32]
+        L.psispec_w4_workspace.restype = sz
+        L.psispec_w4_linear.argtypes = [P, P, i64, i32, P, i64, i32, P, P, i64, i32, P, sz, P]
+        L.psispec_w4_linear.restype = i32
+        L.psispec_w4_gated.argtypes = [P, P, i32, P, i64, i32, P, i64, i32, P, i64, i32, P, sz, P]
+        L.psispec_w4_gated.restype = i32
         L.psispec_strerror.argtypes = [i32]
         L.psispec_strerror.restype = ctypes.c_char_p
         L.psispec_timing_enable.argtypes = [i32]
@@ -944,6 +966,249 @@ def psispec_pages_reserve(pool: torch.Tensor, table: torch.Tensor, refs: torch.T
                                          workspace.data_ptr(), workspace.numel(), _dev_stream(dev))
     _check(rc, "psispec_pages_reserve")
     return status
+
+
+def _rows_of(t: torch.Tensor, width: int, dev, name: str):
+    """(pointer, elements from one row to the next, rows) of [..., width]: rows of contiguous elements,
+    evenly spaced."""
+    if t.get_device() != dev.index:
+        _gpu_device(t, name)
+        _same_dev(t, dev, name)
+    shape, st = t.shape, t.stride()
+    if len(shape) < 1 or shape[-1] != width:
+        raise PsispecError(f"{name} must be [..., {width}], got {list(shape)}")
+    if len(shape) == 2:
+        rows, step = shape[0], st[0]
+        if (st[1] == 1 or width == 1) and (step >= width or rows <= 1):
+            return t.data_ptr(), step if rows > 1 else width, rows
+    rows, step = 1, width
+    if width > 1 and st[-1] != 1:
+        raise PsispecError(f"the rows of {name} must be contiguous")
+    for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 0:
+            return t.data_ptr(), width, 0
+        if n == 1:
+            continue
+        if rows == 1:
+            step = x
+        elif x != rows * step:
+            raise PsispecError(f"the rows of {name} must be evenly spaced")
+        rows *= n
+    if rows > 1 and step < width:
+        raise PsispecError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), step, rows
+
+
+_SIXTEEN = {torch.bfloat16: PSISPEC_BF16, torch.float16: PSISPEC_F16}
+_LAYER_DTYPES = {**_SIXTEEN, torch.float8_e4m3fn: PSISPEC_F8E4M3}
+
+
+def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
+                        residual: torch.Tensor | None = None,
+                        residual_out: torch.Tensor | None = None, eps: float = 1e-6,
+                        quant: str | None = None, out: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None, stream=None):
+    """The residual's addition and the root-mean-square norm: h = x + residual, out = h / sqrt(mean(h^2) +
+    eps) * weight.  x [..., dim] (bf16 or f16; rows evenly spaced), weight [dim] of x's dtype (1 when not
+    given), residual of x's shape and dtype or float32.  h is written to residual_out (residual's dtype; by
+    default residual itself, which then holds the new residual stream; without residual only when
+    given).  quant: None, "row" (out float8_e4m3fn, one float32 scale per row: the row's largest value
+    over 448) or "mx" (float8_e4m3fn with a float8_e8m0fnu scale per 32 columns, the smallest power of two
+    that keeps them within 448: the rows of psispec_w4_linear and psispec_w4_gated); out times scale
+    is the norm.  Returns (out, residual_out, scale), None for what there is not."""
+    if x.dim() < 1:
+        raise PsispecError("x must be [..., dim]")
+    dim, dt = x.shape[-1], x.dtype
+    dev, code = _gpu_device(x, "x"), _SIXTEEN.get(dt)
+    if code is None:
+        raise PsispecError(f"x must be bfloat16 or float16, got {dt}")
+    if quant not in (None, "row", "mx"):
+        raise PsispecError(f'quant must be None, "row" or "mx", got {quant!r}')
+    xp, xs, rows = _rows_of(x, dim, dev, "x")
+    wp = 0 if weight is None else _flat(weight, (dim,), dt, dev, "weight")
+    rp = rs = rop = ros = 0
+    rcode = code
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        if residual.dtype != dt and residual.dtype != torch.float32:
+            raise PsispecError(f"residual must be {dt} or float32, got {residual.dtype}")
+        if residual.shape != x.shape:
+            raise PsispecError("residual must have the shape of x")
+        rp, rs, _ = _rows_of(residual, dim, dev, "residual")
+    if residual_out is not None:
+        rt = residual_out.dtype
+        if rt != (dt if residual is None else residual.dtype) and (residual is not None
+                                                                   or rt != torch.float32):
+            raise PsispecError("residual_out must have the dtype of residual (of x, or float32, without)")
+        if residual_out.shape != x.shape:
+            raise PsispecError("residual_out must have the shape of x")
+        rop, ros, _ = _rows_of(residual_out, dim, dev, "residual_out")
+        if rt == torch.float32:
+            rcode = PSISPEC_F32
+    ot = dt if quant is None else torch.float8_e4m3fn
+    sp, ss, scode = 0, 0, PSISPEC_F32
+    with _On.guard(dev, stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=ot, device=dev)
+        elif out.dtype != ot or out.shape != x.shape:
+            raise PsispecError(f"out must be {ot} with the shape of x")
+        op, os_, _ = _rows_of(out, dim, dev, "out")
+        if quant == "row":
+            if scale is None:
+                scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            sp = _flat(scale, x.shape[:-1], torch.float32, dev, "scale")
+        elif quant == "mx":
+            if dim % 32:
+                raise PsispecError("mx scales need a multiple of 32 columns")
+            if scale is None:
+                scale = torch.empty((*x.shape[:-1], dim // 32), dtype=torch.float8_e8m0fnu, device=dev)
+            elif scale.dtype != torch.float8_e8m0fnu or scale.shape[:-1] != x.shape[:-1]:
+                raise PsispecError("scale must be float8_e8m0fnu [..., dim / 32]")
+            sp, ss, _ = _rows_of(scale, dim // 32, dev, "scale")
+            scode = PSISPEC_E8M0
+        elif scale is not None:
+            raise PsispecError("scale goes with quant")
+        rc = lib().psispec_add_rmsnorm(xp, xs, code, rp, rs, rop, ros, rcode, wp, eps, rows, dim, op, os_,
+                                       _LAYER_DTYPES[ot], sp, ss, scode, _dev_stream(dev))
+    _check(rc, "psispec_add_rmsnorm")
+    return out, residual_out, scale
+
+
+class W4Weight:
+    """A linear layer's weights of 4 bits in the library's order (psispec_w4_pack): out_features,
+    in_features, group, format ("int" or "mx"), packed (uint8)."""
+
+    __slots__ = ("packed", "out_features", "in_features", "group", "format", "device", "_struct")
+
+    def __init__(self, packed, out_features, in_features, group, format, scale_dtype):
+        self.packed, self.out_features, self.in_features = packed, out_features, in_features
+        self.group, self.format, self.device = group, format, packed.device
+        self._struct = _W4_STRUCT.pack(packed.data_ptr(), out_features, in_features, group,
+                                       _W4_FORMATS[format], scale_dtype, 0)
+
+
+_W4_STRUCT = struct.Struct("Q6i")  # psispec_w4_weight
+_W4_FORMATS = {"int": PSISPEC_W4_INT, "mx": PSISPEC_W4_MX}
+_W4_ACTIVATIONS = {"silu": PSISPEC_W4_SILU, "gelu": PSISPEC_W4_GELU, "gelu_tanh": PSISPEC_W4_GELU_TANH}
+
+
+def w4_packed_bytes(out_features, in_features, group, format) -> int:
+    return int(lib().psispec_w4_packed_bytes(out_features, in_features, group, _W4_FORMATS[format]))
+
+
+def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "int", group: int = 128,
+                    packed: torch.Tensor | None = None, stream=None) -> W4Weight:
+    """A layer's weights for psispec_w4_linear and psispec_w4_gated, once when it is loaded.  codes uint8
+    [out_features][in_features / 2], the even input's code in the low four bits; scales [out_features]
+    [ceil(in_features / group)].  "int": two's complement codes, scales bfloat16 or float16, group 32, 64
+    or a multiple of 128; "mx": 4-bit floats (sign, 2 bits of exponent, 1 of mantissa), scales
+    float8_e8m0fnu, group 32.  in_features is a multiple of 32.  packed: uint8 of w4_packed_bytes at
+    least (allocated when not given); codes and scales are not needed afterwards."""
+    if format not in _W4_FORMATS:
+        raise PsispecError(f'format must be "int" or "mx", got {format!r}')
+    dev = _gpu_device(codes, "codes")
+    if codes.dtype != torch.uint8 or codes.dim() != 2:
+        raise PsispecError("codes must be uint8 [out_features][in_features / 2]")
+    n, k = codes.shape[0], 2 * codes.shape[1]
+    want = (torch.float8_e8m0fnu,) if format == "mx" else (torch.bfloat16, torch.float16)
+    if scales.dtype not in want:
+        raise PsispecError(f"scales must be {' or '.join(map(str, want))}, got {scales.dtype}")
+    group = int(group)
+    if group < 1 or scales.shape != (n, -(-k // group)):
+        raise PsispecError("scales must be [out_features][ceil(in_features / group)]")
+    need = w4_packed_bytes(n, k, group, format)
+    if need == 0:
+        raise PsispecError("unsupported sizes (in_features a multiple of 32, at most 2^20 features; group 32 "
+                           "for mx, 32, 64 or a multiple of 128 for int)")
+    cp, cs, _ = _rows_of(codes, k // 2, dev, "codes")
+    sp, ss, _ = _rows_of(scales, scales.shape[1], dev, "scales")
+    with _On.guard(dev, stream):
+        packed = _workspace_for(packed, need, dev, "psispec_w4_pack")
+        w = W4Weight(packed, n, k, group, format,
+                     PSISPEC_E8M0 if format == "mx" else _SIXTEEN[scales.dtype])
+        rc = lib().psispec_w4_pack(cp, cs, sp, ss, w._struct, packed.numel(), _dev_stream(dev))
+    _check(rc, "psispec_w4_pack")
+    return w
+
+
+@functools.lru_cache(maxsize=4096)
+def w4_workspace_bytes(rows, out_features, in_features, matrices=1) -> int:
+    return int(lib().psispec_w4_workspace(rows, out_features, in_features, matrices))
+
+
+def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace, stream):
+    k, n, dt = w.in_features, w.out_features, x.dtype
+    dev, code = _gpu_device(x, "x"), _LAYER_DTYPES.get(dt)
+    if code is None:
+        raise PsispecError(f"x must be bfloat16, float16 or float8_e4m3fn, got {dt}")
+    _same_dev(w, dev, "the weight")
+    xp, xs, rows = _rows_of(x, k, dev, "x")
+    sp = ss = 0
+    if code == PSISPEC_F8E4M3:
+        if w.format != "mx":
+            raise PsispecError("8-bit rows go with mx weights")
+        if x_scale is None or x_scale.dtype != torch.float8_e8m0fnu or x_scale.shape[:-1] != x.shape[:-1]:
+            raise PsispecError("8-bit rows need x_scale, float8_e8m0fnu [..., in_features / 32]")
+        sp, ss, _ = _rows_of(x_scale, k // 32, dev, "x_scale")
+        ot = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    else:
+        if x_scale is not None:
+            raise PsispecError("x_scale goes with 8-bit rows")
+        ot = out_dtype or dt
+    ocode = _SIXTEEN.get(ot)
+    if ocode is None or (code != PSISPEC_F8E4M3 and ot != dt):
+        raise PsispecError("out must be of x's dtype (bfloat16 or float16 for 8-bit rows)")
+    shape = (*x.shape[:-1], n)
+    bp = 0 if bias is None else _flat(bias, (n,), ot, dev, "bias")
+    with _On.guard(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=ot, device=dev)
+        elif out.dtype != ot or out.shape != shape:
+            raise PsispecError(f"out must be {ot} {list(shape)}")
+        op, os_, _ = _rows_of(out, n, dev, "out")
+        need = w4_workspace_bytes(rows, n, k, 1 if w2 is None else 2)
+        wp = wn = 0
+        if need:
+            workspace = _workspace_for(workspace, need, dev, what)
+            wp, wn = workspace.data_ptr(), workspace.numel()
+        if w2 is None:
+            rc = lib().psispec_w4_linear(w._struct, xp, xs, code, sp, ss, rows, bp, op, os_, ocode, wp, wn,
+                                         _dev_stream(dev))
+        else:
+            rc = lib().psispec_w4_gated(w._struct, w2._struct, act, xp, xs, code, sp, ss, rows, op, os_,
+                                        ocode, wp, wn, _dev_stream(dev))
+    _check(rc, what)
+    return out
+
+
+def psispec_w4_linear(x: torch.Tensor, weight: W4Weight, x_scale: torch.Tensor | None = None,
+                      bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """A linear layer with weights of 4 bits: x [..., in_features] (bf16, f16; or, with mx weights,
+    float8_e4m3fn with x_scale float8_e8m0fnu [..., in_features / 32], psispec_add_rmsnorm's "mx" rows)
+    to out [..., out_features] of x's dtype (bf16, or f16 by out_dtype or out, for 8-bit rows).
+    Rows 16-byte aligned and evenly spaced; bias [out_features] of out's dtype."""
+    return _w4_product("psispec_w4_linear", x, weight, None, 0, x_scale, bias, out, out_dtype, workspace,
+                       stream)
+
+
+def psispec_w4_gated(x: torch.Tensor, gate: W4Weight, up: W4Weight, activation: str = "silu",
+                     x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Both projections of a gated feed-forward block, the activation and the product in one kernel:
+    act(x gate^T) * (x up^T), activation "silu", "gelu" or "gelu_tanh"; x, x_scale and out as in
+    psispec_w4_linear, gate and up of the same features, group and format."""
+    act = _W4_ACTIVATIONS.get(activation)
+    if act is None:
+        raise PsispecError(f'activation must be "silu", "gelu" or "gelu_tanh", got {activation!r}')
+    if (up.out_features, up.in_features, up.group, up.format) != (
+            gate.out_features, gate.in_features, gate.group, gate.format):
+        raise PsispecError("gate and up must have the same features, group and format")
+    _same_dev(up, gate.device, "up")
+    return _w4_product("psispec_w4_gated", x, gate, up, act, x_scale, None, out, out_dtype, workspace, stream)
 
 
 def peak_read(buf: torch.Tensor, out: torch.Tensor, blocks: int, stream=None):

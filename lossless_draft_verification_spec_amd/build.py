@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "rows.hip", "topp.hip", "linear.hip", "tree.hip", "draw.hip", "drafts.hip",
            "kv.hip", "treeq.hip", "lmhead.hip", "peak.hip", "append.hip", "attend.hip", "attend_bf16.hip",
            "attend_f16.hip", "attend_bf16_f8.hip", "attend_f16_f8.hip", "pages.hip",
-           "paged_api.hip"]
+           "paged_api.hip", "norm.hip", "w4_pack.hip", "w4.hip", "w4_few_bf16.hip", "w4_few_f16.hip",
+           "w4_few_f8.hip", "layers_api.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are disabled for every HIP object.

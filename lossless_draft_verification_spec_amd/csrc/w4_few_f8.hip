@@ -1,0 +1,10 @@
+// w4_few_f8.hip -- the 4-bit products of few rows for rows of 8 bits.
+#include "w4_few.h"
+
+namespace psispec {
+
+hipError_t launch_w4_few_f8(const W4Args& a, int mats, hipStream_t stream) {
+  return mats == 2 ? w4::launch_few<w4::F8, 0, 2>(a, stream) : w4::launch_few<w4::F8, 0, 1>(a, stream);
+}
+
+}  // namespace psispec
