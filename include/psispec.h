@@ -582,7 +582,7 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *   out      rows of n elements, out_stride elements apart, of dtype (8-bit x: BF16 or F16); overlaps no input
  *            (PSISPEC_EINVAL)
  *   rows     0..2^24-1 (0 launches nothing), ceil(rows / 16) * ceil(n / 16) < 2^23
- *   gate, up of the same n, k, group and format
+ *   gate, up of the same n, k, group, format and scale_dtype
  * The workspace is psispec_w4_workspace(rows, n, k, 1) bytes, (.., 2) for a gated call; 0: none is needed and
  * NULL will do.  Sums are taken in a fixed order: reruns are bitwise identical.
  */

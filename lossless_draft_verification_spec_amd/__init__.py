@@ -1077,18 +1077,19 @@ def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
 
 class W4Weight:
     """A linear layer's weights of 4 bits in the library's order (psispec_w4_pack): out_features,
-    in_features, group, format ("int" or "mx"), packed (uint8)."""
+    in_features, group, format ("int" or "mx"), scale_dtype, packed (uint8)."""
 
-    __slots__ = ("packed", "out_features", "in_features", "group", "format", "device", "_struct")
+    __slots__ = ("packed", "out_features", "in_features", "group", "format", "scale_dtype", "device", "_struct")
 
     def __init__(self, packed, out_features, in_features, group, format, scale_dtype):
         self.packed, self.out_features, self.in_features = packed, out_features, in_features
-        self.group, self.format, self.device = group, format, packed.device
+        self.group, self.format, self.scale_dtype, self.device = group, format, scale_dtype, packed.device
         self._struct = _W4_STRUCT.pack(packed.data_ptr(), out_features, in_features, group,
-                                       _W4_FORMATS[format], scale_dtype, 0)
+                                       _W4_FORMATS[format], _W4_SCALES[scale_dtype], 0)
 
 
 _W4_STRUCT = struct.Struct("Q6i")  # psispec_w4_weight
+_W4_SCALES = {**_SIXTEEN, torch.float8_e8m0fnu: PSISPEC_E8M0}
 _W4_FORMATS = {"int": PSISPEC_W4_INT, "mx": PSISPEC_W4_MX}
 _W4_ACTIVATIONS = {"silu": PSISPEC_W4_SILU, "gelu": PSISPEC_W4_GELU, "gelu_tanh": PSISPEC_W4_GELU_TANH}
 
@@ -1125,8 +1126,7 @@ def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "in
     sp, ss, _ = _rows_of(scales, scales.shape[1], dev, "scales")
     with _On.guard(dev, stream):
         packed = _workspace_for(packed, need, dev, "psispec_w4_pack")
-        w = W4Weight(packed, n, k, group, format,
-                     PSISPEC_E8M0 if format == "mx" else _SIXTEEN[scales.dtype])
+        w = W4Weight(packed, n, k, group, format, scales.dtype)
         rc = lib().psispec_w4_pack(cp, cs, sp, ss, w._struct, packed.numel(), _dev_stream(dev))
     _check(rc, "psispec_w4_pack")
     return w
@@ -1200,13 +1200,14 @@ def psispec_w4_gated(x: torch.Tensor, gate: W4Weight, up: W4Weight, activation: 
                      stream=None) -> torch.Tensor:
     """Both projections of a gated feed-forward block, the activation and the product in one kernel:
     act(x gate^T) * (x up^T), activation "silu", "gelu" or "gelu_tanh"; x, x_scale and out as in
-    psispec_w4_linear, gate and up of the same features, group and format."""
+    psispec_w4_linear, gate and up of the same features, group,
+    format and scale type."""
     act = _W4_ACTIVATIONS.get(activation)
     if act is None:
         raise PsispecError(f'activation must be "silu", "gelu" or "gelu_tanh", got {activation!r}')
-    if (up.out_features, up.in_features, up.group, up.format) != (
-            gate.out_features, gate.in_features, gate.group, gate.format):
-        raise PsispecError("gate and up must have the same features, group and format")
+    if (up.out_features, up.in_features, up.group, up.format, up.scale_dtype) != (
+            gate.out_features, gate.in_features, gate.group, gate.format, gate.scale_dtype):
+        raise PsispecError("gate and up must have the same features, group, format and scale type")
     _same_dev(up, gate.device, "up")
     return _w4_product("psispec_w4_gated", x, gate, up, act, x_scale, None, out, out_dtype, workspace, stream)
 

@@ -20,7 +20,7 @@ SOURCES = ["api.hip", "rows.hip", "topp.hip", "linear.hip", "tree.hip", "draw.hi
            "kv.hip", "treeq.hip", "lmhead.hip", "peak.hip", "append.hip", "attend.hip", "attend_bf16.hip",
            "attend_f16.hip", "attend_bf16_f8.hip", "attend_f16_f8.hip", "pages.hip",
            "paged_api.hip", "norm.hip", "w4_pack.hip", "w4.hip", "w4_few_bf16.hip", "w4_few_f16.hip",
-           "w4_few_f8.hip", "layers_api.hip"]
+           "w4_few_f8.hip", "w4_many_bf16.hip", "w4_many_f16.hip", "w4_many_f8.hip", "layers_api.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are disabled for every HIP object.

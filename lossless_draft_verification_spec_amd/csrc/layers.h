@@ -26,7 +26,7 @@ hipError_t launch_add_rmsnorm(const AddNormArgs& a, psispec_dtype dtype, hipStre
 //   PSISPEC_W4_INT  32 j + 8 g + 0..7: nibble s, s + 4 = inputs 2s, 2s + 1 of the eight, code + 8
 //   PSISPEC_W4_MX   32 g + 8 j + 0..7: nibble s = input s, the code as it is
 // so word j is the lane's part of the j-th 16x16x32 matrix instruction of the tile (and the 16 bytes,
-// for MX, its part of the 16x16x128 one).  Scales: INT [tile][16 outputs][groups per tile] in 16 bits,
+// for MX, its part of the 16x16x128 one).  Scales: INT [tile][groups per tile][16 outputs] in 16 bits,
 // MX [tile][64 lanes] a byte.  top (MX): the largest scale byte of each output.
 struct W4Layout {
   int ntiles, ktiles, gpt;  // tiles of outputs, of inputs; groups per tile (INT; larger groups repeat)
@@ -58,7 +58,7 @@ struct W4Args {
   const uint8_t* codes[2];  // the second of a gated call: the matrix that multiplies
   const void* scales[2];
   const uint8_t* top[2];
-  int scale_f16[2];
+  int scale_f16;  // INT scales F16, else BF16
   const void* x;
   const uint8_t* x_scale;  // 8-bit rows: scale byte of every 32 inputs
   const void* bias;
@@ -67,11 +67,16 @@ struct W4Args {
   int rows, n, k, ntiles, ktiles, gpt;
   int act;      // psispec_w4_activation of a gated call
   int out_f16;  // out (and bias) F16, else BF16
+  int out_vec;  // rows of out start at multiples of 8 bytes
   void* workspace;
 };
 hipError_t launch_w4_few_bf16(const W4Args& a, int format, int mats, hipStream_t stream);
 hipError_t launch_w4_few_f16(const W4Args& a, int format, int mats, hipStream_t stream);
 hipError_t launch_w4_few_f8(const W4Args& a, int mats, hipStream_t stream);
+hipError_t launch_w4_many_bf16(const W4Args& a, int format, int mats, hipStream_t stream);
+hipError_t launch_w4_many_f16(const W4Args& a, int format, int mats, hipStream_t stream);
+hipError_t launch_w4_many_f8(const W4Args& a, int mats, hipStream_t stream);
+size_t w4_many_workspace_bytes(int rows, int n, int k, int mats);
 size_t w4_workspace_bytes(int rows, int n, int k, int mats);
 hipError_t launch_w4(const W4Args& a, psispec_dtype dtype, int format, int mats, hipStream_t stream);
 

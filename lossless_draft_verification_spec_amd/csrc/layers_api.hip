@@ -80,7 +80,8 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
   const bool f8 = dtype == PSISPEC_F8E4M3;
   if (f8 ? out_dtype != PSISPEC_BF16 && out_dtype != PSISPEC_F16 : out_dtype != dtype) return PSISPEC_EDTYPE;
   if (f8 && w->format != PSISPEC_W4_MX) return PSISPEC_EUNSUPPORTED;
-  if (w2 && (w2->n != w->n || w2->k != w->k || w2->group != w->group || w2->format != w->format)) return PSISPEC_EINVAL;
+  if (w2 && (w2->n != w->n || w2->k != w->k || w2->group != w->group || w2->format != w->format ||
+             w2->scale_dtype != w->scale_dtype)) return PSISPEC_EINVAL;
   if (rows < 0 || rows > kMaxRows) return PSISPEC_EINVAL;
   const int mats = w2 ? 2 : 1;
   const W4Layout l = w4_layout(w->n, w->k, w->group, w->format);
@@ -105,8 +106,8 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
     a.codes[i] = static_cast<const uint8_t*>(p->packed);
     a.scales[i] = a.codes[i] + l.scales_at;
     a.top[i] = a.codes[i] + l.top_at;
-    a.scale_f16[i] = p->scale_dtype == PSISPEC_F16;
   }
+  a.scale_f16 = w->scale_dtype == PSISPEC_F16;
   a.x = x;
   a.x_scale = static_cast<const uint8_t*>(x_scale);
   a.bias = bias;
@@ -122,6 +123,7 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
   a.gpt = l.gpt;
   a.act = act;
   a.out_f16 = out_dtype == PSISPEC_F16;
+  a.out_vec = aligned(out, 8) && a.out_stride % 4 == 0;
   a.workspace = workspace;
   return launch_w4(a, dtype, w->format, mats, static_cast<hipStream_t>(stream)) == hipSuccess ? PSISPEC_OK
                                                                                               : PSISPEC_EHIP;

@@ -1,8 +1,8 @@
 // w4.h -- what the kernels of the 4-bit products share: the weights' decoding, the activation, the store.
 //
-// The matrix instructions take rows of x as their first operand and 16 outputs as their second; lane l
-// holds row (output) l % 16, inputs of its quarter g = l / 16, and of the result column l % 16 (an
-// output), rows 4 g + 0..3.
+// The matrix instructions take 16 outputs as their first operand and 16 rows of x as their second; lane l
+// holds output (row) l % 16, inputs of its quarter g = l / 16, and of the result outputs 4 g + 0..3 of row
+// l % 16: neighbours, stored together.
 //
 // INT codes enter the product as 16 + (code + 8) = code + 24, a shift and an and-or per pair: the four
 // bits lie right below the exponent of 16.  Their product with a group of inputs starts from
@@ -29,23 +29,35 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 struct F8 {};  // rows of e4m3 with a power of two per 32 inputs
 
-__device__ inline f32x4 mfma(u32x4 x, u32x4 w, f32x4 c, __bf16) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
-                                                 __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+__device__ inline f32x4 mfma(u32x4 w, u32x4 x, f32x4 c, __bf16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
+                                                 __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
 }
-__device__ inline f32x4 mfma(u32x4 x, u32x4 w, f32x4 c, _Float16) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x),
-                                                __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+__device__ inline f32x4 mfma(u32x4 w, u32x4 x, f32x4 c, _Float16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w),
+                                                __builtin_bit_cast(f16x8, x), c, 0, 0, 0);
 }
 
-// 8 INT codes (word of the packed layout) as code + 24
-__device__ inline u32x4 int_codes(uint32_t w, __bf16) {
-  return u32x4{((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-               ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
+// The numbers of int_codes in registers: an and-or takes one literal at most, and two of them make the compiler
+// split it.
+struct IntBits {
+  uint32_t mask, magic;
+};
+template <typename X>
+__device__ inline IntBits int_bits() {
+  IntBits b{__is_same(X, __bf16) ? 0x00780078u : 0x03c003c0u, __is_same(X, __bf16) ? 0x41804180u : 0x4c004c00u};
+  asm("" : "+s"(b.mask));
+  asm("" : "+v"(b.magic));
+  return b;
 }
-__device__ inline u32x4 int_codes(uint32_t w, _Float16) {
-  return u32x4{((w << 6) & 0x03c003c0u) | 0x4c004c00u, ((w << 2) & 0x03c003c0u) | 0x4c004c00u,
-               ((w >> 2) & 0x03c003c0u) | 0x4c004c00u, ((w >> 6) & 0x03c003c0u) | 0x4c004c00u};
+// 8 INT codes (word of the packed layout) as code + 24
+__device__ inline u32x4 int_codes(uint32_t w, IntBits k, __bf16) {
+  return u32x4{((w << 3) & k.mask) | k.magic, ((w >> 1) & k.mask) | k.magic, ((w >> 5) & k.mask) | k.magic,
+               ((w >> 9) & k.mask) | k.magic};
+}
+__device__ inline u32x4 int_codes(uint32_t w, IntBits k, _Float16) {
+  return u32x4{((w << 6) & k.mask) | k.magic, ((w << 2) & k.mask) | k.magic, ((w >> 2) & k.mask) | k.magic,
+               ((w >> 6) & k.mask) | k.magic};
 }
 // eight times -24
 __device__ inline u32x4 minus24(__bf16) { return u32x4{0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u}; }
@@ -88,6 +100,14 @@ __device__ inline u32x4 f8_rows(uint32_t lo, uint32_t hi, float scale) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
 }
 
+// 128 inputs of 16 outputs with MX weights (lane: inputs 32 g + 0..31) and of 16 rows of 8 bits (lane: inputs
+// 16 g + 0..15 in x0, 64 + 16 g + 0..15 in x1; scale byte of inputs 32 g ..)
+__device__ inline f32x4 mfma_mx(u32x4 w, int ws, u32x4 x0, u32x4 x1, int xs, f32x4 c) {
+  const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  const i32x8 b = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, ws, 0, xs);
+}
+
 __device__ inline float activate(float x, int act) {
   if (act == PSISPEC_W4_SILU) return x / (1.0f + expf(-x));
   if (act == PSISPEC_W4_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
@@ -95,22 +115,41 @@ __device__ inline float activate(float x, int act) {
   return 0.5f * x * (1.0f + tanhf(u));
 }
 
+// The scales of the lane's outputs 4 g + 0..3, four numbers of 16 bits
+template <bool F16>
+__device__ inline f32x4 scales_of(u32x2 w) {
+  return f32x4{scale16(w[0] & 0xffffu, F16), scale16(w[0] >> 16, F16), scale16(w[1] & 0xffffu, F16),
+               scale16(w[1] >> 16, F16)};
+}
+
 __device__ inline float load16(const void* p, int64_t i, bool f16) {
   return scale16(static_cast<const uint16_t*>(p)[i], f16);
 }
-__device__ inline uint16_t round16(float v, bool f16) {
+__device__ inline uint32_t round16(float v, bool f16) {
   return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// bias and rounding of a linear layer, or activation and product of a gated one
+// Outputs n .. n + 3 of a row: bias and rounding of a linear layer, or activation and product of a gated one.
 template <int MATS>
-__device__ inline void store(const W4Args& a, int row, int n, float first, float second) {
-  float y;
-  if (MATS == 2)
-    y = activate(first, a.act) * second;
-  else
-    y = a.bias ? first + load16(a.bias, n, a.out_f16) : first;
-  static_cast<uint16_t*>(a.out)[(int64_t)row * a.out_stride + n] = round16(y, a.out_f16);
+__device__ inline void store4(const W4Args& a, int64_t row, int n, f32x4 first, f32x4 second) {
+  uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_stride + n;
+  uint32_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float v;
+    if (MATS == 2)
+      v = activate(first[e], a.act) * second[e];
+    else
+      v = a.bias && n + e < a.n ? first[e] + load16(a.bias, n + e, a.out_f16) : first[e];
+    y[e] = round16(v, a.out_f16);
+  }
+  if (a.out_vec && n + 4 <= a.n) {
+    *reinterpret_cast<u32x2*>(out) = u32x2{y[0] | y[1] << 16, y[2] | y[3] << 16};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.n) out[e] = (uint16_t)y[e];
+  }
 }
 
 }  // namespace w4

@@ -27,7 +27,8 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
   struct Slot {
     u32x4 w[NB];
     u32x4 x[MT][XL];
-    uint32_t s[NB][2];
+    uint32_t e[NB];  // MX: scale byte
+    u32x2 s[NB][kMx ? 1 : GPT];
     uint32_t xs[MT];
   };
   Slot slot[D];
@@ -53,18 +54,11 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
       const int64_t tile = (int64_t)min(nt0 + b % NT, a.ntiles - 1) * a.ktiles + t;
       q.w[b] = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(a.codes[b / NT] + tile * 1024 + lane * 16));
-      const uint8_t* sc = static_cast<const uint8_t*>(a.scales[b / NT]);
-      if constexpr (kMx) {
-        q.s[b][0] = sc[tile * 64 + lane];
-      } else if constexpr (GPT == 1) {
-        q.s[b][0] = reinterpret_cast<const uint16_t*>(sc)[tile * 16 + c];
-      } else if constexpr (GPT == 2) {
-        q.s[b][0] = reinterpret_cast<const uint32_t*>(sc)[tile * 16 + c];
-      } else {
-        const u32x2 v = reinterpret_cast<const u32x2*>(sc)[tile * 16 + c];
-        q.s[b][0] = v[0];
-        q.s[b][1] = v[1];
-      }
+      if constexpr (kMx)
+        q.e[b] = static_cast<const uint8_t*>(a.scales[b / NT])[tile * 64 + lane];
+#pragma unroll
+      for (int p = 0; p < GPT; ++p)
+        q.s[b][p] = static_cast<const u32x2*>(a.scales[b / NT])[(tile * GPT + p) * 4 + g];
     }
     const bool whole = (t + 1) * 128 <= a.k;
 #pragma unroll
@@ -88,6 +82,7 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[m][b] = f32x4{0, 0, 0, 0};
 
+  [[maybe_unused]] const IntBits bits = int_bits<X>();
   const auto compute = [&](const Slot& q) {
     if constexpr (kF8) {
 #pragma unroll
@@ -99,20 +94,20 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
                          __uint_as_float(q.xs[m] << 23));
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const u32x4 w = mx_codes(q.w[b][j], __uint_as_float(q.s[b][0] << 23), __bf16());
+          const u32x4 w = mx_codes(q.w[b][j], __uint_as_float(q.e[b] << 23), __bf16());
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[m][b] = mfma(x[m], w, acc[m][b], __bf16());
+          for (int m = 0; m < MT; ++m) acc[m][b] = mfma(w, x[m], acc[m][b], __bf16());
         }
       }
     } else if constexpr (kMx) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float s = mx_scale((int)q.s[b][0], top[b], X());
+        const float s = mx_scale((int)q.e[b], top[b], X());
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const u32x4 w = mx_codes(q.w[b][j], s, X());
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[m][b] = mfma(q.x[m][j], w, acc[m][b], X());
+          for (int m = 0; m < MT; ++m) acc[m][b] = mfma(w, q.x[m][j], acc[m][b], X());
         }
       }
     } else {
@@ -124,22 +119,22 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
         for (int m = 0; m < MT; ++m) {
           first[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < JG; ++j) first[m] = mfma(q.x[m][p * JG + j], minus24(X()), first[m], X());
+          for (int j = 0; j < JG; ++j) first[m] = mfma(minus24(X()), q.x[m][p * JG + j], first[m], X());
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float s = scale16(q.s[b][p >> 1] >> (16 * (p & 1)), a.scale_f16[b / NT]);
+          const f32x4 s = a.scale_f16 ? scales_of<true>(q.s[b][p]) : scales_of<false>(q.s[b][p]);
           f32x4 part[MT];
 #pragma unroll
           for (int j = 0; j < JG; ++j) {
-            const u32x4 w = int_codes(q.w[b][p * JG + j], X());
+            const u32x4 w = int_codes(q.w[b][p * JG + j], bits, X());
 #pragma unroll
-            for (int m = 0; m < MT; ++m) part[m] = mfma(q.x[m][p * JG + j], w, j ? part[m] : first[m], X());
+            for (int m = 0; m < MT; ++m) part[m] = mfma(w, q.x[m][p * JG + j], j ? part[m] : first[m], X());
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][b][i] = fmaf(part[m][i], s, acc[m][b][i]);
+            for (int i = 0; i < 4; ++i) acc[m][b][i] = fmaf(part[m][i], s[i], acc[m][b][i]);
         }
       }
     }
@@ -162,27 +157,21 @@ __global__ __launch_bounds__(64 * KW) void k_w4_few(W4Args a) {
     for (int b = 0; b < NB; ++b) s_acc[wave][m * NB + b][lane] = acc[m][b];
   __syncthreads();
   for (int o = wave; o < MT * NT; o += KW) {
-    const int m = o / NT, b = o - m * NT, n = (nt0 + b) * 16 + c;
+    const int m = o / NT, b = o - m * NT, n = (nt0 + b) * 16 + 4 * g, row = m0 + 16 * m + c;
     f32x4 y[MATS];
 #pragma unroll
     for (int q = 0; q < MATS; ++q) {
       y[q] = s_acc[0][m * NB + q * NT + b][lane];
       for (int w = 1; w < KW; ++w) y[q] += s_acc[w][m * NB + q * NT + b][lane];
     }
-    if (n >= a.n) continue;
+    if (n >= a.n || row >= a.rows) continue;
     if constexpr (kMx && __is_same(X, _Float16)) {
 #pragma unroll
-      for (int q = 0; q < MATS; ++q) {
-        const int e = a.top[q][n];
+      for (int q = 0; q < MATS; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[q][i] = mx_back(y[q][i], e, X());
-      }
+        for (int i = 0; i < 4; ++i) y[q][i] = mx_back(y[q][i], a.top[q][n + i], X());
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = m0 + 16 * m + 4 * g + i;
-      if (row < a.rows) store<MATS>(a, row, n, y[0][i], MATS == 2 ? y[MATS - 1][i] : 0.0f);
-    }
+    store4<MATS>(a, row, n, y[0], y[MATS - 1]);
   }
 }
 

@@ -1,0 +1,363 @@
+// w4_many.h -- the 4-bit products of many rows.
+//
+// A workgroup of four waves owns 128 rows x 128 outputs (of a gated call 64 outputs of either matrix), a
+// wave 64 x 64 of them.  The rows go through LDS, 256 bytes of each per step, two steps deep, by loads that
+// write LDS themselves; slot s of row r holds the row's 16-byte chunk s ^ (r % 16), so that the reads of 16
+// rows at one chunk fall on all banks.  The weights come straight from memory in the order of the matrix
+// instructions, one step ahead, and are decoded once per 64 rows.  What INT products start from,
+// -24 sum(x) per row and group, is formed by one pass over the rows before (k_w4_sums) and travels with
+// them: formed by the matrix cores here it would be a fifth of their work.  Few tiles: the inputs are cut
+// into parts whose sums are joined in their order by k_w4_join.
+#pragma once
+
+#include "w4.h"
+
+namespace psispec {
+namespace w4 {
+
+constexpr int kBM = 128, kStageRow = 256;  // rows of a workgroup; bytes of a row per step
+constexpr int kRsrc3 = 0x00020000;         // raw buffer: out of range reads give 0
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) uint32_t global_u32;
+
+// An LDS read.  The restrict-qualified parameter of an inlined function gives it an alias scope of its own, so
+// that the compiler does not wait before it for every load to LDS in flight: the kernel orders those and the
+// reads itself, by a wait and a barrier per step.
+template <typename V>
+__device__ __attribute__((always_inline)) inline V lds_read(const V* __restrict__ p) {
+  return *p;
+}
+
+struct ManyArgs {
+  W4Args a;
+  float* sums;  // INT: [tile of inputs][group][rows up to a multiple of 128]
+  float* part;  // cut inputs: [part][matrix][row][output, up to a multiple of 16]
+  int mpad, npad, mblocks, nblocks, parts, steps;  // steps of a part
+};
+
+// -24 sum(x) over each group of each row; a wave per row and tile of 128 inputs
+template <typename X>
+__global__ __launch_bounds__(256) void k_w4_sums(ManyArgs m) {
+  const W4Args& a = m.a;
+  const int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // 16 lanes per item, 8 inputs each
+  const int t = (int)(item / m.mpad), row = (int)(item - (int64_t)t * m.mpad);
+  if (t >= a.ktiles) return;
+  const int c = threadIdx.x & 15, k = t * 128 + 8 * c;
+  float s = 0.0f;
+  if (row < a.rows && k < a.k) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + (int64_t)row * a.x_stride + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s += scale16(v[i] & 0xffffu, __is_same(X, _Float16)) + scale16(v[i] >> 16, __is_same(X, _Float16));
+  }
+  const int per = 16 / a.gpt;  // lanes of a group
+  for (int o = 1; o < per; o <<= 1) s += __shfl_xor(s, o, 64);
+  if (c % per == 0) m.sums[((int64_t)t * a.gpt + c / per) * m.mpad + row] = -24.0f * s;
+}
+
+// The parts' sums in their order, then what a product ends with; a thread per four outputs.
+template <int MATS>
+__global__ __launch_bounds__(256) void k_w4_join(ManyArgs m) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, plane = (int64_t)m.a.rows * m.npad;
+  if (4 * i >= plane) return;
+  const int64_t row = 4 * i / m.npad;
+  const int n = (int)(4 * i - row * m.npad);
+  if (n >= m.a.n) return;
+  f32x4 y[MATS];
+#pragma unroll
+  for (int q = 0; q < MATS; ++q) {
+    y[q] = *reinterpret_cast<const f32x4*>(m.part + q * plane + 4 * i);
+    for (int p = 1; p < m.parts; ++p)
+      y[q] += *reinterpret_cast<const f32x4*>(m.part + ((int64_t)p * MATS + q) * plane + 4 * i);
+  }
+  store4<MATS>(m.a, row, n, y[0], y[MATS - 1]);
+}
+
+// X: __bf16, _Float16 or F8; GPT: INT groups per tile, 0: MX; SF16: scales in F16
+template <typename X, int GPT, int MATS, bool SF16>
+__global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
+  constexpr bool kMx = GPT == 0, kF8 = __is_same(X, F8);
+  constexpr int MT = 4, NB = 4, NT = NB / MATS;
+  constexpr int TPS = kF8 ? 2 : 1;  // tiles of 128 inputs per step
+  // One array: rows, then (INT) -24 sum(x) [group][128 rows], then the scales of each wave's tiles [tile][group][16
+  // outputs].  With several arrays the compiler gives each an alias scope and waits for their loads again.
+  constexpr int kSumAt = kBM * kStageRow, kScAt = kSumAt + (kMx ? 0 : GPT < 2 ? 1024 : GPT * kBM * 4);
+  constexpr int kScWave = kMx ? 0 : GPT < 2 ? 256 : GPT * 128, kStage = kScAt + 4 * kScWave;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_x[2][kStage];
+  const W4Args& a = m.a;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave >> 1, wn = wave & 1;
+
+  // Neighbouring workgroups go to the eight XCDs in turn: each XCD gets a run of columns, whose weights it
+  // reads alone, and within it the row blocks of a column one after the other.
+  const unsigned total = (unsigned)m.mblocks * m.nblocks * m.parts, per = total / 8, rest = total % 8;
+  const unsigned xcd = blockIdx.x & 7, in = blockIdx.x >> 3;
+  const unsigned id = xcd * per + (xcd < rest ? xcd : rest) + in;
+  const int mb = (int)(id % m.mblocks), nb = (int)(id / m.mblocks % m.nblocks), part = (int)(id / m.mblocks / m.nblocks);
+  const int m0 = mb * kBM;
+  const int nt0 = (nb * 2 + wn) * NT;
+  const int step0 = part * m.steps, step1 = min(step0 + m.steps, (a.ktiles + TPS - 1) / TPS);
+
+  // rows into LDS: load i of a wave fills rows 32 wave + 4 i .. + 3
+  const int rowbytes = a.k * (kF8 ? 1 : 2);
+  const int rows = min(kBM, a.rows - m0);
+  const int64_t stride = a.x_stride * (kF8 ? 1 : 2);
+  const uint8_t* xbase = static_cast<const uint8_t*>(a.x) + (int64_t)m0 * stride;
+  const int extent = (int)((rows - 1) * stride) + rowbytes;
+  int off[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 32 * wave + 4 * i + (lane >> 4);
+    off[i] = (int)(min(r, rows - 1) * stride) + 16 * ((lane & 15) ^ (r & 15));
+  }
+  // word `lane` of load i of a tile's scales: pairs of outputs, 8 GPT words a tile (with one group the upper half
+  // of the lanes repeats the lower)
+  const uint32_t* sc_at[kMx ? 1 : (GPT + 1) / 2];
+  if constexpr (!kMx) {
+#pragma unroll
+    for (int i = 0; i < (GPT + 1) / 2; ++i) {
+      const int word = (64 * i + lane) % (NB * 8 * GPT), b = word / (8 * GPT);
+      const int64_t tile = (int64_t)min(nt0 + b % NT, a.ntiles - 1) * a.ktiles;
+      sc_at[i] = static_cast<const uint32_t*>(b / NT ? a.scales[1] : a.scales[0]) + tile * (8 * GPT) + word % (8 * GPT);
+    }
+  }
+  const auto load_x = [&](int st, int buf) {
+    const int at = st * kStageRow;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(xbase + at), (short)0, extent - at, kRsrc3);
+    const bool whole = at + kStageRow <= rowbytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int o = off[i];
+      if (!whole) {
+        const int rr = 32 * wave + 4 * i + (lane >> 4);
+        if (at + 16 * ((lane & 15) ^ (rr & 15)) >= rowbytes) o = 0x7ffffff0;  // behind the row: zeros
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(s_x[buf] + (32 * wave + 4 * i) * kStageRow), 16, o, 0, 0, 0);
+    }
+    if constexpr (!kMx) {
+      // 128 rows of each group: 512 bytes, two groups a load
+      if (wave < (GPT + 1) / 2) {
+        const __amdgpu_buffer_rsrc_t q = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(m.sums + (int64_t)st * GPT * m.mpad + m0), (short)0, (GPT - 1) * m.mpad * 4 + 512, kRsrc3);
+        const int grp = 2 * wave + (lane >> 5);
+        const int o = grp < GPT ? grp * m.mpad * 4 + 16 * (lane & 31) : 0x7ffffff0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (lds_void*)(s_x[buf] + kSumAt + 1024 * wave), 16, o, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < (GPT + 1) / 2; ++i)
+        __builtin_amdgcn_global_load_lds((const global_u32*)(sc_at[i] + (int64_t)st * (8 * GPT)),
+                                         (lds_void*)(s_x[buf] + kScAt + wave * kScWave + 256 * i), 4, 0, 0);
+    }
+  };
+
+  struct Codes {
+    u32x4 w[TPS][NB];
+    uint32_t e[TPS][NB];  // MX: scale byte
+    uint32_t xs[TPS][MT];
+  };
+  const uint8_t* xsrow[MT];
+  int top[NB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    xsrow[i] = kF8 ? a.x_scale + (int64_t)min(m0 + 64 * wm + 16 * i + c, a.rows - 1) * a.xs_stride : nullptr;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    top[b] = kMx && __is_same(X, _Float16) ? a.top[b / NT][min(nt0 + b % NT, a.ntiles - 1) * 16 + c] : 0;
+  const auto load_w = [&](Codes& q, int st) {
+#pragma unroll
+    for (int h = 0; h < TPS; ++h) {
+      const int t = st * TPS + h;
+      if (TPS > 1 && t >= a.ktiles) continue;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int64_t tile = (int64_t)min(nt0 + b % NT, a.ntiles - 1) * a.ktiles + t;
+        q.w[h][b] = *reinterpret_cast<const u32x4*>(a.codes[b / NT] + tile * 1024 + lane * 16);
+        if constexpr (kMx)
+          q.e[h][b] = static_cast<const uint8_t*>(a.scales[b / NT])[tile * 64 + lane];
+      }
+      if constexpr (kF8) {
+        const int blk = 4 * t + g;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) q.xs[h][i] = blk * 32 < a.k ? xsrow[i][blk] : 127;
+      }
+    }
+  };
+
+  f32x4 acc[MT][NB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[i][b] = f32x4{0, 0, 0, 0};
+
+  // the wave's row 16 i + c at chunk `ch`
+  const auto read_x = [&](int buf, int i, int ch) {
+    return lds_read(reinterpret_cast<const u32x4*>(s_x[buf] + (64 * wm + 16 * i + c) * kStageRow + 16 * (ch ^ c)));
+  };
+  [[maybe_unused]] const IntBits bits = int_bits<X>();
+  const auto compute = [&](const Codes& q, int buf, int st) {
+    if constexpr (kF8) {
+#pragma unroll
+      for (int h = 0; h < TPS; ++h) {
+        if (st * TPS + h >= a.ktiles) break;
+        u32x4 lo[MT], hi[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          lo[i] = read_x(buf, i, 8 * h + g);
+          hi[i] = read_x(buf, i, 8 * h + 4 + g);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i][b] = mfma_mx(q.w[h][b], (int)q.e[h][b], lo[i], hi[i], (int)q.xs[h][i], acc[i][b]);
+      }
+    } else if constexpr (kMx) {
+      float s[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) s[b] = mx_scale((int)q.e[0][b], top[b], X());
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 x[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[i] = read_x(buf, i, 4 * g + j);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const u32x4 w = mx_codes(q.w[0][b][j], s[b], X());
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[i][b] = mfma(w, x[i], acc[i][b], X());
+        }
+      }
+    } else {
+      // A group's products with one tile of outputs, then, under the next ones, its sums times the scales: the
+      // barriers keep the compiler from starting every group's products first (it would spill 200 registers).
+      constexpr int JG = 4 / GPT;
+      f32x4 sum[2][MT], s[2];
+      const auto scale_in = [&](int at, int b) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][b][e] = fmaf(sum[at][i][e], s[at][e], acc[i][b][e]);
+      };
+#pragma unroll
+      for (int p = 0; p < GPT; ++p) {
+        u32x4 x[JG][MT];
+        f32x4 first[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const float f = lds_read(reinterpret_cast<const float*>(s_x[buf] + kSumAt) + p * kBM + 64 * wm + 16 * i + c);
+          first[i] = f32x4{f, f, f, f};
+#pragma unroll
+          for (int j = 0; j < JG; ++j) x[j][i] = read_x(buf, i, 4 * (p * JG + j) + g);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int at = (p * NB + b) & 1;
+          s[at] = scales_of<SF16>(lds_read(reinterpret_cast<const u32x2*>(
+              s_x[buf] + kScAt + wave * kScWave + ((b * GPT + p) * 16 + 4 * g) * 2)));
+#pragma unroll
+          for (int j = 0; j < JG; ++j) {
+            const u32x4 w = int_codes(q.w[0][b][p * JG + j], bits, X());
+#pragma unroll
+            for (int i = 0; i < MT; ++i) sum[at][i] = mfma(w, x[j][i], j ? sum[at][i] : first[i], X());
+          }
+          if (p + b > 0) scale_in(at ^ 1, (b + NB - 1) % NB);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      scale_in((GPT * NB - 1) & 1, NB - 1);
+    }
+  };
+
+  // One barrier per step: past it the step's rows have landed for every wave (each waited for its own loads)
+  // and every wave is done with the step before, whose buffer the next loads overwrite.
+  Codes q, next;
+  load_x(step0, 0);
+  load_w(q, step0);
+  for (int st = step0, buf = 0; st < step1; ++st, buf ^= 1) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __syncthreads();
+    if (st + 1 < step1) {
+      load_x(st + 1, buf ^ 1);
+      load_w(next, st + 1);
+    }
+    compute(q, buf, st);
+    q = next;
+  }
+
+#pragma unroll
+  for (int b = 0; b < NT; ++b) {
+    const int n = (nt0 + b) * 16 + 4 * g;
+    if (n >= a.n) continue;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int row = m0 + 64 * wm + 16 * i + c;
+      if (row >= a.rows) continue;
+      f32x4 y[MATS];
+#pragma unroll
+      for (int z = 0; z < MATS; ++z) {
+        y[z] = acc[i][z * NT + b];
+        if constexpr (kMx && __is_same(X, _Float16)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[z][e] = mx_back(y[z][e], a.top[z][n + e], X());
+        }
+      }
+      if (m.parts > 1) {
+#pragma unroll
+        for (int z = 0; z < MATS; ++z)
+          *reinterpret_cast<f32x4*>(m.part + (((int64_t)part * MATS + z) * a.rows + row) * m.npad + n) = y[z];
+      } else {
+        store4<MATS>(a, row, n, y[0], y[MATS - 1]);
+      }
+    }
+  }
+}
+
+// How the work is cut, from the sizes alone
+struct ManyPlan {
+  int mblocks, nblocks, parts, steps, mpad, npad;
+  size_t part_at, bytes;
+};
+inline ManyPlan many_plan(int rows, int n, int k, int mats, int tiles_per_step) {
+  ManyPlan p{};
+  p.mblocks = (rows + kBM - 1) / kBM;
+  p.nblocks = (n + 128 / mats - 1) / (128 / mats);
+  p.mpad = p.mblocks * kBM;
+  p.npad = (n + 15) / 16 * 16;
+  const int ktiles = (k + 127) / 128, all = (ktiles + tiles_per_step - 1) / tiles_per_step;
+  const int64_t blocks = (int64_t)p.mblocks * p.nblocks;
+  int parts = blocks >= 256 ? 1 : (int)(512 / blocks);
+  if (parts > all / 4) parts = all / 4 > 1 ? all / 4 : 1;
+  p.steps = (all + parts - 1) / parts;
+  p.parts = (all + p.steps - 1) / p.steps;
+  p.part_at = ((size_t)ktiles * 4 * p.mpad * 4 + 255) / 256 * 256;
+  p.bytes = p.part_at + (p.parts > 1 ? (size_t)p.parts * mats * rows * p.npad * 4 : 0);
+  return p;
+}
+
+template <typename X, int GPT, int MATS>
+hipError_t launch_many(const W4Args& a, hipStream_t stream) {
+  constexpr bool kF8 = __is_same(X, F8);
+  const ManyPlan p = many_plan(a.rows, a.n, a.k, MATS, kF8 ? 2 : 1);
+  ManyArgs m{a, static_cast<float*>(a.workspace), nullptr, p.mpad, p.npad, p.mblocks, p.nblocks, p.parts, p.steps};
+  m.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + p.part_at);
+  if constexpr (!kF8 && GPT > 0) {
+    const int64_t items = (int64_t)p.mpad * a.ktiles;
+    PSISPEC_LAUNCH("w4_sums", (k_w4_sums<X>), dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, m);
+  }
+  const dim3 grid((unsigned)p.mblocks * p.nblocks * p.parts);
+  if (GPT > 0 && a.scale_f16)
+    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", (k_w4_many<X, GPT, MATS, GPT != 0>), grid, dim3(256), 0, stream,
+                   m);
+  else
+    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", (k_w4_many<X, GPT, MATS, false>), grid, dim3(256), 0, stream,
+                   m);
+  if (p.parts > 1) {
+    const int64_t all = (int64_t)a.rows * p.npad / 4;
+    PSISPEC_LAUNCH("w4_join", k_w4_join<MATS>, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, stream, m);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace w4
+}  // namespace psispec

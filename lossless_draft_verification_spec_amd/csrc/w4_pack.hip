@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4PackArgs a, W4Layout l) {
   } else if (g < l.gpt) {
     const uint16_t* sc = static_cast<const uint16_t*>(a.scales) + (int64_t)n * a.scales_stride;
     const int k = t * 128 + g * (128 / l.gpt);
-    reinterpret_cast<uint16_t*>(a.packed + l.scales_at)[(tile * 16 + (lane & 15)) * l.gpt + g] =
+    reinterpret_cast<uint16_t*>(a.packed + l.scales_at)[(tile * l.gpt + g) * 16 + (lane & 15)] =
         in && k < a.k ? sc[k / a.group] : 0;
   }
 }
