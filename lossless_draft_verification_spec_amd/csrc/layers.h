@@ -27,7 +27,7 @@ hipError_t launch_add_rmsnorm(const AddNormArgs& a, psispec_dtype dtype, hipStre
 //   PSISPEC_W4_MX   32 g + 8 j + 0..7: nibble s = input s, the code as it is
 // so word j is the lane's part of the j-th 16x16x32 matrix instruction of the tile (and the 16 bytes,
 // for MX, its part of the 16x16x128 one).  Scales: INT [tile][groups per tile][16 outputs] in 16 bits,
-// MX [tile][64 lanes] a byte.  top (MX): the largest scale byte of each output.
+// MX [tile of outputs][pair of tiles of inputs][64 lanes][2] a byte.  top (MX): the largest scale byte of each output.
 struct W4Layout {
   int ntiles, ktiles, gpt;  // tiles of outputs, of inputs; groups per tile (INT; larger groups repeat)
   size_t scales_at, top_at, bytes;
@@ -39,9 +39,15 @@ inline W4Layout w4_layout(int n, int k, int group, int format) {
   l.gpt = group < 128 ? 128 / group : 1;
   const size_t tiles = (size_t)l.ntiles * l.ktiles;
   l.scales_at = tiles * 1024;
-  l.top_at = l.scales_at + tiles * (format == PSISPEC_W4_MX ? 64 : (size_t)32 * l.gpt);
+  l.top_at = l.scales_at + (format == PSISPEC_W4_MX ? (size_t)l.ntiles * ((l.ktiles + 1) / 2) * 128
+                                                    : tiles * 32 * l.gpt);
   l.bytes = (l.top_at + (format == PSISPEC_W4_MX ? (size_t)l.ntiles * 16 : 0) + 255) / 256 * 256;
   return l;
+}
+
+// where the MX scale of lane 0 lies: tile t of the inputs of tile nt of the outputs; lane l's is 2 l further
+__host__ __device__ inline int64_t mx_scale_at(int64_t nt, int t, int ktiles) {
+  return (nt * ((ktiles + 1) / 2) + t / 2) * 128 + (t & 1);
 }
 
 struct W4PackArgs {

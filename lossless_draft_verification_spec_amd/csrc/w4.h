@@ -26,8 +26,25 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef uint64_t u64_any __attribute__((aligned(1)));
 
 struct F8 {};  // rows of e4m3 with a power of two per 32 inputs
+
+constexpr int kStageRow = 256;      // bytes of a row per step
+constexpr int kRsrc3 = 0x00020000;  // raw buffer: reads out of range give 0
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) uint32_t global_u32;
+
+// s_waitcnt: at most n loads in flight, the other counters as they are
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+// An LDS read.  The restrict-qualified parameter of an inlined function gives it an alias scope of its own, so
+// that the compiler does not wait before it for every load to LDS in flight: the kernels order those and the
+// reads themselves.
+template <typename V>
+__device__ __attribute__((always_inline)) inline V lds_read(const V* __restrict__ p) {
+  return *p;
+}
 
 __device__ inline f32x4 mfma(u32x4 w, u32x4 x, f32x4 c, __bf16) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
@@ -100,12 +117,23 @@ __device__ inline u32x4 f8_rows(uint32_t lo, uint32_t hi, float scale) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
 }
 
+// The scales of the eight blocks from `blk` on of a row of 8-bit numbers; those behind the last of `all` are 1
+// (their values are read as zeros)
+__device__ inline uint64_t row_scales(const uint8_t* row, int blk, int all) {
+  if (blk + 8 <= all) return *reinterpret_cast<const u64_any*>(row + blk);
+  uint64_t v = 0x7f7f7f7f7f7f7f7full;
+  for (int i = 0; i < all - blk; ++i) v = (v & ~(0xffull << (8 * i))) | (uint64_t)row[blk + i] << (8 * i);
+  return v;
+}
+
 // 128 inputs of 16 outputs with MX weights (lane: inputs 32 g + 0..31) and of 16 rows of 8 bits (lane: inputs
-// 16 g + 0..15 in x0, 64 + 16 g + 0..15 in x1; scale byte of inputs 32 g ..)
+// 16 g + 0..15 in x0, 64 + 16 g + 0..15 in x1; byte 0 of xs the scale of inputs 32 g ..),
+// byte WS of ws that of the output
+template <int WS>
 __device__ inline f32x4 mfma_mx(u32x4 w, int ws, u32x4 x0, u32x4 x1, int xs, f32x4 c) {
   const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
   const i32x8 b = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, ws, 0, xs);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, WS, ws, 0, xs);
 }
 
 __device__ inline float activate(float x, int act) {

@@ -1,13 +1,12 @@
 // w4_many.h -- the 4-bit products of many rows.
 //
-// A workgroup of four waves owns 128 rows x 128 outputs (of a gated call 64 outputs of either matrix), a
-// wave 64 x 64 of them.  The rows go through LDS, 256 bytes of each per step, two steps deep, by loads that
-// write LDS themselves; slot s of row r holds the row's 16-byte chunk s ^ (r % 16), so that the reads of 16
-// rows at one chunk fall on all banks.  The weights come straight from memory in the order of the matrix
-// instructions, one step ahead, and are decoded once per 64 rows.  What INT products start from,
-// -24 sum(x) per row and group, is formed by one pass over the rows before (k_w4_sums) and travels with
-// them: formed by the matrix cores here it would be a fifth of their work.  Few tiles: the inputs are cut
-// into parts whose sums are joined in their order by k_w4_join.
+// A workgroup of four waves owns 64 rows x 64 NB outputs of all matrices, a wave 64 rows x 16 NB outputs.  The
+// rows go through LDS, 256 bytes of each per step, by loads that write LDS themselves; slot s of row r holds the
+// row's 16-byte chunk s ^ (r % 16), so that the reads of 16 rows at one chunk fall on all banks.  The weights come
+// straight from memory in the order of the matrix instructions and are decoded once per 64 rows.  What INT
+// products start from, -24 sum(x) per row and group, is formed by one pass over the rows before (k_w4_sums) and
+// travels with them: formed by the matrix cores here it would be a fifth of their work.  Loads run one step
+// ahead (two or three steps ahead, and 128 rows per workgroup, were no faster).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
 #pragma once
 
 #include "w4.h"
@@ -15,22 +14,11 @@
 namespace psispec {
 namespace w4 {
 
-constexpr int kBM = 128, kStageRow = 256;  // rows of a workgroup; bytes of a row per step
-constexpr int kRsrc3 = 0x00020000;         // raw buffer: out of range reads give 0
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) uint32_t global_u32;
-
-// An LDS read.  The restrict-qualified parameter of an inlined function gives it an alias scope of its own, so
-// that the compiler does not wait before it for every load to LDS in flight: the kernel orders those and the
-// reads itself, by a wait and a barrier per step.
-template <typename V>
-__device__ __attribute__((always_inline)) inline V lds_read(const V* __restrict__ p) {
-  return *p;
-}
+constexpr int kBM = 64;  // rows of a workgroup
 
 struct ManyArgs {
   W4Args a;
-  float* sums;  // INT: [tile of inputs][group][rows up to a multiple of 128]
+  float* sums;  // INT: [tile of inputs][group][rows up to a multiple of 64]
   float* part;  // cut inputs: [part][matrix][row][output, up to a multiple of 16]
   int mpad, npad, mblocks, nblocks, parts, steps;  // steps of a part
 };
@@ -74,20 +62,21 @@ __global__ __launch_bounds__(256) void k_w4_join(ManyArgs m) {
 }
 
 // X: __bf16, _Float16 or F8; GPT: INT groups per tile, 0: MX; SF16: scales in F16
-template <typename X, int GPT, int MATS, bool SF16>
+// NB: tiles of 16 outputs of a wave, of all matrices
+template <typename X, int GPT, int MATS, bool SF16, int NB>
 __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
   constexpr bool kMx = GPT == 0, kF8 = __is_same(X, F8);
-  constexpr int MT = 4, NB = 4, NT = NB / MATS;
+  constexpr int MT = kBM / 16, NT = NB / MATS, kLoads = kBM / 16;
   constexpr int TPS = kF8 ? 2 : 1;  // tiles of 128 inputs per step
-  // One array: rows, then (INT) -24 sum(x) [group][128 rows], then the scales of each wave's tiles [tile][group][16
+  // One array: rows, then (INT) -24 sum(x) [group][row], then the scales of each wave's tiles [tile][group][16
   // outputs].  With several arrays the compiler gives each an alias scope and waits for their loads again.
-  constexpr int kSumAt = kBM * kStageRow, kScAt = kSumAt + (kMx ? 0 : GPT < 2 ? 1024 : GPT * kBM * 4);
-  constexpr int kScWave = kMx ? 0 : GPT < 2 ? 256 : GPT * 128, kStage = kScAt + 4 * kScWave;
+  constexpr int kSumAt = kBM * kStageRow, kScAt = kSumAt + (kF8 ? 4 * 512 : kMx ? 0 : GPT * kBM * 4);
+  constexpr int kScLoads = (NB * 8 * GPT + 63) / 64;  // words of a wave's scales over 64
+  constexpr int kScWave = kMx ? 0 : kScLoads * 256, kStage = kScAt + 4 * kScWave;
   __shared__ __attribute__((aligned(1024))) uint8_t s_x[2][kStage];
   const W4Args& a = m.a;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wm = wave >> 1, wn = wave & 1;
 
   // Neighbouring workgroups go to the eight XCDs in turn: each XCD gets a run of columns, whose weights it
   // reads alone, and within it the row blocks of a column one after the other.
@@ -96,27 +85,27 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
   const unsigned id = xcd * per + (xcd < rest ? xcd : rest) + in;
   const int mb = (int)(id % m.mblocks), nb = (int)(id / m.mblocks % m.nblocks), part = (int)(id / m.mblocks / m.nblocks);
   const int m0 = mb * kBM;
-  const int nt0 = (nb * 2 + wn) * NT;
+  const int nt0 = (nb * 4 + wave) * NT;
   const int step0 = part * m.steps, step1 = min(step0 + m.steps, (a.ktiles + TPS - 1) / TPS);
 
-  // rows into LDS: load i of a wave fills rows 32 wave + 4 i .. + 3
+  // rows into LDS: load i of a wave fills four rows from 4 (kLoads wave + i) on
   const int rowbytes = a.k * (kF8 ? 1 : 2);
   const int rows = min(kBM, a.rows - m0);
   const int64_t stride = a.x_stride * (kF8 ? 1 : 2);
   const uint8_t* xbase = static_cast<const uint8_t*>(a.x) + (int64_t)m0 * stride;
   const int extent = (int)((rows - 1) * stride) + rowbytes;
-  int off[8];
+  int off[kLoads];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 32 * wave + 4 * i + (lane >> 4);
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 4 * (kLoads * wave + i) + (lane >> 4);
     off[i] = (int)(min(r, rows - 1) * stride) + 16 * ((lane & 15) ^ (r & 15));
   }
-  // word `lane` of load i of a tile's scales: pairs of outputs, 8 GPT words a tile (with one group the upper half
-  // of the lanes repeats the lower)
-  const uint32_t* sc_at[kMx ? 1 : (GPT + 1) / 2];
+  // word `lane` of load i of a tile's scales: pairs of outputs, 8 GPT words a tile (lanes behind the
+  // last repeat the first)
+  const uint32_t* sc_at[kMx ? 1 : kScLoads];
   if constexpr (!kMx) {
 #pragma unroll
-    for (int i = 0; i < (GPT + 1) / 2; ++i) {
+    for (int i = 0; i < kScLoads; ++i) {
       const int word = (64 * i + lane) % (NB * 8 * GPT), b = word / (8 * GPT);
       const int64_t tile = (int64_t)min(nt0 + b % NT, a.ntiles - 1) * a.ktiles;
       sc_at[i] = static_cast<const uint32_t*>(b / NT ? a.scales[1] : a.scales[0]) + tile * (8 * GPT) + word % (8 * GPT);
@@ -127,60 +116,52 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(xbase + at), (short)0, extent - at, kRsrc3);
     const bool whole = at + kStageRow <= rowbytes;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int o = off[i];
-      if (!whole) {
-        const int rr = 32 * wave + 4 * i + (lane >> 4);
-        if (at + 16 * ((lane & 15) ^ (rr & 15)) >= rowbytes) o = 0x7ffffff0;  // behind the row: zeros
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(s_x[buf] + (32 * wave + 4 * i) * kStageRow), 16, o, 0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) {
+      const int rr = 4 * (kLoads * wave + i) + (lane >> 4);
+      const int o = whole || at + 16 * ((lane & 15) ^ (rr & 15)) < rowbytes ? off[i] : 0x7ffffff0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(s_x[buf] + 4 * (kLoads * wave + i) * kStageRow), 16, (int)o, 0, 0,
+                                               0);
     }
     if constexpr (!kMx) {
-      // 128 rows of each group: 512 bytes, two groups a load
-      if (wave < (GPT + 1) / 2) {
-        const __amdgpu_buffer_rsrc_t q = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(m.sums + (int64_t)st * GPT * m.mpad + m0), (short)0, (GPT - 1) * m.mpad * 4 + 512, kRsrc3);
-        const int grp = 2 * wave + (lane >> 5);
-        const int o = grp < GPT ? grp * m.mpad * 4 + 16 * (lane & 31) : 0x7ffffff0;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (lds_void*)(s_x[buf] + kSumAt + 1024 * wave), 16, o, 0, 0, 0);
-      }
+      // its 64 rows of a group each wave (with fewer groups than waves some load the same)
+      const int grp = wave % GPT;
+      __builtin_amdgcn_global_load_lds(
+          (const global_u32*)(m.sums + ((int64_t)st * GPT + grp) * m.mpad + m0 + lane),
+          (lds_void*)(s_x[buf] + kSumAt + 4 * kBM * grp), 4, 0, 0);
 #pragma unroll
-      for (int i = 0; i < (GPT + 1) / 2; ++i)
+      for (int i = 0; i < kScLoads; ++i)
         __builtin_amdgcn_global_load_lds((const global_u32*)(sc_at[i] + (int64_t)st * (8 * GPT)),
                                          (lds_void*)(s_x[buf] + kScAt + wave * kScWave + 256 * i), 4, 0, 0);
     }
   };
 
   struct Codes {
+    uint64_t xs;  // 8-bit rows: scales of row `lane`
     u32x4 w[TPS][NB];
-    uint32_t e[TPS][NB];  // MX: scale byte
-    uint32_t xs[TPS][MT];
+    uint32_t e[NB];  // MX: scale byte (8-bit rows: those of both tiles)
   };
-  const uint8_t* xsrow[MT];
+  const uint8_t* xsrow = kF8 ? a.x_scale + (int64_t)min(m0 + lane, a.rows - 1) * a.xs_stride : nullptr;
   int top[NB];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xsrow[i] = kF8 ? a.x_scale + (int64_t)min(m0 + 64 * wm + 16 * i + c, a.rows - 1) * a.xs_stride : nullptr;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
     top[b] = kMx && __is_same(X, _Float16) ? a.top[b / NT][min(nt0 + b % NT, a.ntiles - 1) * 16 + c] : 0;
   const auto load_w = [&](Codes& q, int st) {
 #pragma unroll
     for (int h = 0; h < TPS; ++h) {
-      const int t = st * TPS + h;
-      if (TPS > 1 && t >= a.ktiles) continue;
+      const int t = min(st * TPS + h, a.ktiles - 1);  // behind the last: rows of zeros, any weights will do
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int64_t tile = (int64_t)min(nt0 + b % NT, a.ntiles - 1) * a.ktiles + t;
+        const int nt = min(nt0 + b % NT, a.ntiles - 1);
+        const int64_t tile = (int64_t)nt * a.ktiles + t;
         q.w[h][b] = *reinterpret_cast<const u32x4*>(a.codes[b / NT] + tile * 1024 + lane * 16);
-        if constexpr (kMx)
-          q.e[h][b] = static_cast<const uint8_t*>(a.scales[b / NT])[tile * 64 + lane];
+        if (kMx && h == 0) {
+          const uint8_t* e = static_cast<const uint8_t*>(a.scales[b / NT]) + mx_scale_at(nt, t, a.ktiles);
+          q.e[b] = kF8 ? reinterpret_cast<const uint16_t*>(e)[lane] : e[2 * lane];
+        }
       }
-      if constexpr (kF8) {
-        const int blk = 4 * t + g;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) q.xs[h][i] = blk * 32 < a.k ? xsrow[i][blk] : 127;
-      }
+    }
+    if constexpr (kF8) {
+      q.xs = row_scales(xsrow, 8 * st, a.k / 32);  // lane = row: a load per row and step, not per operand
     }
   };
 
@@ -192,14 +173,24 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
 
   // the wave's row 16 i + c at chunk `ch`
   const auto read_x = [&](int buf, int i, int ch) {
-    return lds_read(reinterpret_cast<const u32x4*>(s_x[buf] + (64 * wm + 16 * i + c) * kStageRow + 16 * (ch ^ c)));
+    return lds_read(reinterpret_cast<const u32x4*>(s_x[buf] + (16 * i + c) * kStageRow + 16 * (ch ^ c)));
   };
   [[maybe_unused]] const IntBits bits = int_bits<X>();
-  const auto compute = [&](const Codes& q, int buf, int st) {
+  const auto compute = [&](const Codes& q, int buf) {
     if constexpr (kF8) {
+      // each wave turns the rows' scales for itself: lane (row c of a tile, g) takes byte g of either half
+      uint64_t* const mine = reinterpret_cast<uint64_t*>(s_x[buf] + kSumAt + wave * 512);
+      mine[lane] = q.xs;
+      wave_sync();
+      uint32_t xs[2][MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const u32x2 v = lds_read(reinterpret_cast<const u32x2*>(mine + 16 * i + c));
+        xs[0][i] = v[0] >> (8 * g);
+        xs[1][i] = v[1] >> (8 * g);
+      }
 #pragma unroll
       for (int h = 0; h < TPS; ++h) {
-        if (st * TPS + h >= a.ktiles) break;
         u32x4 lo[MT], hi[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -210,12 +201,13 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            acc[i][b] = mfma_mx(q.w[h][b], (int)q.e[h][b], lo[i], hi[i], (int)q.xs[h][i], acc[i][b]);
+            acc[i][b] = h == 0 ? mfma_mx<0>(q.w[h][b], (int)q.e[b], lo[i], hi[i], (int)xs[h][i], acc[i][b])
+                               : mfma_mx<1>(q.w[h][b], (int)q.e[b], lo[i], hi[i], (int)xs[h][i], acc[i][b]);
       }
     } else if constexpr (kMx) {
       float s[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) s[b] = mx_scale((int)q.e[0][b], top[b], X());
+      for (int b = 0; b < NB; ++b) s[b] = mx_scale((int)q.e[b], top[b], X());
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         u32x4 x[MT];
@@ -245,7 +237,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
         f32x4 first[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const float f = lds_read(reinterpret_cast<const float*>(s_x[buf] + kSumAt) + p * kBM + 64 * wm + 16 * i + c);
+          const float f = lds_read(reinterpret_cast<const float*>(s_x[buf] + kSumAt) + p * kBM + 16 * i + c);
           first[i] = f32x4{f, f, f, f};
 #pragma unroll
           for (int j = 0; j < JG; ++j) x[j][i] = read_x(buf, i, 4 * (p * JG + j) + g);
@@ -271,18 +263,31 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
 
   // One barrier per step: past it the step's rows have landed for every wave (each waited for its own loads)
   // and every wave is done with the step before, whose buffer the next loads overwrite.
-  Codes q, next;
+  Codes q[2];
   load_x(step0, 0);
-  load_w(q, step0);
-  for (int st = step0, buf = 0; st < step1; ++st, buf ^= 1) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __syncthreads();
-    if (st + 1 < step1) {
-      load_x(st + 1, buf ^ 1);
-      load_w(next, st + 1);
+  load_w(q[0], step0);
+  for (int st = step0; st < step1; st += 2) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      if (st + d >= step1) break;
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (st + d + 1 < step1) {
+        load_x(st + d + 1, d ^ 1);
+        load_w(q[d ^ 1], st + d + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      compute(q[d], d);
+      // The step's sums end here: put off behind the next loads, they would take registers that there are not.
+#ifdef __HIP_DEVICE_COMPILE__  // the host has no such registers
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(acc[i][b]));
+#endif
+      __builtin_amdgcn_sched_barrier(0);
     }
-    compute(q, buf, st);
-    q = next;
   }
 
 #pragma unroll
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
     if (n >= a.n) continue;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const int row = m0 + 64 * wm + 16 * i + c;
+      const int row = m0 + 16 * i + c;
       if (row >= a.rows) continue;
       f32x4 y[MATS];
 #pragma unroll
@@ -315,13 +320,16 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
 
 // How the work is cut, from the sizes alone
 struct ManyPlan {
+  int nb;  // tiles of outputs of a wave
   int mblocks, nblocks, parts, steps, mpad, npad;
   size_t part_at, bytes;
 };
 inline ManyPlan many_plan(int rows, int n, int k, int mats, int tiles_per_step) {
   ManyPlan p{};
+  p.nb = rows <= 128 ? 2 : 4;
+  const int bn = 64 * p.nb / mats;
   p.mblocks = (rows + kBM - 1) / kBM;
-  p.nblocks = (n + 128 / mats - 1) / (128 / mats);
+  p.nblocks = (n + bn - 1) / bn;
   p.mpad = p.mblocks * kBM;
   p.npad = (n + 15) / 16 * 16;
   const int ktiles = (k + 127) / 128, all = (ktiles + tiles_per_step - 1) / tiles_per_step;
@@ -335,6 +343,18 @@ inline ManyPlan many_plan(int rows, int n, int k, int mats, int tiles_per_step) 
   return p;
 }
 
+template <typename X, int GPT, bool SF16, int MATS>
+void launch_many_scales(const ManyArgs& m, const ManyPlan& p, hipStream_t stream) {
+  const auto go = [&](auto kernel) {
+    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", kernel, dim3((unsigned)p.mblocks * p.nblocks * p.parts),
+                   dim3(256), 0, stream, m);
+  };
+  if (p.nb == 4)
+    go((k_w4_many<X, GPT, MATS, SF16, 4>));
+  else
+    go((k_w4_many<X, GPT, MATS, SF16, 2>));
+}
+
 template <typename X, int GPT, int MATS>
 hipError_t launch_many(const W4Args& a, hipStream_t stream) {
   constexpr bool kF8 = __is_same(X, F8);
@@ -345,13 +365,10 @@ hipError_t launch_many(const W4Args& a, hipStream_t stream) {
     const int64_t items = (int64_t)p.mpad * a.ktiles;
     PSISPEC_LAUNCH("w4_sums", (k_w4_sums<X>), dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, m);
   }
-  const dim3 grid((unsigned)p.mblocks * p.nblocks * p.parts);
   if (GPT > 0 && a.scale_f16)
-    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", (k_w4_many<X, GPT, MATS, GPT != 0>), grid, dim3(256), 0, stream,
-                   m);
+    launch_many_scales<X, GPT, GPT != 0, MATS>(m, p, stream);
   else
-    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", (k_w4_many<X, GPT, MATS, false>), grid, dim3(256), 0, stream,
-                   m);
+    launch_many_scales<X, GPT, false, MATS>(m, p, stream);
   if (p.parts > 1) {
     const int64_t all = (int64_t)a.rows * p.npad / 4;
     PSISPEC_LAUNCH("w4_join", k_w4_join<MATS>, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, stream, m);

@@ -34,7 +34,9 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4PackArgs a, W4Layout l) {
   if (mx) {
     const uint8_t* sc = static_cast<const uint8_t*>(a.scales) + (int64_t)n * a.scales_stride;
     const int blocks = a.k / 32, b = 4 * t + g;
-    a.packed[l.scales_at + tile * 64 + lane] = in && b < blocks ? sc[b] : 0;
+    uint8_t* at = a.packed + l.scales_at + mx_scale_at(nt, t, l.ktiles) + 2 * lane;
+    at[0] = in && b < blocks ? sc[b] : 0;
+    if (t == l.ktiles - 1 && t % 2 == 0) at[1] = 0;  // no tile: never decoded but with rows of zeros
     if (t == 0) {
       int top = 0;
       if (in)
