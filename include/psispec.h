@@ -574,7 +574,8 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  (F16 rows with MX weights:
  * exact for scales down to 2^-36 of the output's largest, smaller ones give weights off by at most 2^-38 of
  * that largest scale.)  Infinities in x give infinities or NaN.
- *   x        rows of k elements, x_stride elements apart, 16-byte aligned, strides of 16-byte multiples: dtype
+ *   x        rows of k elements, x_stride elements apart, 16-byte aligned, strides of 16-byte multiples up to 2^24
+ *            bytes: dtype
  *            PSISPEC_BF16, PSISPEC_F16, or (MX weights) PSISPEC_F8E4M3 with x_scale: rows of k / 32 E8M0 bytes,
  *            x_scale_stride apart (NULL for the other types).  8-bit rows go through the scaled matrix
  *            instruction at twice the 16-bit rate

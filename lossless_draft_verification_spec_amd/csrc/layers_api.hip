@@ -12,6 +12,8 @@ constexpr int kMaxFeatures = 1 << 20;
 constexpr int kMaxRows = (1 << 24) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 36;  // elements: a row's offset stays below 2^62 bytes
 
+constexpr int64_t kMaxRowStride = 1 << 24;  // bytes: 64 rows are reached by 32-bit offsets
+
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
 // `n` rows of `width` bytes, `stride` bytes apart
@@ -91,7 +93,7 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
   if ((e = check_packed(w)) != PSISPEC_OK || (w2 && (e = check_packed(w2)) != PSISPEC_OK)) return e;
   const int xb = f8 ? 1 : 2;
   if (!x || !out || f8 != (x_scale != nullptr) || !aligned(x, 16) || !aligned(out, 2) || !aligned(bias, 2) || !stride_ok(x_stride, w->k, rows) ||
-      (rows > 1 && x_stride * xb % 16) || !stride_ok(out_stride, w->n, rows) ||
+      (rows > 1 && (x_stride * xb % 16 || x_stride * xb > kMaxRowStride)) || !stride_ok(out_stride, w->n, rows) ||
       (f8 && !stride_ok(xs_stride, w->k / 32, rows)))
     return PSISPEC_EINVAL;
   const Rows ro{out, out_stride * 2, (int64_t)w->n * 2, rows}, rx{x, x_stride * xb, (int64_t)w->k * xb, rows},

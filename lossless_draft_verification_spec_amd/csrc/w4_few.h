@@ -1,4 +1,4 @@
-// w4_few.h -- the 4-bit products of few rows.
+// w4_few.h -- the 4-bit products of few rows, and of more where there are few outputs.
 //
 // The weights are read once, straight from memory into the registers that feed the matrix cores (the
 // packed order makes each load 1 KB in a row).  A workgroup owns NT tiles of 16 outputs; its KW waves take
@@ -236,12 +236,14 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
 }
 
 // The largest tile whose workgroups still cover most of the 256 CUs: a tile of twice the rows or outputs reads
-// the rows' or the weights' operands once instead of twice.  4096 x 4096, 64 rows: 64 rows x 32 outputs (128
-// workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 16384 x 4096, 64 rows: 64 x 32 17.9, 32 x 32
-// 20.4.  Eight waves share a tile's inputs, four when there are two workgroups per CU and more (64 x 32 at
-// 16384 outputs: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
+// the weights or the rows once instead of twice.  4096 x 4096 INT, 64 rows: 64 rows x 32 outputs (128
+// workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 12288 x 4096, 64 rows: 64 x 64 (192) 15.4,
+// 32 x 32 (768) 15.8.  Eight waves share a tile's inputs, four where several workgroups share a CU (64 rows x 32
+// outputs at 16384 x 4096: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
 template <typename X, int GPT, bool SF16, int MATS>
 hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
+  constexpr int kFill = 192, kShare = 320, kLong = 64;  // workgroups, workgroups, tiles of 128 inputs
+  constexpr int kWide = MATS == 2 ? 2 : 4;
   const auto blocks = [&](int r4, int nt) {
     return (int64_t)((a.ntiles + nt - 1) / nt) * ((a.rows + 4 * r4 - 1) / (4 * r4));
   };
@@ -249,14 +251,20 @@ hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
     PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", kernel, dim3((unsigned)blocks(r4, nt)), dim3(64 * kw), 0,
                    stream, a);
   };
-  constexpr int kFill = 192, kLong = 64;  // workgroups; tiles of 128 inputs
-  if (a.rows > 32 && blocks(16, 2) >= kFill) {
-    if (blocks(16, 2) >= 512)
-      go((k_w4_few<X, GPT, SF16, 16, 2, MATS, 4>), 16, 2, 4);
+  if (a.rows > 32 && blocks(16, kWide) >= kFill) {
+    if (blocks(16, kWide) >= kShare)
+      go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 4>), 16, kWide, 4);
     else
-      go((k_w4_few<X, GPT, SF16, 16, 2, MATS, 8>), 16, 2, 8);
+      go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 8>), 16, kWide, 8);
+  } else if (MATS == 1 && a.rows > 16 && blocks(8, 4) >= kFill) {
+    if constexpr (MATS == 1) {
+      if (blocks(8, 4) >= kShare)
+        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 4>), 8, 4, 4);
+      else
+        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 8>), 8, 4, 8);
+    }
   } else if (a.rows > 16 && blocks(8, 2) >= kFill) {
-    if (blocks(8, 2) >= 512)
+    if (blocks(8, 2) >= kShare)
       go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 4>), 8, 2, 4);
     else
       go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 8>), 8, 2, 8);

@@ -7,6 +7,10 @@
 // products start from, -24 sum(x) per row and group, is formed by one pass over the rows before (k_w4_sums) and
 // travels with them: formed by the matrix cores here it would be a fifth of their work.  Loads run one step
 // ahead (two or three steps ahead, and 128 rows per workgroup, were no faster).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
+// 576 rows (device time): 12288 x 4096 INT 66 us (0.88 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 33 (1.7); two
+// such INT layers gated 125; 2048 rows, 4096 x 12288: 199, 163 (1.26), 86 (2.4); a library product of 16-bit
+// numbers takes 184 for the last.  INT is bound by the vector units beside the matrix cores (decoding, scales),
+// the others by the matrix cores and the traffic between the L2 and the CUs.
 #pragma once
 
 #include "w4.h"
@@ -318,31 +322,6 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
   }
 }
 
-// How the work is cut, from the sizes alone
-struct ManyPlan {
-  int nb;  // tiles of outputs of a wave
-  int mblocks, nblocks, parts, steps, mpad, npad;
-  size_t part_at, bytes;
-};
-inline ManyPlan many_plan(int rows, int n, int k, int mats, int tiles_per_step) {
-  ManyPlan p{};
-  p.nb = rows <= 128 ? 2 : 4;
-  const int bn = 64 * p.nb / mats;
-  p.mblocks = (rows + kBM - 1) / kBM;
-  p.nblocks = (n + bn - 1) / bn;
-  p.mpad = p.mblocks * kBM;
-  p.npad = (n + 15) / 16 * 16;
-  const int ktiles = (k + 127) / 128, all = (ktiles + tiles_per_step - 1) / tiles_per_step;
-  const int64_t blocks = (int64_t)p.mblocks * p.nblocks;
-  int parts = blocks >= 256 ? 1 : (int)(512 / blocks);
-  if (parts > all / 4) parts = all / 4 > 1 ? all / 4 : 1;
-  p.steps = (all + parts - 1) / parts;
-  p.parts = (all + p.steps - 1) / p.steps;
-  p.part_at = ((size_t)ktiles * 4 * p.mpad * 4 + 255) / 256 * 256;
-  p.bytes = p.part_at + (p.parts > 1 ? (size_t)p.parts * mats * rows * p.npad * 4 : 0);
-  return p;
-}
-
 template <typename X, int GPT, bool SF16, int MATS>
 void launch_many_scales(const ManyArgs& m, const ManyPlan& p, hipStream_t stream) {
   const auto go = [&](auto kernel) {
@@ -358,8 +337,8 @@ void launch_many_scales(const ManyArgs& m, const ManyPlan& p, hipStream_t stream
 template <typename X, int GPT, int MATS>
 hipError_t launch_many(const W4Args& a, hipStream_t stream) {
   constexpr bool kF8 = __is_same(X, F8);
-  const ManyPlan p = many_plan(a.rows, a.n, a.k, MATS, kF8 ? 2 : 1);
-  ManyArgs m{a, static_cast<float*>(a.workspace), nullptr, p.mpad, p.npad, p.mblocks, p.nblocks, p.parts, p.steps};
+  const ManyPlan p = many_plan(a.rows, a.n, a.k, MATS);
+  ManyArgs m{a, static_cast<float*>(a.workspace), nullptr, p.mpad, p.npad, p.mblocks, p.nblocks, p.parts, kF8 ? p.steps / 2 : p.steps};
   m.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + p.part_at);
   if constexpr (!kF8 && GPT > 0) {
     const int64_t items = (int64_t)p.mpad * a.ktiles;

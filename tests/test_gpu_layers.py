@@ -237,17 +237,31 @@ def test_linear_large(rows, n, k, dtype, fmt, group):
     _product(rows, n, k, dtype, fmt, group, seed=3, spread=8)
 
 
+@pytest.mark.parametrize("rows,n,k", [(1601, 2039, 32), (1601, 2039, 160), (3137, 2047, 288), (801, 2033, 8224),
+                                      (900, 2048, 16384)])
+@pytest.mark.parametrize("dtype,fmt,group", KINDS)
+def test_linear_many(rows, n, k, dtype, fmt, group):
+    """Sizes that are cut into tiles of 64 rows x 256 and 128 outputs, and into parts of the inputs."""
+    _product(rows, n, k, dtype, fmt, group, seed=k, pad=16 * (k < 1000), bias=k == 160, spread=8)
+
+
+@pytest.mark.parametrize("rows,n,k", [(801, 2039, 160), (1600, 2047, 416), (449, 2035, 8224)])
+@pytest.mark.parametrize("dtype,fmt,group", KINDS)
+def test_gated_many(rows, n, k, dtype, fmt, group):
+    _product(rows, n, k, dtype, fmt, group, seed=k, act="silu", pad=16 * (k < 1000), scale_dtype=FH)
+
+
 def test_8bit_rows_to_f16():
     _product(20, 33, 256, F8, "mx", 32, seed=1, out_dtype=FH)
     _product(90, 33, 256, F8, "mx", 32, seed=1, out_dtype=FH, act="silu")
 
 
-@pytest.mark.parametrize("rows", [4, 80])
-def test_f16_rows_take_far_apart_mx_scales(rows):
+@pytest.mark.parametrize("rows,n", [(4, 48), (80, 48), (1601, 2039)])
+def test_f16_rows_take_far_apart_mx_scales(rows, n):
     """Scales over 2^-30 of the largest are exact for F16 rows; an output whose scales are all small, or all
     large, is scaled back as a whole."""
     g = _gen(2)
-    n, k = 48, 512
+    k = 512
     codes, s = ref.make_weight(n, k, "mx", 32, g, spread=30)
     e = s.view(torch.uint8).clone()
     e[1] = 60   # an output of tiny weights, one of large ones
@@ -266,11 +280,11 @@ def test_f16_rows_take_far_apart_mx_scales(rows):
     _within(got, want, bound)
 
 
-@pytest.mark.parametrize("rows", [3, 80])
+@pytest.mark.parametrize("rows,n", [(3, 40), (80, 40), (1601, 2039)])
 @pytest.mark.parametrize("dtype", [BF, FH, F8])
-def test_nan_scales_and_bad_rows_stay_where_they_are(rows, dtype):
+def test_nan_scales_and_bad_rows_stay_where_they_are(rows, n, dtype):
     g = _gen(9)
-    n, k = 40, 288
+    k = 288
     codes, s = ref.make_weight(n, k, "mx", 32, g)
     e = s.view(torch.uint8).clone()
     e[7, 3] = 255
@@ -289,12 +303,12 @@ def test_nan_scales_and_bad_rows_stay_where_they_are(rows, dtype):
     assert torch.equal(out[rest], clean[rest])
 
 
-@pytest.mark.parametrize("rows", [3, 80])
+@pytest.mark.parametrize("rows,n", [(3, 33), (80, 33), (1601, 2039)])
 @pytest.mark.parametrize("dtype,fmt,group", KINDS)
-def test_inputs_behind_the_last_are_not_read(rows, dtype, fmt, group):
+def test_inputs_behind_the_last_are_not_read(rows, n, dtype, fmt, group):
     """NaN right behind each row's inputs, in the columns that a tile of 128 still covers, and behind the last row."""
     g = _gen(4)
-    n, k = 33, 160
+    k = 160
     x, xs = ref.make_rows(rows, k, dtype, g)
     codes, s = ref.make_weight(n, k, fmt, group, g)
     raw = torch.full((rows + 40, k + 128), float("nan"), device=DEV).to(dtype)
@@ -338,10 +352,10 @@ def test_empty_and_batched_rows():
     assert psispec_add_rmsnorm(x[:0])[0].shape == (0, 9, 128)
 
 
-@pytest.mark.parametrize("rows", [1, 30, 64, 300])
-def test_runs_are_bitwise_equal(rows):
+@pytest.mark.parametrize("rows,n", [(1, 520), (30, 520), (64, 520), (300, 520), (1601, 2039)])
+def test_runs_are_bitwise_equal(rows, n):
     g = _gen(rows)
-    codes, s = ref.make_weight(520, 2080, "int", 128, g)
+    codes, s = ref.make_weight(n, 2080, "int", 128, g)
     w = psispec_w4_pack(_gpu(codes), _gpu(s))
     x = _gpu(ref.make_rows(rows, 2080, BF, g)[0])
     first = psispec_w4_linear(x, w)
@@ -351,9 +365,10 @@ def test_runs_are_bitwise_equal(rows):
 
 def test_two_streams_with_workspaces_of_their_own():
     g = _gen(12)
-    codes, s = ref.make_weight(512, 1024, "int", 128, g)
+    codes, s = ref.make_weight(4096, 8192, "int", 128, g)
     w = psispec_w4_pack(_gpu(codes), _gpu(s))
-    xs = [_gpu(ref.make_rows(r, 1024, BF, g)[0]) for r in (200, 140)]
+    xs = [_gpu(ref.make_rows(r, 8192, BF, g)[0]) for r in (500, 440)]  # inputs in parts
+    assert all(w4_workspace_bytes(x.shape[0], 4096, 8192) > x.shape[0] * 4096 * 4 for x in xs)
     want = [psispec_w4_linear(x, w) for x in xs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in xs]
@@ -366,12 +381,12 @@ def test_two_streams_with_workspaces_of_their_own():
         assert all(torch.equal(a, y) for y in b)
 
 
-@pytest.mark.parametrize("rows", [9, 160])
-def test_layer_in_a_graph(rows):
+@pytest.mark.parametrize("fmt,rows,h,f", [("mx", 9, 256, 640), ("mx", 160, 256, 640), ("int", 1601, 1024, 2048),
+                                          ("mx", 801, 2048, 8192)])
+def test_layer_in_a_graph(fmt, rows, h, f):
     """Norm, gated projections and the projection back, captured once and replayed on new rows."""
     g = _gen(13)
-    h, f = 256, 640
-    mats = [psispec_w4_pack(*map(_gpu, ref.make_weight(*nk, "mx", 32, g)), "mx", 32) for nk in
+    mats = [psispec_w4_pack(*map(_gpu, ref.make_weight(*nk, fmt, 32, g)), fmt, 32) for nk in
             ((f, h), (f, h), (h, f))]
     wt = _gpu((1 + 0.1 * torch.randn(h, generator=g)).to(BF))
     x = torch.zeros((rows, h), dtype=BF, device=DEV)
@@ -379,7 +394,7 @@ def test_layer_in_a_graph(rows):
     ro = torch.zeros_like(res)
 
     def layer():
-        q, _, s = psispec_add_rmsnorm(x, wt, residual=res, residual_out=ro, quant="mx")
+        q, _, s = psispec_add_rmsnorm(x, wt, residual=res, residual_out=ro, quant="mx" if fmt == "mx" else None)
         a = psispec_w4_gated(q, mats[0], mats[1], x_scale=s)
         return psispec_w4_linear(a, mats[2])
 
@@ -492,7 +507,7 @@ def test_refusals_of_the_binding():
 
 
 def test_workspace_is_what_the_query_says():
-    for rows, n, k in ((1, 64, 128), (100, 500, 512), (700, 4096, 4096)):
+    for rows, n, k in ((1, 64, 128), (100, 500, 512), (1601, 2039, 416), (801, 2033, 8224)):
         g = _gen(rows)
         codes, s = ref.make_weight(n, k, "int", 128, g)
         w = psispec_w4_pack(_gpu(codes), _gpu(s))

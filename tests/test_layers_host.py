@@ -89,7 +89,7 @@ def test_product_checks(L):
     for kw in (dict(dtype=F8), dict(dtype=F8, sc=SC, ss=7), dict(sc=SC, ss=8)):
         assert _linear(L, m, **kw) == -1, kw
     for kw in (dict(rows=-1), dict(rows=1 << 24), dict(x=None), dict(out=None), dict(x=X + 8), dict(xs=248), dict(xs=260),
-               dict(os_=63), dict(out=OUT + 1), dict(bias=W + 1), dict(xs=1 << 40)):
+               dict(os_=63), dict(out=OUT + 1), dict(bias=W + 1), dict(xs=1 << 40), dict(xs=(1 << 23) + 8)):
         assert _linear(L, **kw) == -1, kw
     # 2^23 tiles of 16 rows x 16 outputs and more
     assert _linear(L, _weight(n=1 << 20), rows=2048, os_=1 << 20) == -1
@@ -101,7 +101,7 @@ def test_product_checks(L):
     assert _gated(L, out=PK2) == -1
     for kw in (dict(act=-1), dict(act=3)):
         assert _gated(L, **kw) == -1, kw
-    for kw in (dict(n=80), dict(k=128), dict(group=64), MX):
+    for kw in (dict(n=80), dict(k=128), dict(group=64), dict(scale_dtype=FH), MX):
         assert _gated(L, u=_weight(packed=PK2, **kw)) == -1, kw
     assert L.psispec_w4_gated(ctypes.byref(_weight()), None, 0, X, 256, BF, None, 0, 4, OUT, 64, BF, WS, BIG, None) == -1
 
@@ -124,6 +124,11 @@ def test_pack_checks(L):
 def test_workspace_query(L):
     for bad in ((0, 64, 256, 1), (4, 0, 256, 1), (4, 64, 0, 1), (4, 64, 256, 0), (4, 64, 256, 3), (1 << 24, 64, 256, 1)):
         assert L.psispec_w4_workspace(*bad) == 0
+    assert L.psispec_w4_workspace(64, 1 << 16, 4096, 2) == 0  # few rows need none
+    assert L.psispec_w4_workspace(576, 12288, 4096, 2) > 0
+    w = _weight(n=12288, k=4096)
+    for kw in (dict(ws=None), dict(ws=WS + 16), dict(wsn=L.psispec_w4_workspace(576, 12288, 4096, 1) - 1)):
+        assert _linear(L, w, xs=4096, os_=12288, rows=576, x=1 << 35, out=1 << 36, **kw) == -3, kw
 
 
 def test_the_binding_needs_gpu_tensors():
