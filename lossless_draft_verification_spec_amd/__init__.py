@@ -968,25 +968,22 @@ def psispec_pages_reserve(pool: torch.Tensor, table: torch.Tensor, refs: torch.T
     return status
 
 
-def _rows_of(t: torch.Tensor, width: int, dev, name: str):
-    """(pointer, elements from one row to the next, rows) of [..., width]: rows of contiguous elements,
-    evenly spaced."""
-    if t.get_device() != dev.index:
+def _rows_of(t: torch.Tensor, shape, idx: int, name: str):
+    """(pointer, elements from one row to the next) of a tensor of this shape on GPU `idx`: rows of
+    contiguous elements along its last dimension, evenly spaced."""
+    if t.shape != shape:
+        raise PsispecError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != idx:
         _gpu_device(t, name)
-        _same_dev(t, dev, name)
-    shape, st = t.shape, t.stride()
-    if len(shape) < 1 or shape[-1] != width:
-        raise PsispecError(f"{name} must be [..., {width}], got {list(shape)}")
-    if len(shape) == 2:
-        rows, step = shape[0], st[0]
-        if (st[1] == 1 or width == 1) and (step >= width or rows <= 1):
-            return t.data_ptr(), step if rows > 1 else width, rows
-    rows, step = 1, width
+        raise PsispecError(f"{name} is on {t.device}, expected cuda:{idx}")
+    width = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    st = t.stride()
     if width > 1 and st[-1] != 1:
         raise PsispecError(f"the rows of {name} must be contiguous")
+    rows, step = 1, width
     for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        if n == 0:
-            return t.data_ptr(), width, 0
         if n == 1:
             continue
         if rows == 1:
@@ -996,7 +993,16 @@ def _rows_of(t: torch.Tensor, width: int, dev, name: str):
         rows *= n
     if rows > 1 and step < width:
         raise PsispecError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), step, rows
+    return t.data_ptr(), step
+
+
+def _elsewhere(idx: int, stream) -> bool:
+    """The call is not on GPU idx's current stream: it goes there first (_On.guard)."""
+    return stream is not None or _current_device() != idx
+
+
+def _idx_stream(idx: int):
+    return _raw_stream(idx) if _raw_stream is not None else _stream(None)
 
 
 _SIXTEEN = {torch.bfloat16: PSISPEC_BF16, torch.float16: PSISPEC_F16}
@@ -1016,62 +1022,66 @@ def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
     over 448) or "mx" (float8_e4m3fn with a float8_e8m0fnu scale per 32 columns, the smallest power of two
     that keeps them within 448: the rows of psispec_w4_linear and psispec_w4_gated); out times scale
     is the norm.  Returns (out, residual_out, scale), None for what there is not."""
-    if x.dim() < 1:
-        raise PsispecError("x must be [..., dim]")
-    dim, dt = x.shape[-1], x.dtype
-    dev, code = _gpu_device(x, "x"), _SIXTEEN.get(dt)
-    if code is None:
-        raise PsispecError(f"x must be bfloat16 or float16, got {dt}")
-    if quant not in (None, "row", "mx"):
-        raise PsispecError(f'quant must be None, "row" or "mx", got {quant!r}')
-    xp, xs, rows = _rows_of(x, dim, dev, "x")
-    wp = 0 if weight is None else _flat(weight, (dim,), dt, dev, "weight")
-    rp = rs = rop = ros = 0
-    rcode = code
+    shape, dt, idx = x.shape, x.dtype, x.get_device()
+    code = _SIXTEEN.get(dt)
+    if idx < 0 or code is None or not shape or shape[-1] < 1:
+        _gpu_device(x, "x")
+        raise PsispecError(f"x must be bfloat16 or float16 [..., dim], got {dt} {list(shape)}")
+    if _elsewhere(idx, stream):
+        with _On.guard(x.device, stream):
+            return psispec_add_rmsnorm(x, weight, residual, residual_out, eps, quant, out, scale)
+    dim = shape[-1]
+    rows = x.numel() // dim
+    xp, xs = _rows_of(x, shape, idx, "x")
+    wp = rp = rs = rop = ros = sp = ss = 0
+    if weight is not None:
+        if weight.dtype != dt or weight.shape != shape[-1:] or not weight.is_contiguous():
+            raise PsispecError(f"weight must be contiguous {str(dt)[6:]} [{dim}]")
+        wp, _ = _rows_of(weight, weight.shape, idx, "weight")
+    rcode, rt = code, dt
     if residual is not None:
+        rt = residual.dtype
+        if rt != dt and rt != torch.float32:
+            raise PsispecError(f"residual must be {dt} or float32, got {rt}")
+        rp, rs = _rows_of(residual, shape, idx, "residual")
         if residual_out is None:
             residual_out = residual
-        if residual.dtype != dt and residual.dtype != torch.float32:
-            raise PsispecError(f"residual must be {dt} or float32, got {residual.dtype}")
-        if residual.shape != x.shape:
-            raise PsispecError("residual must have the shape of x")
-        rp, rs, _ = _rows_of(residual, dim, dev, "residual")
+    elif residual_out is not None and residual_out.dtype == torch.float32:
+        rt = torch.float32
     if residual_out is not None:
-        rt = residual_out.dtype
-        if rt != (dt if residual is None else residual.dtype) and (residual is not None
-                                                                   or rt != torch.float32):
+        if residual_out.dtype != rt:
             raise PsispecError("residual_out must have the dtype of residual (of x, or float32, without)")
-        if residual_out.shape != x.shape:
-            raise PsispecError("residual_out must have the shape of x")
-        rop, ros, _ = _rows_of(residual_out, dim, dev, "residual_out")
+        rop, ros = _rows_of(residual_out, shape, idx, "residual_out")
         if rt == torch.float32:
             rcode = PSISPEC_F32
-    ot = dt if quant is None else torch.float8_e4m3fn
-    sp, ss, scode = 0, 0, PSISPEC_F32
-    with _On.guard(dev, stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=ot, device=dev)
-        elif out.dtype != ot or out.shape != x.shape:
-            raise PsispecError(f"out must be {ot} with the shape of x")
-        op, os_, _ = _rows_of(out, dim, dev, "out")
-        if quant == "row":
-            if scale is None:
-                scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-            sp = _flat(scale, x.shape[:-1], torch.float32, dev, "scale")
-        elif quant == "mx":
+    ocode, scode = code, PSISPEC_F32
+    if quant is None:
+        if scale is not None:
+            raise PsispecError("scale goes with quant")
+    else:
+        dt, ocode = torch.float8_e4m3fn, PSISPEC_F8E4M3
+        if quant == "mx":
             if dim % 32:
                 raise PsispecError("mx scales need a multiple of 32 columns")
-            if scale is None:
-                scale = torch.empty((*x.shape[:-1], dim // 32), dtype=torch.float8_e8m0fnu, device=dev)
-            elif scale.dtype != torch.float8_e8m0fnu or scale.shape[:-1] != x.shape[:-1]:
-                raise PsispecError("scale must be float8_e8m0fnu [..., dim / 32]")
-            sp, ss, _ = _rows_of(scale, dim // 32, dev, "scale")
-            scode = PSISPEC_E8M0
-        elif scale is not None:
-            raise PsispecError("scale goes with quant")
-        rc = lib().psispec_add_rmsnorm(xp, xs, code, rp, rs, rop, ros, rcode, wp, eps, rows, dim, op, os_,
-                                       _LAYER_DTYPES[ot], sp, ss, scode, _dev_stream(dev))
-    _check(rc, "psispec_add_rmsnorm")
+            sshape, st, scode = (*shape[:-1], dim // 32), torch.float8_e8m0fnu, PSISPEC_E8M0
+        elif quant == "row":
+            sshape, st = shape[:-1], torch.float32
+        else:
+            raise PsispecError(f'quant must be None, "row" or "mx", got {quant!r}')
+        if scale is None:
+            scale = torch.empty(sshape, dtype=st, device=x.device)
+        if scale.dtype != st or (scode == PSISPEC_F32 and not scale.is_contiguous()):
+            raise PsispecError(f"scale must be {st} {list(sshape)}, contiguous for one number per row")
+        sp, ss = _rows_of(scale, sshape, idx, "scale") if sshape else (scale.data_ptr(), 0)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    elif out.dtype != dt:
+        raise PsispecError(f"out must be {dt}, got {out.dtype}")
+    op, os_ = _rows_of(out, shape, idx, "out")
+    rc = lib().psispec_add_rmsnorm(xp, xs, code, rp, rs, rop, ros, rcode, wp, eps, rows, dim, op, os_, ocode,
+                                   sp, ss, scode, _idx_stream(idx))
+    if rc:
+        _check(rc, "psispec_add_rmsnorm")
     return out, residual_out, scale
 
 
@@ -1079,11 +1089,13 @@ class W4Weight:
     """A linear layer's weights of 4 bits in the library's order (psispec_w4_pack): out_features,
     in_features, group, format ("int" or "mx"), scale_dtype, packed (uint8)."""
 
-    __slots__ = ("packed", "out_features", "in_features", "group", "format", "scale_dtype", "device", "_struct")
+    __slots__ = ("packed", "out_features", "in_features", "group", "format", "scale_dtype", "_struct",
+                 "_need")
 
     def __init__(self, packed, out_features, in_features, group, format, scale_dtype):
         self.packed, self.out_features, self.in_features = packed, out_features, in_features
-        self.group, self.format, self.scale_dtype, self.device = group, format, scale_dtype, packed.device
+        self.group, self.format, self.scale_dtype = group, format, scale_dtype
+        self._need = {}  # workspace bytes by (rows, matrices)
         self._struct = _W4_STRUCT.pack(packed.data_ptr(), out_features, in_features, group,
                                        _W4_FORMATS[format], _W4_SCALES[scale_dtype], 0)
 
@@ -1122,8 +1134,8 @@ def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "in
     if need == 0:
         raise PsispecError("unsupported sizes (in_features a multiple of 32, at most 2^20 features; group 32 "
                            "for mx, 32, 64 or a multiple of 128 for int)")
-    cp, cs, _ = _rows_of(codes, k // 2, dev, "codes")
-    sp, ss, _ = _rows_of(scales, scales.shape[1], dev, "scales")
+    cp, cs = _rows_of(codes, codes.shape, dev.index, "codes")
+    sp, ss = _rows_of(scales, scales.shape, dev.index, "scales")
     with _On.guard(dev, stream):
         packed = _workspace_for(packed, need, dev, "psispec_w4_pack")
         w = W4Weight(packed, n, k, group, format, scales.dtype)
@@ -1132,53 +1144,61 @@ def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "in
     return w
 
 
-@functools.lru_cache(maxsize=4096)
 def w4_workspace_bytes(rows, out_features, in_features, matrices=1) -> int:
     return int(lib().psispec_w4_workspace(rows, out_features, in_features, matrices))
 
 
-def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace, stream):
-    k, n, dt = w.in_features, w.out_features, x.dtype
-    dev, code = _gpu_device(x, "x"), _LAYER_DTYPES.get(dt)
-    if code is None:
-        raise PsispecError(f"x must be bfloat16, float16 or float8_e4m3fn, got {dt}")
-    _same_dev(w, dev, "the weight")
-    xp, xs, rows = _rows_of(x, k, dev, "x")
-    sp = ss = 0
+def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace):
+    shape, dt, idx = x.shape, x.dtype, w.packed.get_device()
+    k, n = w.in_features, w.out_features
+    code = _LAYER_DTYPES.get(dt)
+    if code is None or not shape or shape[-1] != k:
+        raise PsispecError(f"x must be bfloat16, float16 or float8_e4m3fn [..., {k}], got {dt} {list(shape)}")
+    rows = x.numel() // k
+    xp, xs = _rows_of(x, shape, idx, "x")
+    sp = ss = bp = wp = wn = 0
     if code == PSISPEC_F8E4M3:
         if w.format != "mx":
             raise PsispecError("8-bit rows go with mx weights")
-        if x_scale is None or x_scale.dtype != torch.float8_e8m0fnu or x_scale.shape[:-1] != x.shape[:-1]:
+        if x_scale is None or x_scale.dtype != torch.float8_e8m0fnu:
             raise PsispecError("8-bit rows need x_scale, float8_e8m0fnu [..., in_features / 32]")
-        sp, ss, _ = _rows_of(x_scale, k // 32, dev, "x_scale")
+        sp, ss = _rows_of(x_scale, (*shape[:-1], k // 32), idx, "x_scale")
         ot = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+        if ot not in _SIXTEEN:
+            raise PsispecError("out must be bfloat16 or float16")
     else:
         if x_scale is not None:
             raise PsispecError("x_scale goes with 8-bit rows")
-        ot = out_dtype or dt
-    ocode = _SIXTEEN.get(ot)
-    if ocode is None or (code != PSISPEC_F8E4M3 and ot != dt):
-        raise PsispecError("out must be of x's dtype (bfloat16 or float16 for 8-bit rows)")
-    shape = (*x.shape[:-1], n)
-    bp = 0 if bias is None else _flat(bias, (n,), ot, dev, "bias")
-    with _On.guard(dev, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=ot, device=dev)
-        elif out.dtype != ot or out.shape != shape:
-            raise PsispecError(f"out must be {ot} {list(shape)}")
-        op, os_, _ = _rows_of(out, n, dev, "out")
-        need = w4_workspace_bytes(rows, n, k, 1 if w2 is None else 2)
-        wp = wn = 0
-        if need:
-            workspace = _workspace_for(workspace, need, dev, what)
-            wp, wn = workspace.data_ptr(), workspace.numel()
-        if w2 is None:
-            rc = lib().psispec_w4_linear(w._struct, xp, xs, code, sp, ss, rows, bp, op, os_, ocode, wp, wn,
-                                         _dev_stream(dev))
-        else:
-            rc = lib().psispec_w4_gated(w._struct, w2._struct, act, xp, xs, code, sp, ss, rows, op, os_,
-                                        ocode, wp, wn, _dev_stream(dev))
-    _check(rc, what)
+        ot = dt
+        if out_dtype is not None and out_dtype != dt:
+            raise PsispecError(f"out must be of x's dtype, {dt}")
+    oshape = (*shape[:-1], n)
+    if out is None:
+        out = torch.empty(oshape, dtype=ot, device=x.device)
+    elif out.dtype != ot:
+        raise PsispecError(f"out must be {ot}, got {out.dtype}")
+    op, os_ = _rows_of(out, oshape, idx, "out")
+    if bias is not None:
+        if bias.dtype != ot or not bias.is_contiguous():
+            raise PsispecError(f"bias must be contiguous {ot} [{n}]")
+        bp, _ = _rows_of(bias, (n,), idx, "bias")
+    key = (rows, w2 is None)
+    need = w._need.get(key)
+    if need is None:
+        if len(w._need) >= 4096:
+            w._need.clear()
+        need = w._need[key] = w4_workspace_bytes(rows, n, k, 1 if w2 is None else 2)
+    if need:
+        workspace = _workspace_for(workspace, need, x.device, what)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    if w2 is None:
+        rc = lib().psispec_w4_linear(w._struct, xp, xs, code, sp, ss, rows, bp, op, os_, _SIXTEEN[ot], wp, wn,
+                                     _idx_stream(idx))
+    else:
+        rc = lib().psispec_w4_gated(w._struct, w2._struct, act, xp, xs, code, sp, ss, rows, op, os_, _SIXTEEN[ot],
+                                    wp, wn, _idx_stream(idx))
+    if rc:
+        _check(rc, what)
     return out
 
 
@@ -1190,8 +1210,10 @@ def psispec_w4_linear(x: torch.Tensor, weight: W4Weight, x_scale: torch.Tensor |
     float8_e4m3fn with x_scale float8_e8m0fnu [..., in_features / 32], psispec_add_rmsnorm's "mx" rows)
     to out [..., out_features] of x's dtype (bf16, or f16 by out_dtype or out, for 8-bit rows).
     Rows 16-byte aligned and evenly spaced; bias [out_features] of out's dtype."""
-    return _w4_product("psispec_w4_linear", x, weight, None, 0, x_scale, bias, out, out_dtype, workspace,
-                       stream)
+    if _elsewhere(weight.packed.get_device(), stream):
+        with _On.guard(weight.packed.device, stream):
+            return psispec_w4_linear(x, weight, x_scale, bias, out, out_dtype, workspace)
+    return _w4_product("psispec_w4_linear", x, weight, None, 0, x_scale, bias, out, out_dtype, workspace)
 
 
 def psispec_w4_gated(x: torch.Tensor, gate: W4Weight, up: W4Weight, activation: str = "silu",
@@ -1205,11 +1227,14 @@ def psispec_w4_gated(x: torch.Tensor, gate: W4Weight, up: W4Weight, activation: 
     act = _W4_ACTIVATIONS.get(activation)
     if act is None:
         raise PsispecError(f'activation must be "silu", "gelu" or "gelu_tanh", got {activation!r}')
-    if (up.out_features, up.in_features, up.group, up.format, up.scale_dtype) != (
-            gate.out_features, gate.in_features, gate.group, gate.format, gate.scale_dtype):
+    if up._struct[8:] != gate._struct[8:]:  # all but the pointer
         raise PsispecError("gate and up must have the same features, group, format and scale type")
-    _same_dev(up, gate.device, "up")
-    return _w4_product("psispec_w4_gated", x, gate, up, act, x_scale, None, out, out_dtype, workspace, stream)
+    if up.packed.get_device() != gate.packed.get_device():
+        raise PsispecError(f"up is on {up.packed.device}, expected {gate.packed.device}")
+    if _elsewhere(gate.packed.get_device(), stream):
+        with _On.guard(gate.packed.device, stream):
+            return psispec_w4_gated(x, gate, up, activation, x_scale, out, out_dtype, workspace)
+    return _w4_product("psispec_w4_gated", x, gate, up, act, x_scale, None, out, out_dtype, workspace)
 
 
 def peak_read(buf: torch.Tensor, out: torch.Tensor, blocks: int, stream=None):
