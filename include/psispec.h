@@ -542,7 +542,8 @@ psispec_status psispec_add_rmsnorm(const void* x, int64_t x_stride, psispec_dtyp
  *                   6 and their negatives from code 8 on); scales E8M0, group 32
  * psispec_w4_pack writes a layer's codes and scales, as a checkpoint holds them, in the order in which the
  * products read them into `packed` (device, 256-byte aligned, psispec_w4_packed_bytes, the caller's for as long
- * as the layer is used).  Once per layer; the codes and scales are not needed afterwards.
+ * as the layer is used).  Once per layer; the codes and scales are not needed afterwards.  packed_bytes gives 0 for
+ * what is not supported.
  *   codes      row n at n * codes_stride bytes: k / 2 bytes, the even input's code in the low four bits
  *   scales     row n at n * scales_stride elements: ceil(k / group) of scale_dtype (a last group may be short)
  */
@@ -551,7 +552,7 @@ typedef enum { PSISPEC_W4_SILU = 0, PSISPEC_W4_GELU = 1, PSISPEC_W4_GELU_TANH = 
 typedef struct {
   void* packed;        /* device; the products only read it */
   int32_t n;           /* outputs, 1..2^20 */
-  int32_t k;           /* inputs, a multiple of 32, 32..2^20 */
+  int32_t k;           /* inputs, a multiple of 32, 32..2^20; ceil(n / 16) * ceil(k / 128) <= 2^26 - 4 */
   int32_t group;       /* inputs per scale */
   int32_t format;      /* psispec_w4_format */
   int32_t scale_dtype; /* PSISPEC_BF16 or PSISPEC_F16 (INT), PSISPEC_E8M0 (MX) */
@@ -571,14 +572,17 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *                      or a (1 + erf(a / sqrt 2)) / 2                                 (PSISPEC_W4_GELU)
  *                      or a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2           (PSISPEC_W4_GELU_TANH)
  * Codes and rows enter the matrix cores as they are, the sums are of 32 bits, INT scales are applied to the
- * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  (F16 rows with MX weights:
- * exact for scales down to 2^-36 of the output's largest, smaller ones give weights off by at most 2^-38 of
- * that largest scale.)  Infinities in x give infinities or NaN.
+ * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  Two exceptions:
+ *   F16 rows, MX weights  exact for scales down to 2^-36 of the output's largest; smaller ones give weights off
+ *                         by at most 2^-38 of that largest scale
+ *   8-bit rows            go through the scaled matrix instruction, at twice the 16-bit rate: among eight
+ *                         neighbouring inputs each product is cut to a multiple of 2^-13 of the power of two
+ *                         that the largest of them reaches
+ * An infinity or a NaN in a row, its scale or an output's scale gives infinities or NaN in that row, that
+ * output, and nowhere else.
  *   x        rows of k elements, x_stride elements apart, 16-byte aligned, strides of 16-byte multiples up to 2^24
- *            bytes: dtype
- *            PSISPEC_BF16, PSISPEC_F16, or (MX weights) PSISPEC_F8E4M3 with x_scale: rows of k / 32 E8M0 bytes,
- *            x_scale_stride apart (NULL for the other types).  8-bit rows go through the scaled matrix
- *            instruction at twice the 16-bit rate
+ *            bytes: dtype PSISPEC_BF16, PSISPEC_F16, or (MX weights) PSISPEC_F8E4M3 with x_scale: rows of k / 32
+ *            E8M0 bytes, x_scale_stride apart (NULL for the other types)
  *   bias     [n] of out_dtype, or NULL
  *   out      rows of n elements, out_stride elements apart, of dtype (8-bit x: BF16 or F16); overlaps no input
  *            (PSISPEC_EINVAL)

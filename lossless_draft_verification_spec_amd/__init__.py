@@ -1086,18 +1086,31 @@ def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
 
 
 class W4Weight:
-    """A linear layer's weights of 4 bits in the library's order (psispec_w4_pack): out_features,
-    in_features, group, format ("int" or "mx"), scale_dtype, packed (uint8)."""
+    """A linear layer's weights of 4 bits in the library's order (psispec_w4_pack, or its packed bytes again):
+    out_features, in_features, group, format ("int" or "mx"), scale_dtype, packed (uint8).  Not changed once
+    made."""
 
     __slots__ = ("packed", "out_features", "in_features", "group", "format", "scale_dtype", "_struct",
                  "_need")
 
     def __init__(self, packed, out_features, in_features, group, format, scale_dtype):
-        self.packed, self.out_features, self.in_features = packed, out_features, in_features
-        self.group, self.format, self.scale_dtype = group, format, scale_dtype
-        self._need = {}  # workspace bytes by (rows, matrices)
-        self._struct = _W4_STRUCT.pack(packed.data_ptr(), out_features, in_features, group,
-                                       _W4_FORMATS[format], _W4_SCALES[scale_dtype], 0)
+        dev = _gpu_device(packed, "packed")
+        need = w4_packed_bytes(out_features, in_features, group, format) if format in _W4_FORMATS else 0
+        if need == 0 or scale_dtype not in _W4_SCALES or (format == "mx") != (scale_dtype == torch.float8_e8m0fnu):
+            raise PsispecError(f"no such weights: {format} of {out_features} x {in_features}, group {group}, "
+                               f"scales {scale_dtype}")
+        if (packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < need
+                or packed.data_ptr() % 256):
+            raise PsispecError(f"packed must be a contiguous, 256-byte aligned uint8 tensor on {dev} with at least "
+                               f"{need} elements")
+        form = _W4_STRUCT.pack(packed.data_ptr(), out_features, in_features, group, _W4_FORMATS[format],
+                               _W4_SCALES[scale_dtype], 0)
+        # _need: workspace bytes by (rows, matrices)
+        for name, v in zip(self.__slots__, (packed, out_features, in_features, group, format, scale_dtype, form, {})):
+            object.__setattr__(self, name, v)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a W4Weight is not changed: make another")
 
 
 _W4_STRUCT = struct.Struct("Q6i")  # psispec_w4_weight
@@ -1208,7 +1221,9 @@ def psispec_w4_linear(x: torch.Tensor, weight: W4Weight, x_scale: torch.Tensor |
                       stream=None) -> torch.Tensor:
     """A linear layer with weights of 4 bits: x [..., in_features] (bf16, f16; or, with mx weights,
     float8_e4m3fn with x_scale float8_e8m0fnu [..., in_features / 32], psispec_add_rmsnorm's "mx" rows)
-    to out [..., out_features] of x's dtype (bf16, or f16 by out_dtype or out, for 8-bit rows).
+    to out [..., out_features] of x's dtype (bf16, or f16 by out_dtype or out, for 8-bit rows).  Sums are of 32
+    bits and no weight is rounded; 8-bit rows: among eight neighbouring inputs each product is cut to a multiple
+    of 2^-13 of the largest one's power of two.
     Rows 16-byte aligned and evenly spaced; bias [out_features] of out's dtype."""
     if _elsewhere(weight.packed.get_device(), stream):
         with _On.guard(weight.packed.device, stream):
@@ -1222,8 +1237,7 @@ def psispec_w4_gated(x: torch.Tensor, gate: W4Weight, up: W4Weight, activation: 
                      stream=None) -> torch.Tensor:
     """Both projections of a gated feed-forward block, the activation and the product in one kernel:
     act(x gate^T) * (x up^T), activation "silu", "gelu" or "gelu_tanh"; x, x_scale and out as in
-    psispec_w4_linear, gate and up of the same features, group,
-    format and scale type."""
+    psispec_w4_linear, gate and up of the same features, group, format and scale type."""
     act = _W4_ACTIVATIONS.get(activation)
     if act is None:
         raise PsispecError(f'activation must be "silu", "gelu" or "gelu_tanh", got {activation!r}')

@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int kMaxRows = (1 << 24) - 1;
+constexpr int64_t kMaxTiles = (int64_t(1) << 26) - 4;  // of a weight: a wave each packs them, below 2^32 threads
 constexpr int64_t kMaxStride = int64_t(1) << 36;  // elements: a row's offset stays below 2^62 bytes
 
 constexpr int64_t kMaxRowStride = 1 << 24;  // bytes: 64 rows are reached by 32-bit offsets
@@ -55,6 +56,7 @@ int element_size(psispec_dtype t) { return t == PSISPEC_F32 ? 4 : t == PSISPEC_F
 psispec_status check_weight(const psispec_w4_weight* w) {
   if (!w || w->reserved != 0) return PSISPEC_EINVAL;
   if (w->n < 1 || w->n > kMaxFeatures || w->k < 32 || w->k > kMaxFeatures || w->k % 32) return PSISPEC_EINVAL;
+  if ((int64_t)((w->n + 15) / 16) * ((w->k + 127) / 128) > kMaxTiles) return PSISPEC_EINVAL;
   if (w->format == PSISPEC_W4_MX) {
     if (w->group != 32) return PSISPEC_EINVAL;
     return w->scale_dtype == PSISPEC_E8M0 ? PSISPEC_OK : PSISPEC_EDTYPE;
@@ -206,7 +208,7 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
   const int64_t groups = (w->k + w->group - 1) / w->group;
   const int ss = w->format == PSISPEC_W4_MX ? 1 : 2;
   if (!codes || !scales || !aligned(scales, ss) || !stride_ok(codes_stride, w->k / 2, w->n) ||
-      !stride_ok(scales_stride, groups, w->n) || (int64_t)l.ntiles * l.ktiles > (int64_t(1) << 26) - 4)
+      !stride_ok(scales_stride, groups, w->n))
     return PSISPEC_EINVAL;
   const Rows rp{w->packed, 0, (int64_t)l.bytes, 1};
   if (meet(rp, Rows{codes, codes_stride, w->k / 2, w->n}) ||

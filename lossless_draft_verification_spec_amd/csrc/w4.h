@@ -20,9 +20,7 @@ namespace psispec {
 namespace w4 {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -108,15 +106,6 @@ __device__ inline float scale16(uint32_t bits, bool f16) {
   return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : bf16_bits_to_f32((uint16_t)bits);
 }
 
-// 8 numbers of 8 bits times their power of two: exact in BF16 (values under 2^-126 lose bits, as its
-// smallest numbers do)
-__device__ inline u32x4 f8_rows(uint32_t lo, uint32_t hi, float scale) {
-  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
-}
-
 // The scales of the eight blocks from `blk` on of a row of 8-bit numbers; those behind the last of `all` are 1
 // (their values are read as zeros)
 __device__ inline uint64_t row_scales(const uint8_t* row, int blk, int all) {
@@ -128,7 +117,9 @@ __device__ inline uint64_t row_scales(const uint8_t* row, int blk, int all) {
 
 // 128 inputs of 16 outputs with MX weights (lane: inputs 32 g + 0..31) and of 16 rows of 8 bits (lane: inputs
 // 16 g + 0..15 in x0, 64 + 16 g + 0..15 in x1; byte 0 of xs the scale of inputs 32 g ..),
-// byte WS of ws that of the output
+// byte WS of ws that of the output.  Twice the 16-bit instructions' rate; what it costs: among eight
+// neighbouring inputs each product is cut toward zero to a multiple of 2^-13 of the largest one's power of two
+// (eights are joined in 32 bits).  The rows' own rounding to 3 bits of mantissa is 2^-4 of each value.
 template <int WS>
 __device__ inline f32x4 mfma_mx(u32x4 w, int ws, u32x4 x0, u32x4 x1, int xs, f32x4 c) {
   const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
@@ -136,11 +127,11 @@ __device__ inline f32x4 mfma_mx(u32x4 w, int ws, u32x4 x0, u32x4 x1, int xs, f32
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, WS, ws, 0, xs);
 }
 
+// 1 + erf(z) = erfc(-z) and 1 + tanh(u) = 2 / (1 + exp(-2 u)): without the loss of digits on the negative side
 __device__ inline float activate(float x, int act) {
-  if (act == PSISPEC_W4_SILU) return x / (1.0f + expf(-x));
-  if (act == PSISPEC_W4_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
-  const float u = 0.79788456080286535588f * (x + 0.044715f * x * x * x);  // sqrt(2 / pi) (x + ...)
-  return 0.5f * x * (1.0f + tanhf(u));
+  if (act == PSISPEC_W4_GELU) return 0.5f * x * erfcf(-0.70710678118654752440f * x);
+  const float u = act == PSISPEC_W4_SILU ? x : 1.59576912160573071176f * (x + 0.044715f * x * x * x);  // 2 sqrt(2 / pi)
+  return x / (1.0f + expf(-u));
 }
 
 // The scales of the lane's outputs 4 g + 0..3, four numbers of 16 bits

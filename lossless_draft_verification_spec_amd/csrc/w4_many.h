@@ -27,24 +27,25 @@ struct ManyArgs {
   int mpad, npad, mblocks, nblocks, parts, steps;  // steps of a part
 };
 
-// -24 sum(x) over each group of each row; a wave per row and tile of 128 inputs
+// -24 sum(x) over each group of each row: 16 lanes per row and tile of 128 inputs, 8 inputs each.  Bound by the
+// rows' bytes: 2048 rows of 12288 11 us (4.6 TB/s).
 template <typename X>
 __global__ __launch_bounds__(256) void k_w4_sums(ManyArgs m) {
   const W4Args& a = m.a;
-  const int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // 16 lanes per item, 8 inputs each
-  const int t = (int)(item / m.mpad), row = (int)(item - (int64_t)t * m.mpad);
-  if (t >= a.ktiles) return;
-  const int c = threadIdx.x & 15, k = t * 128 + 8 * c;
-  float s = 0.0f;
-  if (row < a.rows && k < a.k) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + (int64_t)row * a.x_stride + k);
+  const int c = threadIdx.x & 15, per = 16 / a.gpt;  // lanes of a group
+  const int64_t all = (int64_t)m.mpad * a.ktiles;
+  for (int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); item < all; item += (int64_t)gridDim.x * 16) {
+    const int t = (int)(item / m.mpad), row = (int)(item - (int64_t)t * m.mpad), k = t * 128 + 8 * c;
+    float s = 0.0f;
+    if (row < a.rows && k < a.k) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + (int64_t)row * a.x_stride + k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s += scale16(v[i] & 0xffffu, __is_same(X, _Float16)) + scale16(v[i] >> 16, __is_same(X, _Float16));
+      for (int i = 0; i < 4; ++i)
+        s += scale16(v[i] & 0xffffu, __is_same(X, _Float16)) + scale16(v[i] >> 16, __is_same(X, _Float16));
+    }
+    for (int o = 1; o < per; o <<= 1) s += __shfl_xor(s, o, 64);  // mpad is a multiple of 64: whole waves
+    if (c % per == 0) m.sums[((int64_t)t * a.gpt + c / per) * m.mpad + row] = -24.0f * s;
   }
-  const int per = 16 / a.gpt;  // lanes of a group
-  for (int o = 1; o < per; o <<= 1) s += __shfl_xor(s, o, 64);
-  if (c % per == 0) m.sums[((int64_t)t * a.gpt + c / per) * m.mpad + row] = -24.0f * s;
 }
 
 // The parts' sums in their order, then what a product ends with; a thread per four outputs.
@@ -341,8 +342,9 @@ hipError_t launch_many(const W4Args& a, hipStream_t stream) {
   ManyArgs m{a, static_cast<float*>(a.workspace), nullptr, p.mpad, p.npad, p.mblocks, p.nblocks, p.parts, kF8 ? p.steps / 2 : p.steps};
   m.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + p.part_at);
   if constexpr (!kF8 && GPT > 0) {
-    const int64_t items = (int64_t)p.mpad * a.ktiles;
-    PSISPEC_LAUNCH("w4_sums", (k_w4_sums<X>), dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, m);
+    const int64_t blocks = (int64_t)p.mpad * a.ktiles / 16;  // a launch takes less than 2^32 threads
+    PSISPEC_LAUNCH("w4_sums", (k_w4_sums<X>), dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0,
+                   stream, m);
   }
   if (GPT > 0 && a.scale_f16)
     launch_many_scales<X, GPT, GPT != 0, MATS>(m, p, stream);

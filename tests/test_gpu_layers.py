@@ -1,13 +1,15 @@
 """The layers around the paged attention (through the binding) against 64-bit references: the norm with the
 residual's addition, linear layers with weights of 4 bits, the gated projections, and a run of them together
 with the cache."""
+import math
+
 import pytest
 import torch
 
 import layers_ref as ref
 from layers_ref import BF, E8, F8, FH
 from lossless_draft_verification_spec_amd import (
-    PsispecError, psispec_add_rmsnorm, psispec_paged_attention, psispec_qkv_append, psispec_w4_gated,
+    PsispecError, W4Weight, psispec_add_rmsnorm, psispec_paged_attention, psispec_qkv_append, psispec_w4_gated,
     psispec_w4_linear, psispec_w4_pack, rope_frequencies, w4_workspace_bytes)
 
 pytestmark = pytest.mark.gpu
@@ -162,6 +164,35 @@ def test_norm_zeros_and_extremes():
     assert (err <= (2.0 ** -4 + 2.0 ** -16) * y.abs() + 2.0 ** -10 * s + 448 * 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e18, 1e25, 3e37])
+@pytest.mark.parametrize("quant", [None, "row", "mx"])
+@pytest.mark.parametrize("dim", [512, 3104, 9024])
+def test_norm_of_numbers_whose_squares_32_bits_do_not_hold(scale, quant, dim):
+    g = _gen(3)
+    x = torch.zeros((5, dim), dtype=BF)
+    r = torch.randn((5, dim), generator=g).clamp(-4, 4)
+    r[[0, 1, 3, 4]] *= scale  # one ordinary row among them
+    y, h = ref.norm(x, None, r, 0.0)
+    out, ro, s = psispec_add_rmsnorm(_gpu(x), residual=_gpu(r), eps=0.0, quant=quant)
+    assert torch.equal(ro.cpu(), r)
+    s = 1.0 if s is None else s.cpu().double()[:, None] if quant == "row" else ref.powers(s.cpu()).repeat_interleave(32, 1)
+    step = ref.half_step(y / s, BF if quant is None else F8) * s
+    _within(out.cpu().double() * s, y, (2 * ref.NORM_REL * y.abs() + step) * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("dim,quant", [(8, None), (8, "row"), (32, "mx")])
+def test_norm_of_more_rows_than_a_launch_takes(dim, quant):
+    g = _gen(4)
+    some, many = 4096, (1 << 21) + 4096 + 3
+    x = torch.randn((some, dim), generator=g).to(BF).to(DEV)
+    r = torch.randn((some, dim), generator=g).to(DEV)
+    idx = torch.arange(many, device=DEV) % some
+    first = psispec_add_rmsnorm(x, residual=r.clone(), quant=quant)
+    for a, b in zip(psispec_add_rmsnorm(x[idx], residual=r[idx], quant=quant), first):
+        if b is not None:
+            assert torch.equal(a.view(torch.uint8), b[idx].view(torch.uint8))
+
+
 # ------------------------------------------------------------------------------------- products
 
 def _product(rows, n, k, dtype, fmt, group, seed, pad=0, bias=False, act=None, scale_dtype=BF, spread=4,
@@ -295,6 +326,12 @@ def test_nan_scales_and_bad_rows_stay_where_they_are(rows, n, dtype):
     assert torch.isnan(out[:, 7]).all()
     keep = [i for i in range(n) if i != 7]
     assert torch.equal(out[:, keep], clean[:, keep])
+    if xs is not None:  # a NaN among the rows' scales
+        e = xs.view(torch.uint8).clone()
+        e[2, 4] = 255
+        out = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32), x_scale=_gpu(e.view(E8)))
+        rest = [i for i in range(rows) if i != 2]
+        assert torch.isnan(out[2]).all() and torch.equal(out[rest], clean[rest])
     x2 = x.clone()
     x2[1, 10] = float("nan")
     out = psispec_w4_linear(_gpu(x2), psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32), x_scale=_gpu(xs))
@@ -338,6 +375,62 @@ def test_packing_takes_views():
     assert torch.equal(a.packed[:used], buf[:used]) and (buf[a.packed.numel():] == 9).all()
     x = torch.randn((4, k), generator=g).to(BF).to(DEV)
     assert torch.equal(psispec_w4_linear(x, a), psispec_w4_linear(x, b))
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Rows more than 2^31 elements from the first, and more sums of groups than one launch has threads for."""
+    g = _gen(31)
+    some, many, n, k = 128, (1 << 17) + 70, 40, 16512
+    codes, s = ref.make_weight(n, k, "int", 128, g)
+    w = psispec_w4_pack(_gpu(codes), _gpu(s))
+    x = _gpu(ref.make_rows(some, k, BF, g)[0])
+    idx = torch.arange(many, device=DEV) % some
+    y = psispec_w4_linear(x[idx], w)
+    want, bound = ref.linear(x.cpu(), None, codes, s, "int", 128, None, BF)
+    _within(y[-some:].roll(many % some, 0), want, bound)
+    assert torch.equal(y, y[:some][idx])
+
+
+def test_packed_bytes_again():
+    g = _gen(32)
+    codes, s = ref.make_weight(48, 160, "mx", 32, g)
+    w = psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32)
+    x = _gpu(ref.make_rows(3, 160, BF, g)[0])
+    assert torch.equal(psispec_w4_linear(x, W4Weight(w.packed.clone(), 48, 160, 32, "mx", E8)), psispec_w4_linear(x, w))
+    for bad in ((w.packed[:-1], 48, 160, 32, "mx", E8), (w.packed.cpu(), 48, 160, 32, "mx", E8),
+                (w.packed, 64, 320, 32, "mx", E8), (w.packed, 48, 160, 32, "mx", BF), (w.packed, 48, 160, 32, "int", E8),
+                (w.packed, 48, 150, 32, "mx", E8), (w.packed, 48, 160, 32, "nf4", BF), (w.packed.float(), 48, 160, 32, "mx", E8)):
+        with pytest.raises(PsispecError):
+            W4Weight(*bad)
+    with pytest.raises(AttributeError):
+        w.packed = w.packed.clone()
+
+
+def test_gated_far_from_zero():
+    """A gate of large negative and positive sums: what the activations leave is still right to the last bit but one."""
+    codes = torch.full((16, 16), 0x22, dtype=torch.uint8)  # w = 1 and 1: MX code 2
+    w = psispec_w4_pack(_gpu(codes), _gpu(torch.full((16, 1), 127, dtype=torch.uint8).view(E8)), "mx", 32)
+    a = torch.tensor([-60.0, -12.0, -9.0, -6.5, -5.0, -4.0, -2.0, -0.5, 0.0, 0.5, 5.0, 60.0, 3e4, -3e4, 1e30, -1e30])
+    x = torch.zeros((16, 32))
+    x[:, 0] = a
+    x = x.to(BF)
+    a = x[:, 0].double()
+    for act, f in ref.ACT.items():
+        y = psispec_w4_gated(_gpu(x), w, w, activation=act).cpu().double()[:, 0]
+        if act == "gelu":
+            want = a * torch.special.log_ndtr(a).exp()
+        else:
+            u = a if act == "silu" else 2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)
+            want = a * torch.where(u < -700, 0.0, torch.sigmoid(u))
+        want = want * a
+        # the exponent u is off by a few 2^-24 |u| in 32 bits, and the exponential by that much of itself; beyond
+        # 2^11 a negative side is 0
+        u = a.abs() if act == "silu" else (a * a / 2 if act == "gelu" else 2 * 0.8 * (a.abs() + 0.045 * a.abs() ** 3))
+        big = want.abs() > 2.0 ** 120
+        rel = 2.0 ** -8 + 2.0 ** -21 * (u.clamp(max=2048) + 8)
+        err = (y - want).abs()
+        assert (err[~big] <= (rel * want.abs() + 2.0 ** -126 * (1 + a.abs()))[~big]).all(), (act, y, want)
+        assert torch.isfinite(y[a < 0][:8]).all()
 
 
 def test_empty_and_batched_rows():

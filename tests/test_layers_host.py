@@ -117,6 +117,10 @@ def test_pack_checks(L):
     assert need >= 64 * 128 + 64 * 2 * 2 and pack(nbytes=need - 1) == -3
     for kw in (dict(codes=None), dict(sc=None), dict(cs=127), dict(ss=1), dict(sc=SC + 1), dict(codes=PK), dict(sc=PK)):
         assert pack(**kw) == -1, kw
+    # 2^26 - 3 tiles of 16 outputs x 128 inputs and more
+    big = dict(n=1 << 20, k=1 << 17)
+    assert pack(_weight(**big), cs=1 << 16, ss=1 << 10) == -1 and L.psispec_w4_packed_bytes(1 << 20, 1 << 17, 128, 0) == 0
+    assert L.psispec_w4_packed_bytes(1 << 20, (1 << 17) - 128, 128, 0) > 1 << 36
     for bad in ((0, 256, 128, 0), (64, 40, 32, 0), (64, 256, 96, 0), (64, 256, 128, 1), (64, 256, 32, 2)):
         assert L.psispec_w4_packed_bytes(*bad) == 0, bad
 
