@@ -88,6 +88,7 @@ struct ManyPlan {
   bool use;    // else the kernel for few rows takes it
   int nb;      // tiles of outputs of a wave, of all matrices
   int mblocks, nblocks, parts, mpad, npad;
+  int band;    // row blocks that follow each other before the next column
   int steps;   // tiles of 128 inputs of a part, an even number
   size_t part_at, bytes;
 };

@@ -17,6 +17,8 @@ ManyPlan many_plan(int rows, int n, int k, int mats) {
   p.mblocks = (rows + kRows - 1) / kRows;
   p.nblocks = (n + bn - 1) / bn;
   p.mpad = p.mblocks * kRows;
+  const int bands = p.mblocks < 12 ? 1 : (p.mblocks + 4) / 8;
+  p.band = (p.mblocks + bands - 1) / bands;
   p.npad = (n + 15) / 16 * 16;
   const int64_t blocks = (int64_t)p.mblocks * p.nblocks;
   const bool cut = blocks >= kCus * 3 / 8 && ktiles >= 64;
