@@ -6,11 +6,13 @@
 // straight from memory in the order of the matrix instructions and are decoded once per 64 rows.  What INT
 // products start from, -24 sum(x) per row and group, is formed by one pass over the rows before (k_w4_sums) and
 // travels with them: formed by the matrix cores here it would be a fifth of their work.  Loads run one step
-// ahead (two or three steps ahead, and 128 rows per workgroup, were no faster).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
-// 576 rows (device time): 12288 x 4096 INT 66 us (0.88 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 33 (1.7); two
-// such INT layers gated 125; 2048 rows, 4096 x 12288: 199, 163 (1.26), 86 (2.4); a library product of 16-bit
-// numbers takes 184 for the last.  INT is bound by the vector units beside the matrix cores (decoding, scales),
-// the others by the matrix cores and the traffic between the L2 and the CUs.
+// ahead (two steps, 576 rows, 12288 x 4096: 8-bit rows 37 us instead of 35, MX 59 and 59; 128 rows per workgroup
+// were no faster either).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
+// Device time: 576 rows, 12288 x 4096: INT 66 us (0.88 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 32 (1.8); two
+// such INT layers gated 126; 2048 rows, 4096 x 12288: 197 (1.05), 167 (1.23), 87 (2.4); a library product of 16-bit
+// numbers takes 184 for the last.  INT is bound by the vector units beside the matrix cores (decoding, scales: four
+// instructions of theirs per matrix instruction, which keeps them as long as it takes itself), MX by the matrix
+// cores (half of their cycles) and LDS, 8-bit rows by LDS, from which each wave reads all 64 rows.
 #pragma once
 
 #include "w4.h"

@@ -90,8 +90,8 @@ def _norm_case(rows, dim, dtype, residual, quant, pad, seed, weighted=True, eps=
     _within(o.float() * s.to(DEV, F32), y, (rel * 2 + s * ref.half_step(y / s.clamp(min=1e-300), F8)) * (1 + 2.0 ** -8))
 
 
-@pytest.mark.parametrize("dim", [1, 7, 8, 31, 32, 64, 100, 500, 512, 520, 1000, 2048, 2056, 4096, 4104, 5120, 8192,
-                                 8200, 16384, 32768])
+@pytest.mark.parametrize("dim", [1, 7, 8, 31, 32, 64, 100, 500, 512, 520, 1000, 1024, 1032, 2048, 2056, 4096,
+                                 4104, 5120, 8192, 8200, 16384, 16392, 32768])
 @pytest.mark.parametrize("quant", [None, "row", "mx"])
 def test_norm_dims(dim, quant):
     if quant == "mx":
