@@ -254,9 +254,10 @@ void launch_kind(const AddNormArgs& a, int vec, hipStream_t stream) {
                      stream, s, vec);
     }
   };
-  // As few threads per row as hold it in 8 or 16 elements each (a wave waits for no other), in us, rows x dim: 8000 x 512 64 threads 7.6, 256 14.9; 8000 x 1024 64 threads 10.7, 256 18.1 (one row 3.5,
-  // 3.2); 8000 x 4096 256 threads 36.2, 512 40.5 (576 rows 5.8, 6.3; one row 3.9, 3.7); 8000 x 8192 512 threads 89.4,
-  // 1024 95.2; 4000 x 16384 1024 threads of 16 elements 88, of up to 32 120.
+  // As few threads per row as hold it in 8 or 16 elements each (a wave waits for no other).  In us, rows x dim:
+  // 8000 x 512 64 threads 7.6, 256 14.9; 8000 x 1024 64 threads 10.7, 256 18.1 (one row 3.5, 3.2); 8000 x 4096 256
+  // threads 36.2, 512 40.5 (576 rows 5.8, 6.3; one row 3.9, 3.7); 8000 x 8192 512 threads 89.4, 1024 95.2;
+  // 4000 x 16384 1024 threads of 16 elements 88, of up to 32 120.
   if (a.dim <= 512)
     go((k_add_rmsnorm<T, R, KIND, 64, 1>), 4, 256);
   else if (a.dim <= 1024)
