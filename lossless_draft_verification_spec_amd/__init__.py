@@ -1072,7 +1072,10 @@ def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
             scale = torch.empty(sshape, dtype=st, device=x.device)
         if scale.dtype != st or (scode == PSISPEC_F32 and not scale.is_contiguous()):
             raise PsispecError(f"scale must be {st} {list(sshape)}, contiguous for one number per row")
-        sp, ss = _rows_of(scale, sshape, idx, "scale") if sshape else (scale.data_ptr(), 0)
+        if sshape:
+            sp, ss = _rows_of(scale, sshape, idx, "scale")
+        else:  # one row of its own: one number
+            sp, _ = _rows_of(scale.view(1) if scale.numel() == 1 else scale, (1,), idx, "scale")
     if out is None:
         out = torch.empty(shape, dtype=dt, device=x.device)
     elif out.dtype != dt:

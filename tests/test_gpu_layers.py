@@ -137,6 +137,17 @@ def test_norm_in_place_and_defaults():
     assert q.shape == (3, 3, 192) and s.shape == (3, 3, 6) and s.dtype == E8
 
 
+def test_norm_of_a_single_row():
+    x = torch.randn(96, generator=_gen(5)).to(BF).to(DEV)
+    y, _, s = psispec_add_rmsnorm(x, quant="row")
+    y2, _, s2 = psispec_add_rmsnorm(x[None], quant="row")
+    assert s.shape == () and s == s2[0] and torch.equal(y.view(torch.uint8), y2[0].view(torch.uint8))
+    assert psispec_add_rmsnorm(x, quant="mx")[2].shape == (3,)
+    for bad in (torch.zeros(()), torch.zeros(2, device=DEV), torch.zeros(0, device=DEV)):
+        with pytest.raises(PsispecError):
+            psispec_add_rmsnorm(x, quant="row", scale=bad)
+
+
 def test_norm_zeros_and_extremes():
     x = torch.zeros((4, 128), dtype=BF)
     x[1, 3] = float("inf")
@@ -505,6 +516,29 @@ def test_layer_in_a_graph(fmt, rows, h, f):
         torch.cuda.synchronize()
         replayed, kept = y.clone(), ro.clone()
         assert torch.equal(replayed, layer()) and torch.equal(kept, ro)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured apart, replayed in turn on one stream with eager calls of the same workspace between them."""
+    g = _gen(14)
+    n, k = 4096, 8192
+    w = psispec_w4_pack(*map(_gpu, ref.make_weight(n, k, "int", 128, g)))
+    xs = [torch.zeros((r, k), dtype=BF, device=DEV) for r in (500, 440)]  # inputs in parts
+    ws = torch.empty(max(w4_workspace_bytes(x.shape[0], n, k) for x in xs), dtype=torch.uint8, device=DEV)
+    outs = [psispec_w4_linear(x, w, workspace=ws) for x in xs]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in xs]
+    for x, o, gr in zip(xs, outs, graphs):
+        with torch.cuda.graph(gr):
+            psispec_w4_linear(x, w, out=o, workspace=ws)
+    for i in range(4):
+        for x in xs:
+            x.copy_(_gpu(torch.randn(x.shape, generator=g).to(BF)))
+        for gr in graphs:
+            gr.replay()
+        got = [o.clone() for o in outs]
+        want = [psispec_w4_linear(x, w, workspace=ws) for x in xs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
 
 
 def test_a_whole_layer_of_a_verify_forward():
