@@ -578,6 +578,7 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *   8-bit rows            go through the scaled matrix instruction, at twice the 16-bit rate: among eight
  *                         neighbouring inputs each product is cut to a multiple of 2^-13 of the power of two
  *                         that the largest of them reaches
+ * (INT weights: 31 times the sum of |x| over a group has to stay within 32 bits.)
  * An infinity or a NaN in a row, its scale or an output's scale gives infinities or NaN in that row, that
  * output, and nowhere else.
  *   x        rows of k elements, x_stride elements apart, 16-byte aligned, strides of 16-byte multiples up to 2^24

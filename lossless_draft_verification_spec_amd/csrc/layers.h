@@ -23,7 +23,8 @@ hipError_t launch_add_rmsnorm(const AddNormArgs& a, psispec_dtype dtype, hipStre
 // Packed weights of 4 bits (w4_pack.hip).  Tiles of 16 outputs x 128 inputs; outputs and inputs behind
 // the last have code 0 and scale 0.  Lane l of a wave (output l % 16, g = l / 16) owns the 16 bytes at
 // 16 l of a tile, and word j of them holds its inputs
-//   PSISPEC_W4_INT  32 j + 8 g + 0..7: nibble s, s + 4 = inputs 2s, 2s + 1 of the eight, code + 8
+//   PSISPEC_W4_INT  32 j + 8 g + 0..7: nibble s, s + 4 = inputs 2s, 2s + 1 of the eight, code + 8; the word
+//                   turned left by 3 bits
 //   PSISPEC_W4_MX   32 g + 8 j + 0..7: nibble s = input s, the code as it is
 // so word j is the lane's part of the j-th 16x16x32 matrix instruction of the tile (and the 16 bytes,
 // for MX, its part of the 16x16x128 one).  Scales: INT [tile][groups per tile][16 outputs] in 16 bits,

@@ -28,7 +28,8 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4PackArgs a, W4Layout l) {
       else
         v |= ((b & 15) << (4 * s)) | ((b >> 4) << (16 + 4 * s));
     }
-    w[j] = mx ? v : v ^ 0x88888888u;
+    v ^= mx ? 0u : 0x88888888u;
+    w[j] = mx ? v : v << 3 | v >> 29;
   }
   *reinterpret_cast<u32x4*>(a.packed + tile * 1024 + lane * 16) = u32x4{w[0], w[1], w[2], w[3]};
   if (mx) {
