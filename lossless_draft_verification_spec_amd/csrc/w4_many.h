@@ -8,11 +8,12 @@
 // travels with them: formed by the matrix cores here it would be a fifth of their work.  Loads run one step
 // ahead (two steps, 576 rows, 12288 x 4096: 8-bit rows 37 us instead of 35, MX 59 and 59; 128 rows per workgroup
 // were no faster either).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
-// Device time: 576 rows, 12288 x 4096: INT 66 us (0.88 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 32 (1.8); two
-// such INT layers gated 126; 2048 rows, 4096 x 12288: 197 (1.05), 167 (1.23), 87 (2.4); a library product of 16-bit
+// Device time: 576 rows, 12288 x 4096: INT 65 us (0.89 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 32 (1.8); two
+// such INT layers gated 122; 2048 rows, 4096 x 12288: 187 (1.10), 167 (1.23), 87 (2.4); a library product of 16-bit
 // numbers takes 184 for the last.  INT is bound by the vector units beside the matrix cores (decoding, scales: four
-// instructions of theirs per matrix instruction, which keeps them as long as it takes itself), MX by the matrix
-// cores (half of their cycles) and LDS, 8-bit rows by LDS, from which each wave reads all 64 rows.
+// instructions of theirs per matrix instruction, which keeps them as long as it takes itself; their order within a
+// tile made no difference), MX by the matrix cores (half of their cycles) and LDS, 8-bit rows by LDS, from which
+// each wave reads all 64 rows.
 #pragma once
 
 #include "w4.h"
