@@ -244,9 +244,12 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
 // workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 12288 x 4096, 64 rows: 64 x 64 (192) 15.4,
 // 32 x 32 (768) 15.8.  Eight waves share a tile's inputs, four where several workgroups share a CU (64 rows x 32
 // outputs at 16384 x 4096: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
+// Sixteen rows or fewer: 32 outputs unless that leaves one and a half workgroups per CU (9 rows, 2 x 12288 x 4096
+// gated, 384 of them: 13.4 against 11.8 with 16 outputs; 2 x 8192 and 2 x 24576, 256 and 768: 9.7, 22.5 against 9.9, 27.0).
 template <typename X, int GPT, bool SF16, int MATS>
 hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
   constexpr int kFill = 192, kShare = 320, kLong = 64;  // workgroups, workgroups, tiles of 128 inputs
+  constexpr int kOne = 256, kTwo = 448;                 // workgroups: one, nearly two per CU
   constexpr int kWide = MATS == 2 ? 2 : 4;
   const auto blocks = [&](int r4, int nt) {
     return (int64_t)((a.ntiles + nt - 1) / nt) * ((a.rows + 4 * r4 - 1) / (4 * r4));
@@ -273,9 +276,10 @@ hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
     else
       go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 8>), 8, 2, 8);
   } else if (a.rows > 4) {
-    if (blocks(4, 2) >= kFill)
+    const int64_t b = blocks(4, 2);
+    if ((b >= kFill && b <= kOne) || b >= kTwo)
       go((k_w4_few<X, GPT, SF16, 4, 2, MATS, 8>), 4, 2, 8);
-    else if (a.ktiles >= kLong)
+    else if (a.ktiles >= kLong && b < kFill)
       go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 16>), 4, 1, 16);
     else
       go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 8>), 4, 1, 8);
