@@ -523,7 +523,7 @@ psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* tab
  *   rows 0..2^24-1 (0 launches nothing);  dim 1..32768, a multiple of 32 with E8M0 scales
  *   out           rows of out_dtype: dtype or PSISPEC_F8E4M3
  *   scale         with F8E4M3 only (NULL otherwise): [rows] f32, or rows of dim / 32 bytes, scale_stride apart
- * Rows may start anywhere (those 16-byte aligned are read and written 16 bytes at a time).  residual_out and
+ * Rows may start anywhere.  residual_out and
  * out may each be the rows of x or of residual themselves; every other overlap of an output with an input or
  * another output is refused (PSISPEC_EINVAL).  Asynchronous on `stream`; no workspace.
  */

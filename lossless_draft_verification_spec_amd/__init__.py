@@ -980,6 +980,8 @@ def _rows_of(t: torch.Tensor, shape, idx: int, name: str):
     if t.is_contiguous():
         return t.data_ptr(), width
     st = t.stride()
+    if len(st) == 2 and st[1] == 1 and st[0] >= width:
+        return t.data_ptr(), st[0]
     if width > 1 and st[-1] != 1:
         raise PsispecError(f"the rows of {name} must be contiguous")
     rows, step = 1, width

@@ -17,19 +17,20 @@
 namespace psispec {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+// Rows may start anywhere: vectors of their elements' alignment, which global memory takes as they are (8000 rows of
+// 4096, every second one off 16 bytes: 62 us, element by element 149; all of them on 16 bytes 53)
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8), aligned(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2), aligned(1)));
 template <typename T> struct Vec8;
 template <> struct Vec8<__bf16> { typedef bf16x8 type; };
 template <> struct Vec8<_Float16> { typedef f16x8 type; };
 
-// 8 elements of a row from column c on; those from dim on are 0.  vec: the row's chunks are 16-byte
-// aligned.
+// 8 elements of a row from column c on; those from dim on are 0.
 template <typename T>
-__device__ inline void load8(const T* row, int c, int dim, bool vec, float* v) {
-  if (vec && c + 8 <= dim) {
+__device__ inline void load8(const T* row, int c, int dim, float* v) {
+  if (c + 8 <= dim) {
     if constexpr (sizeof(T) == 4) {
       const f32x4 a = *reinterpret_cast<const f32x4*>(row + c), b = *reinterpret_cast<const f32x4*>(row + c + 4);
 #pragma unroll
@@ -46,8 +47,8 @@ __device__ inline void load8(const T* row, int c, int dim, bool vec, float* v) {
 }
 
 template <typename T>
-__device__ inline void store8(T* row, int c, int dim, bool vec, const float* v) {
-  if (vec && c + 8 <= dim) {
+__device__ inline void store8(T* row, int c, int dim, const float* v) {
+  if (c + 8 <= dim) {
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<f32x4*>(row + c) = f32x4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4*>(row + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
@@ -104,12 +105,10 @@ __device__ inline uint32_t row_max(uint32_t v, uint32_t* lds) {
   return m;
 }
 
-enum : int { kVecX = 1, kVecR = 2, kVecRo = 4, kVecW = 8, kVecO = 16 };
-
 // T: x, weight and 16-bit out; R: residual; KIND: NormOut; TPR threads per row, each with up to CPT
 // chunks of 8.
 template <typename T, typename R, int KIND, int TPR, int CPT>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormArgs a, int vec) {
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormArgs a) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
   __shared__ float s_sum[TPR / 64];
   __shared__ double s_wide[TPR / 64];
@@ -128,9 +127,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
     const int c = 8 * (u + i * TPR);
     if (c < a.dim) {
       float r[8] = {};
-      load8(x, c, a.dim, vec & kVecX, h[i]);
-      if (res) load8(res, c, a.dim, vec & kVecR, r);
-      if (wt) load8(wt, c, a.dim, vec & kVecW, w[i]);
+      load8(x, c, a.dim, h[i]);
+      if (res) load8(res, c, a.dim, r);
+      if (wt) load8(wt, c, a.dim, w[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         h[i][e] += r[e];
@@ -142,7 +141,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = 8 * (u + i * TPR);
-      if (c < a.dim) store8(ro, c, a.dim, vec & kVecRo, h[i]);
+      if (c < a.dim) store8(ro, c, a.dim, h[i]);
     }
   }
   // 1 / sqrt(...) = pre * inv.  From 2^-80 on the squares that 32 bits lose are less than 2^-31 of the sum.
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = 8 * (u + i * TPR);
-      if (c < a.dim) store8(out, c, a.dim, vec & kVecO, h[i]);
+      if (c < a.dim) store8(out, c, a.dim, h[i]);
     }
   } else {
     uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
@@ -222,7 +221,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
       }
       if (c < a.dim) {
         const u32x2 q = pack8_e4m3(h[i]);
-        if ((vec & kVecO) && c + 8 <= a.dim) {
+        if (c + 8 <= a.dim) {
           *reinterpret_cast<u32x2*>(out + c) = q;
         } else {
 #pragma unroll
@@ -235,7 +234,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
 }
 
 template <typename T, typename R, int KIND>
-void launch_kind(const AddNormArgs& a, int vec, hipStream_t stream) {
+void launch_kind(const AddNormArgs& a, hipStream_t stream) {
   // a launch takes less than 2^32 threads
   const auto go = [&](auto kernel, int per_block, int threads) {
     constexpr int kSlice = 1 << 21;
@@ -251,7 +250,7 @@ void launch_kind(const AddNormArgs& a, int vec, hipStream_t stream) {
       s.scale = KIND == kNormMx ? on(a.scale, a.scale_stride, 1) : on(a.scale, 1, 4);
       s.rows = a.rows - at < kSlice ? a.rows - at : kSlice;
       PSISPEC_LAUNCH("add_rmsnorm", kernel, dim3((unsigned)((s.rows + per_block - 1) / per_block)), dim3(threads), 0,
-                     stream, s, vec);
+                     stream, s);
     }
   };
   // As few threads per row as hold it in 8 or 16 elements each (a wave waits for no other).  In us, rows x dim:
@@ -275,36 +274,28 @@ void launch_kind(const AddNormArgs& a, int vec, hipStream_t stream) {
 }
 
 template <typename T, typename R>
-void launch_types(const AddNormArgs& a, int vec, hipStream_t stream) {
+void launch_types(const AddNormArgs& a, hipStream_t stream) {
   if (a.kind == kNormSame)
-    launch_kind<T, R, kNormSame>(a, vec, stream);
+    launch_kind<T, R, kNormSame>(a, stream);
   else if (a.kind == kNormRow)
-    launch_kind<T, R, kNormRow>(a, vec, stream);
+    launch_kind<T, R, kNormRow>(a, stream);
   else
-    launch_kind<T, R, kNormMx>(a, vec, stream);
+    launch_kind<T, R, kNormMx>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const AddNormArgs& a, psispec_dtype dtype, hipStream_t stream) {
-  const auto ok = [&](const void* p, int64_t stride, int es, int align) {
-    return (uintptr_t)p % align == 0 && (a.rows == 1 || stride * es % align == 0);
-  };
-  const int rs = a.residual_f32 ? 4 : 2;
-  const int vec = (ok(a.x, a.x_stride, 2, 16) ? kVecX : 0) | (ok(a.residual, a.residual_stride, rs, 16) ? kVecR : 0) |
-                  (ok(a.residual_out, a.residual_out_stride, rs, 16) ? kVecRo : 0) |
-                  (ok(a.weight, 0, 2, 16) ? kVecW : 0) |
-                  (ok(a.out, a.out_stride, a.kind ? 1 : 2, a.kind ? 8 : 16) ? kVecO : 0);
   if (dtype == PSISPEC_BF16) {
     if (a.residual_f32)
-      launch_types<__bf16, float>(a, vec, stream);
+      launch_types<__bf16, float>(a, stream);
     else
-      launch_types<__bf16, __bf16>(a, vec, stream);
+      launch_types<__bf16, __bf16>(a, stream);
   } else {
     if (a.residual_f32)
-      launch_types<_Float16, float>(a, vec, stream);
+      launch_types<_Float16, float>(a, stream);
     else
-      launch_types<_Float16, _Float16>(a, vec, stream);
+      launch_types<_Float16, _Float16>(a, stream);
   }
   return hipGetLastError();
 }

@@ -244,8 +244,9 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
 // workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 12288 x 4096, 64 rows: 64 x 64 (192) 15.4,
 // 32 x 32 (768) 15.8.  Eight waves share a tile's inputs, four where several workgroups share a CU (64 rows x 32
 // outputs at 16384 x 4096: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
-// Sixteen rows or fewer: 32 outputs unless that leaves one and a half workgroups per CU (9 rows, 2 x 12288 x 4096
-// gated, 384 of them: 13.4 against 11.8 with 16 outputs; 2 x 8192 and 2 x 24576, 256 and 768: 9.7, 22.5 against 9.9, 27.0).
+// Little more than one workgroup per CU costs as much as two: 639 rows, 2 x 208 x 9856 gated with 16 rows x 32 outputs
+// (280 workgroups) 27.0, 32 x 32 (140) 21.1; 9 rows, 2 x 12288 x 4096 with 32 outputs (384) 13.4, 16 (768) 11.8, but
+// 2 x 8192 and 2 x 24576 (256 and 768) 9.7 and 22.5 against 9.9 and 27.0.
 template <typename X, int GPT, bool SF16, int MATS>
 hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
   constexpr int kFill = 192, kShare = 320, kLong = 64;  // workgroups, workgroups, tiles of 128 inputs
@@ -270,7 +271,7 @@ hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
       else
         go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 8>), 8, 4, 8);
     }
-  } else if (a.rows > 16 && blocks(8, 2) >= kFill) {
+  } else if (a.rows > 16 && (blocks(8, 2) >= kFill || blocks(4, 2) > kOne)) {
     if (blocks(8, 2) >= kShare)
       go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 4>), 8, 2, 4);
     else
