@@ -572,9 +572,11 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *                      or a (1 + erf(a / sqrt 2)) / 2                                 (PSISPEC_W4_GELU)
  *                      or a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2           (PSISPEC_W4_GELU_TANH)
  * Codes and rows enter the matrix cores as they are, the sums are of 32 bits, INT scales are applied to the
- * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  Two exceptions:
+ * sums of their groups in 32 bits, and out is rounded once: no weight is rounded.  Three exceptions:
  *   F16 rows, MX weights  exact for scales down to 2^-36 of the output's largest; smaller ones give weights off
  *                         by at most 2^-38 of that largest scale
+ *   BF16 rows, MX weights an output whose largest scale is 2^126 takes 2^-127 as 2^-126, one with 2^127 takes
+ *                         both as 2^-125
  *   8-bit rows            go through the scaled matrix instruction, at twice the 16-bit rate: among eight
  *                         neighbouring inputs each product is cut to a multiple of 2^-13 of the power of two
  *                         that the largest of them reaches

@@ -10,7 +10,9 @@
 // -24 sum(x), which the matrix cores form as one more product with a constant, shared by all outputs;
 // the group's sum, exact products in 32 bits, is multiplied by its scale in 32 bits.  So no weight is
 // rounded; what the detour adds is the rounding of 32-bit sums of up to 31 |x| instead of 8 |x|.
-// MX codes are converted with their scale (a power of two: exact in BF16, whose exponents reach as far).
+// MX codes are converted with their scale (a power of two: exact in BF16, whose exponents reach as far but for the
+// largest codes times 2^126 or 2^127: an output with such a scale takes all of its own one or two powers lower, the
+// lowest as they are, and its sum is scaled back).
 // F16 rows take them relative to the largest scale of the output, times 2^13 (the largest is then 6 2^13):
 // exact down to 2^-36 of that scale, below it off by at most 2^-38 of it; the sum is scaled back once.
 #pragma once
@@ -93,15 +95,27 @@ __device__ inline u32x4 mx_codes(uint32_t w, float scale, _Float16) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3))};
 }
-// The scale under which a block's codes enter: byte e of the block, byte `top` of the output
-__device__ inline float mx_scale(int e, int top, __bf16) { return __uint_as_float((uint32_t)e << 23); }
+// The scale under which a block's codes enter: byte e of the block, the largest byte `top` of the output.
+// BF16: 252 at most, so that 6 times it is a number; two saturating subtractions
+__device__ inline uint32_t mx_over(int top) { return __builtin_elementwise_sub_sat((uint32_t)top, 252u); }
+__device__ inline float mx_scale(int e, int top, __bf16) {
+  return __uint_as_float(__builtin_elementwise_sub_sat((uint32_t)e, mx_over(top)) << 23);
+}
 __device__ inline float mx_scale(int e, int top, _Float16) {
   return __uint_as_float((uint32_t)max(e - top + 140, 0) << 23);
 }
 // what the sum is multiplied by in the end
-__device__ inline float mx_back(float acc, int top, __bf16) { return acc; }
+__device__ inline float mx_back(float acc, int top, __bf16) {
+  return top == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(acc, (int)mx_over(top));
+}
 __device__ inline float mx_back(float acc, int top, _Float16) {
   return top == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(acc, top - 140);
+}
+// the same for a BF16 lane's sums of outputs 4 g + 0..3; lane l holds the byte of output l % 16
+__device__ inline void mx_back4(f32x4& acc, int top) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = mx_back(acc[i], __shfl(top, 4 * g + i, 64), __bf16());
 }
 
 __device__ inline float scale16(uint32_t bits, bool f16) {

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
     codes[b] = a.codes[b / NT] + (int64_t)nt * a.ktiles * 1024;
     scales[b] = static_cast<const uint8_t*>(a.scales[b / NT]) +
                 (kMx ? mx_scale_at(nt, 0, a.ktiles) : (int64_t)nt * a.ktiles * (32 * GPT));
-    top[b] = kMx && __is_same(X, _Float16) ? a.top[b / NT][nt * 16 + c] : 0;
+    top[b] = 0;
   }
   const uint32_t lane16 = lane * 16;
   uint8_t* const mine = s_mem + wave * kStage;
@@ -103,6 +103,10 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
       }
     }
     if constexpr (kF8) q.xs = row_scales(xsrow, 8 * st, a.k / 32);  // lane = row: a load per row and step
+    if (kMx && !kF8 && st == wave) {  // once, behind the first loads (before them: 9 rows, 4096 x 12288 7.7 us instead of 7.4)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) top[b] = a.top[b / NT][min(nt0 + b % NT, a.ntiles - 1) * 16 + c];
+    }
   };
 
   f32x4 acc[MT][NB];
@@ -212,6 +216,14 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  if constexpr (kMx && __is_same(X, __bf16)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (__any(top[b] > 252)) {  // the same way for the whole wave
+#pragma unroll
+        for (int m = 0; m < MT; ++m) mx_back4(acc[m][b], top[b]);
+      }
+  }
   f32x4(*s_acc)[64] = reinterpret_cast<f32x4(*)[64]>(s_mem);
   __syncthreads();
 #pragma unroll

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
   int top[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
-    top[b] = kMx && __is_same(X, _Float16) ? a.top[b / NT][min(nt0 + b % NT, a.ntiles - 1) * 16 + c] : 0;
+    top[b] = kMx && !kF8 ? a.top[b / NT][min(nt0 + b % NT, a.ntiles - 1) * 16 + c] : 0;
   const auto load_w = [&](Codes& q, int st) {
 #pragma unroll
     for (int h = 0; h < TPS; ++h) {
@@ -228,7 +228,12 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
     } else if constexpr (kMx) {
       float s[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) s[b] = mx_scale((int)q.e[b], top[b], X());
+      for (int b = 0; b < NB; ++b) {
+#ifdef __HIP_DEVICE_COMPILE__
+        asm volatile("" : "+v"(top[b]));  // looked at here: before the loop it would be waited for
+#endif
+        s[b] = mx_scale((int)q.e[b], top[b], X());
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         u32x4 x[MT];
@@ -311,6 +316,14 @@ __global__ __launch_bounds__(256, 2) void k_w4_many(ManyArgs m) {
     }
   }
 
+  if constexpr (kMx && __is_same(X, __bf16)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (__any(top[b] > 252)) {  // the same way for the whole wave
+#pragma unroll
+        for (int i = 0; i < MT; ++i) mx_back4(acc[i][b], top[b]);
+      }
+  }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
     const int n = (nt0 + b) * 16 + 4 * g;

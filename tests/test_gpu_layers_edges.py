@@ -1,0 +1,95 @@
+"""The layers around the paged attention at the ends of their ranges, against the 64-bit references."""
+import pytest
+import torch
+
+import layers_ref as ref
+from layers_ref import BF, E8, F8, FH
+from lossless_draft_verification_spec_amd import psispec_w4_gated, psispec_w4_linear, psispec_w4_pack
+from test_gpu_layers import DEV, _gen, _gpu, _within
+
+pytestmark = pytest.mark.gpu
+
+
+# few rows, few rows of several tiles, many rows, many rows whose inputs are cut
+MX_SIZES = [(3, 40, 448), (50, 40, 448), (1601, 2039, 448), (801, 2033, 8224)]
+
+
+def _bytes_per_block(k, n, seed, lowest):
+    """MX codes and scale bytes over the whole range: a byte per block of 32 inputs, in turn, and a little lower in
+    every other output."""
+    g = _gen(seed)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g).to(torch.uint8)
+    ends = torch.tensor([254, 253, 252, 251, 200, 127, 60, 5, 4, lowest])
+    base = ends[torch.arange(k // 32) % len(ends)]
+    e = base.repeat(n, 1)
+    e[1::2] = (e[1::2] - 3).clamp(min=lowest)  # 251 at most: nothing beyond BF16
+    return codes, e.to(torch.uint8).view(E8), base, g
+
+
+@pytest.mark.parametrize("rows,n,k", MX_SIZES)
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_bf16_rows_take_every_mx_scale(rows, n, k, act):
+    """Scales from 2^-125 to 2^127 in one output; 6 * 2^127 is beyond BF16, the sums are not."""
+    codes, s, base, g = _bytes_per_block(k, n, rows, 2)
+    x = torch.randn((rows, k), generator=g) * torch.exp2((127.0 - base).clamp(-124, 124)).repeat_interleave(32)
+    x = x.to(BF)
+    w = psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32)
+    if act is None:
+        want, bound = ref.linear(x, None, codes, s, "mx", 32, None, BF)
+        _within(psispec_w4_linear(_gpu(x), w), want, bound)
+        return
+    plain = ref.make_weight(n, k, "mx", 32, g)
+    plain[1].view(torch.uint8).sub_(120)  # the other matrix lower, so that its sums stay in range
+    p = psispec_w4_pack(*map(_gpu, plain), "mx", 32)
+    for mats, packed in (((codes, s), plain), (w, p)), ((plain, (codes, s)), (p, w)):
+        want, bound = ref.gated(x, None, *mats, "mx", 32, act, BF)
+        _within(psispec_w4_gated(_gpu(x), *packed, activation=act), want, bound)
+
+
+@pytest.mark.parametrize("rows,n", [(3, 40), (50, 40), (1601, 2039)])
+@pytest.mark.parametrize("dtype", [BF, FH, F8])
+@pytest.mark.parametrize("e", [0, 1, 2, 126, 252, 253, 254])
+def test_mx_scales_at_both_ends(rows, n, dtype, e):
+    """One scale for a whole layer, rows whose products with it stay in range: each code comes out exactly."""
+    codes = torch.zeros((n, 32), dtype=torch.uint8)
+    codes[:, 0] = torch.arange(n) % 16
+    s = torch.full((n, 2), e, dtype=torch.uint8).view(E8)
+    x, xs = torch.zeros((rows, 64)), None
+    if dtype == F8:
+        x[:, 0], xs = 1.0, torch.full((rows, 2), 254 - e, dtype=torch.uint8).view(E8)
+    else:
+        p = 127 - e
+        x[:, 0] = 2.0 ** (max(-14, min(15, p)) if dtype == FH else max(-124, min(124, p)))
+    x = x.to(dtype)
+    want = (ref.rows_of(x, xs) @ ref.weights(codes, s, "mx", 32)[0].t()).to(BF if dtype == F8 else dtype)
+    y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32), x_scale=_gpu(xs))
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("rows,n", [(3, 40), (50, 40), (1601, 2039)])
+def test_bf16_rows_under_the_largest_mx_scales(rows, n):
+    """An output whose largest scale is 2^127 takes 2^-127 and 2^-126 as 2^-125, one with 2^126 takes 2^-127 as 2^-126;
+    others have them as they are."""
+    codes = torch.full((n, 32), 0x22, dtype=torch.uint8)  # 1 and 1
+    s = torch.zeros((n, 2), dtype=torch.uint8)
+    s[0::3, 1], s[1::3, 1], s[2::3, 1] = 254, 253, 252
+    x = torch.zeros((rows, 64))
+    x[:, 0] = 2.0 ** 120  # the block of byte 0 alone
+    x = x.to(BF)
+    y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(codes), _gpu(s.view(E8)), "mx", 32)).cpu()
+    assert (y[:, 0::3] == 2.0 ** -5).all() and (y[:, 1::3] == 2.0 ** -6).all() and (y[:, 2::3] == 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("rows,n", [(3, 40), (50, 40), (1601, 2039)])
+def test_bf16_rows_below_the_smallest_normal_number(rows, n):
+    codes = torch.full((n, 16), 0x22, dtype=torch.uint8)
+    x = torch.zeros((rows, 32))
+    x[:, 0] = torch.tensor([2.0 ** -127, 3 * 2.0 ** -133, 2.0 ** -133])[torch.arange(rows) % 3]
+    x = x.to(BF)
+    for e in (127, 128, 200, 254):
+        s = torch.full((n, 1), e, dtype=torch.uint8).view(E8)
+        y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32)).cpu()
+        assert torch.equal(y, (x[:, :1].double() * 2.0 ** (e - 127)).to(BF).expand(rows, n)), e
+    s = torch.ones((n, 1), dtype=BF)
+    y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(torch.full_like(codes, 0x33)), _gpu(s), "int", 32)).cpu()
+    assert torch.equal(y.double(), 3 * x[:, :1].double().expand(rows, n))
