@@ -143,11 +143,13 @@ __device__ inline f32x4 mfma_mx(u32x4 w, int ws, u32x4 x0, u32x4 x1, int xs, f32
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, WS, ws, 0, xs);
 }
 
-// 1 + erf(z) = erfc(-z) and 1 + tanh(u) = 2 / (1 + exp(-2 u)): without the loss of digits on the negative side
+// 1 + erf(z) = erfc(-z) and 1 + tanh(u) = 2 / (1 + exp(-2 u)): without the loss of digits on the negative side, and
+// by exp(-|u|), which does not overflow where x exp(u) is still a number (u to -91)
 __device__ inline float activate(float x, int act) {
   if (act == PSISPEC_W4_GELU) return 0.5f * x * erfcf(-0.70710678118654752440f * x);
   const float u = act == PSISPEC_W4_SILU ? x : 1.59576912160573071176f * (x + 0.044715f * x * x * x);  // 2 sqrt(2 / pi)
-  return x / (1.0f + expf(-u));
+  const float t = expf(-fabsf(u));
+  return (u < 0.0f ? x * t : x) / (1.0f + t);
 }
 
 // The scales of the lane's outputs 4 g + 0..3, four numbers of 16 bits

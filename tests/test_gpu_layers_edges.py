@@ -1,4 +1,6 @@
 """The layers around the paged attention at the ends of their ranges, against the 64-bit references."""
+import math
+
 import pytest
 import torch
 
@@ -93,3 +95,32 @@ def test_bf16_rows_below_the_smallest_normal_number(rows, n):
     s = torch.ones((n, 1), dtype=BF)
     y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(torch.full_like(codes, 0x33)), _gpu(s), "int", 32)).cpu()
     assert torch.equal(y.double(), 3 * x[:, :1].double().expand(rows, n))
+
+
+@pytest.mark.parametrize("rows", [1, 40, 1601])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gated_where_the_activation_is_tiny(act, rows):
+    """Activations down to the smallest normal numbers of 32 bits, against a large second sum."""
+    n = 2039 if rows > 1000 else 40
+    gate, up = torch.zeros((n, 16), dtype=torch.uint8), torch.zeros((n, 16), dtype=torch.uint8)
+    gate[:, 0], up[:, 0] = 0x02, 0x20  # 1 times input 0, 1 times input 1
+    s = torch.full((n, 1), 127, dtype=torch.uint8).view(E8)
+    w = [psispec_w4_pack(_gpu(c), _gpu(s), "mx", 32) for c in (gate, up)]
+    a = {"silu": torch.arange(-91.0, -79.0, 0.5), "gelu": torch.arange(-13.0, -10.0, 0.0625),
+         "gelu_tanh": torch.arange(-10.0, -8.0, 0.0625)}[act]
+    for part in a.split(rows):
+        x = torch.zeros((rows, 32))
+        x[:len(part), 0], x[:, 1] = part, 2.0 ** 100
+        x = x.to(BF)
+        y = psispec_w4_gated(_gpu(x), *w, activation=act)[:len(part)].cpu().double()
+        p = x[:len(part), 0].double()
+        if act == "gelu":
+            f, u = p * torch.special.log_ndtr(p).exp(), p * p / 2
+        else:
+            u = p if act == "silu" else 2 * math.sqrt(2 / math.pi) * (p + 0.044715 * p ** 3)
+            f = p * torch.sigmoid(u)
+        # exp and erfc: the argument is off by a few 2^-24 of itself, the value by half a step of 2^-149, times |p|
+        rel = 2.0 ** -8 + 2.0 ** -21 * (u.abs() + 8)
+        bound = (rel * f.abs() + 2.0 ** -149 * (p.abs() + 1)) * 2.0 ** 100
+        want = (f * 2.0 ** 100)[:, None]
+        assert ((y - want).abs() <= bound[:, None]).all(), (y[:, 0], want[:, 0])
