@@ -592,7 +592,8 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *   rows     0..2^24-1 (0 launches nothing), ceil(rows / 16) * ceil(n / 16) < 2^23
  *   gate, up of the same n, k, group, format and scale_dtype
  * The workspace is psispec_w4_workspace(rows, n, k, 1) bytes, (.., 2) for a gated call; 0: none is needed and
- * NULL will do.  Sums are taken in a fixed order: reruns are bitwise identical.
+ * NULL will do.  What is needed of it overlaps no input and no output (PSISPEC_EINVAL).  Sums are taken in a fixed
+ * order: reruns are bitwise identical.
  */
 size_t psispec_w4_workspace(int32_t rows, int32_t n, int32_t k, int32_t mats);
 

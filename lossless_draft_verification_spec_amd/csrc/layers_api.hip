@@ -104,6 +104,9 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
   if (meet(ro, rx) || meet(ro, rs) || meet(ro, rb) || meet(ro, rw) || meet(ro, rw2)) return PSISPEC_EINVAL;
   const size_t need = w4_workspace_bytes(rows, w->n, w->k, mats);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return PSISPEC_EWORKSPACE;
+  const Rows rws{workspace, 0, (int64_t)need, need > 0};
+  if (meet(rws, rx) || meet(rws, rs) || meet(rws, rb) || meet(rws, ro) || meet(rws, rw) || meet(rws, rw2))
+    return PSISPEC_EINVAL;
   W4Args a{};
   for (int i = 0; i < mats; ++i) {
     const psispec_w4_weight* p = i ? w2 : w;

@@ -1,0 +1,36 @@
+"""Host-side refusals of the layers' entry points at the ends of their ranges (no GPU: every call is refused)."""
+import pytest
+
+import lossless_draft_verification_spec_amd as pkg
+from test_layers_host import BF, F8, MX, _gated, _linear, _weight
+
+AT = [1 << 33 + i for i in range(7)]  # addresses far from each other
+
+
+@pytest.fixture(scope="module")
+def L():
+    return pkg.lib()
+
+
+def test_workspace_over_what_a_product_reads_or_writes(L):
+    n, k, rows = 12288, 4096, 576
+    x, out, bias, scales, w1, w2, ws = AT
+    need = L.psispec_w4_workspace(rows, n, k, 1)
+    assert need > 0 and need % 256 == 0
+    sizes = dict(x=x, xs=k, rows=rows, out=out, os_=n, ws=ws, wsn=need)
+    first = _weight(packed=w1, n=n, k=k)
+    last = x + 2 * rows * k  # right behind the rows
+    assert _linear(L, first, **{**sizes, "wsn": need - 256}) == -3
+    for at in (x, last - 256, x + 256 - need, out, out + 2 * rows * n - 256, w1, bias, bias + 2 * n - 256):
+        assert _linear(L, first, bias=bias, **{**sizes, "ws": at}) == -1, hex(at)
+    second = _weight(packed=w2, n=n, k=k)
+    sizes["wsn"] = L.psispec_w4_workspace(rows, n, k, 2)
+    for at in (x, out, w1, w2, w2 + 256):
+        assert _gated(L, first, second, **{**sizes, "ws": at}) == -1, hex(at)
+    # rows of 8 bits in parts, which need one for their sums
+    n, k, rows = 4096, 12288, 576
+    need = L.psispec_w4_workspace(rows, n, k, 1)
+    m = _weight(packed=w1, n=n, k=k, **MX)
+    sizes = dict(x=x, xs=k, dtype=F8, sc=scales, ss=k // 32, rows=rows, out=out, os_=n, odtype=BF, wsn=need)
+    for at in (x, scales, scales + rows * k // 32 - 256, out, w1):
+        assert _linear(L, m, **{**sizes, "ws": at}) == -1, hex(at)
