@@ -591,11 +591,14 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
  *            (PSISPEC_EINVAL)
  *   rows     0..2^24-1 (0 launches nothing), ceil(rows / 16) * ceil(n / 16) < 2^23
  *   gate, up of the same n, k, group, format and scale_dtype
- * The workspace is psispec_w4_workspace(rows, n, k, 1) bytes, (.., 2) for a gated call; 0: none is needed and
- * NULL will do.  What is needed of it overlaps no input and no output (PSISPEC_EINVAL).  Sums are taken in a fixed
+ * The workspace is psispec_w4_weight_workspace(w, rows, 1) bytes, (.., 2) for a gated call; 0: none is needed and
+ * NULL will do.  psispec_w4_workspace(rows, n, k, 1), (.., 2), is enough for either format: MX weights need no
+ * sums of their rows, and mostly nothing.  What is needed of it overlaps no input and no output (PSISPEC_EINVAL).  Sums are taken in a fixed
  * order: reruns are bitwise identical.
  */
 size_t psispec_w4_workspace(int32_t rows, int32_t n, int32_t k, int32_t mats);
+
+size_t psispec_w4_weight_workspace(const psispec_w4_weight* w, int32_t rows, int32_t mats);
 
 psispec_status psispec_w4_linear(const psispec_w4_weight* w, const void* x, int64_t x_stride,
                                  psispec_dtype dtype, const void* x_scale, int64_t x_scale_stride,

@@ -35,7 +35,8 @@ EXPORTS = ("psispec_verify_linear_workspace", "psispec_verify_linear",
            "psispec_kv_commit", "psispec_qkv_append", "psispec_paged_attention_workspace",
            "psispec_paged_attention", "psispec_paged_commit", "psispec_pages_workspace",
            "psispec_pages_assign", "psispec_pages_reserve", "psispec_add_rmsnorm",
-           "psispec_w4_packed_bytes", "psispec_w4_pack", "psispec_w4_workspace", "psispec_w4_linear",
+           "psispec_w4_packed_bytes", "psispec_w4_pack", "psispec_w4_workspace", "psispec_w4_weight_workspace",
+           "psispec_w4_linear",
            "psispec_w4_gated", "psispec_strerror", "psispec_timing_enable",
            "psispec_timing_read", "psispec_peak_read", "psispec_peak_mfma")
 
@@ -141,6 +142,8 @@ def lib():
         L.psispec_w4_pack.restype = i32
         L.psispec_w4_workspace.argtypes = [i32, i32, i32, i32]
         L.psispec_w4_workspace.restype = sz
+        L.psispec_w4_weight_workspace.argtypes = [P, i32, i32]
+        L.psispec_w4_weight_workspace.restype = sz
         L.psispec_w4_linear.argtypes = [P, P, i64, i32, P, i64, i32, P, P, i64, i32, P, sz, P]
         L.psispec_w4_linear.restype = i32
         L.psispec_w4_gated.argtypes = [P, P, i32, P, i64, i32, P, i64, i32, P, i64, i32, P, sz, P]
@@ -1117,6 +1120,10 @@ class W4Weight:
     def __setattr__(self, name, value):
         raise AttributeError("a W4Weight is not changed: make another")
 
+    def workspace_bytes(self, rows, matrices=1) -> int:
+        """What psispec_w4_linear needs for so many rows, psispec_w4_gated with matrices 2; 0: nothing."""
+        return int(lib().psispec_w4_weight_workspace(self._struct, rows, matrices))
+
 
 _W4_STRUCT = struct.Struct("Q6i")  # psispec_w4_weight
 _W4_SCALES = {**_SIXTEEN, torch.float8_e8m0fnu: PSISPEC_E8M0}
@@ -1163,6 +1170,7 @@ def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "in
 
 
 def w4_workspace_bytes(rows, out_features, in_features, matrices=1) -> int:
+    """Enough for weights of either format; W4Weight.workspace_bytes says what one needs."""
     return int(lib().psispec_w4_workspace(rows, out_features, in_features, matrices))
 
 
@@ -1205,7 +1213,7 @@ def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace):
     if need is None:
         if len(w._need) >= 4096:
             w._need.clear()
-        need = w._need[key] = w4_workspace_bytes(rows, n, k, 1 if w2 is None else 2)
+        need = w._need[key] = w.workspace_bytes(rows, 1 if w2 is None else 2)
     if need:
         workspace = _workspace_for(workspace, need, x.device, what)
         wp, wn = workspace.data_ptr(), workspace.numel()

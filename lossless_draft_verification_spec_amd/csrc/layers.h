@@ -93,8 +93,8 @@ struct ManyPlan {
   int steps;   // tiles of 128 inputs of a part, an even number
   size_t part_at, bytes;
 };
-ManyPlan many_plan(int rows, int n, int k, int mats);
-size_t w4_workspace_bytes(int rows, int n, int k, int mats);
+ManyPlan many_plan(int rows, int n, int k, int mats, int format);
+size_t w4_workspace_bytes(int rows, int n, int k, int mats, int format);
 hipError_t launch_w4(const W4Args& a, psispec_dtype dtype, int format, int mats, hipStream_t stream);
 
 }  // namespace psispec

@@ -102,7 +102,7 @@ psispec_status product(const psispec_w4_weight* w, const psispec_w4_weight* w2, 
       rs{x_scale, xs_stride, w->k / 32, rows}, rb{bias, 0, (int64_t)w->n * 2, 1},
       rw{w->packed, 0, (int64_t)l.bytes, 1}, rw2{w2 ? w2->packed : nullptr, 0, (int64_t)l.bytes, 1};
   if (meet(ro, rx) || meet(ro, rs) || meet(ro, rb) || meet(ro, rw) || meet(ro, rw2)) return PSISPEC_EINVAL;
-  const size_t need = w4_workspace_bytes(rows, w->n, w->k, mats);
+  const size_t need = w4_workspace_bytes(rows, w->n, w->k, mats, w->format);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return PSISPEC_EWORKSPACE;
   const Rows rws{workspace, 0, (int64_t)need, need > 0};
   if (meet(rws, rx) || meet(rws, rs) || meet(rws, rb) || meet(rws, ro) || meet(rws, rw) || meet(rws, rw2))
@@ -225,7 +225,12 @@ psispec_status psispec_w4_pack(const uint8_t* codes, int64_t codes_stride, const
 size_t psispec_w4_workspace(int32_t rows, int32_t n, int32_t k, int32_t mats) {
   if (rows < 1 || rows > kMaxRows || n < 1 || n > kMaxFeatures || k < 32 || k > kMaxFeatures || mats < 1 || mats > 2)
     return 0;
-  return w4_workspace_bytes(rows, n, k, mats);
+  return w4_workspace_bytes(rows, n, k, mats, PSISPEC_W4_INT);
+}
+
+size_t psispec_w4_weight_workspace(const psispec_w4_weight* w, int32_t rows, int32_t mats) {
+  if (check_weight(w) != PSISPEC_OK || rows < 1 || rows > kMaxRows || mats < 1 || mats > 2) return 0;
+  return w4_workspace_bytes(rows, w->n, w->k, mats, w->format);
 }
 
 psispec_status psispec_w4_linear(const psispec_w4_weight* w, const void* x, int64_t x_stride, psispec_dtype dtype,

@@ -10,7 +10,7 @@ namespace psispec {
 // 6144 x 4096 (216) 8-bit rows 25 / 21.  Tiles of 64 x 128 up to 1.5 tiles of 64 x 256 per CU (576 rows, 6144 x
 // 4096: MX 31.8 against 36.0; 12288 x 4096: 57 against 53).  Long rows with too few tiles: the inputs are cut so
 // that there are about 432 workgroups (576 rows, 4096 x 12288: INT few 85, three parts 75; 8-bit rows 48 / 39).
-ManyPlan many_plan(int rows, int n, int k, int mats) {
+ManyPlan many_plan(int rows, int n, int k, int mats, int format) {
   constexpr int kRows = 64, kCus = 256;
   ManyPlan p{};
   const int ktiles = (k + 127) / 128, bn = 256 / mats;
@@ -33,18 +33,19 @@ ManyPlan many_plan(int rows, int n, int k, int mats) {
   }
   p.steps = ((ktiles + p.parts - 1) / p.parts + 1) / 2 * 2;
   p.parts = (ktiles + p.steps - 1) / p.steps;
-  p.part_at = ((size_t)ktiles * 4 * p.mpad * 4 + 255) / 256 * 256;  // the sums of up to four groups per tile
+  // INT: the sums of up to four groups per tile
+  p.part_at = format == PSISPEC_W4_INT ? ((size_t)ktiles * 4 * p.mpad * 4 + 255) / 256 * 256 : 0;
   p.bytes = p.part_at + (p.parts > 1 ? (size_t)p.parts * mats * rows * p.npad * 4 : 0);
   return p;
 }
 
-size_t w4_workspace_bytes(int rows, int n, int k, int mats) {
-  const ManyPlan p = many_plan(rows, n, k, mats);
+size_t w4_workspace_bytes(int rows, int n, int k, int mats, int format) {
+  const ManyPlan p = many_plan(rows, n, k, mats, format);
   return p.use ? p.bytes : 0;
 }
 
 hipError_t launch_w4(const W4Args& a, psispec_dtype dtype, int format, int mats, hipStream_t stream) {
-  const bool many = many_plan(a.rows, a.n, a.k, mats).use;
+  const bool many = many_plan(a.rows, a.n, a.k, mats, format).use;
   if (dtype == PSISPEC_BF16)
     return many ? launch_w4_many_bf16(a, format, mats, stream) : launch_w4_few_bf16(a, format, mats, stream);
   if (dtype == PSISPEC_F16)

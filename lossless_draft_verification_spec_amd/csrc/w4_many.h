@@ -367,7 +367,7 @@ void launch_many_scales(const ManyArgs& m, const ManyPlan& p, hipStream_t stream
 template <typename X, int GPT, int MATS>
 hipError_t launch_many(const W4Args& a, hipStream_t stream) {
   constexpr bool kF8 = __is_same(X, F8);
-  const ManyPlan p = many_plan(a.rows, a.n, a.k, MATS);
+  const ManyPlan p = many_plan(a.rows, a.n, a.k, MATS, GPT > 0 ? PSISPEC_W4_INT : PSISPEC_W4_MX);
   ManyArgs m{a, static_cast<float*>(a.workspace), nullptr, p.mpad, p.npad, p.mblocks, p.nblocks, p.parts, kF8 ? p.steps / 2 : p.steps, p.band};
   m.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + p.part_at);
   if constexpr (!kF8 && GPT > 0) {

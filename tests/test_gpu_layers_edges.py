@@ -6,7 +6,8 @@ import torch
 
 import layers_ref as ref
 from layers_ref import BF, E8, F8, FH
-from lossless_draft_verification_spec_amd import psispec_w4_gated, psispec_w4_linear, psispec_w4_pack
+from lossless_draft_verification_spec_amd import (
+    psispec_w4_gated, psispec_w4_linear, psispec_w4_pack, w4_workspace_bytes)
 from test_gpu_layers import DEV, _gen, _gpu, _within
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +125,40 @@ def test_gated_where_the_activation_is_tiny(act, rows):
         bound = (rel * f.abs() + 2.0 ** -149 * (p.abs() + 1)) * 2.0 ** 100
         want = (f * 2.0 ** 100)[:, None]
         assert ((y - want).abs() <= bound[:, None]).all(), (y[:, 0], want[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, FH, F8])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_mx_weights_need_no_workspace_for_uncut_inputs(dtype, act):
+    g = _gen(17)
+    rows, n, k = 1601, 2039, 160
+    x, xs = ref.make_rows(rows, k, dtype, g)
+    mats = [ref.make_weight(n, k, "mx", 32, g, spread=4) for _ in range(2 if act else 1)]
+    w = [psispec_w4_pack(*map(_gpu, m), "mx", 32) for m in mats]
+    assert w[0].workspace_bytes(rows, len(w)) == 0
+    ot = BF if dtype == F8 else dtype
+    x_gpu, xs_gpu, out = _gpu(x), _gpu(xs), torch.empty((rows, n), dtype=ot, device=DEV)
+    before = torch.cuda.memory_stats(DEV)["allocation.all.allocated"]
+    if act:
+        psispec_w4_gated(x_gpu, *w, activation=act, x_scale=xs_gpu, out=out)
+        want, bound = ref.gated(x, xs, *mats, "mx", 32, act, ot)
+    else:
+        psispec_w4_linear(x_gpu, w[0], x_scale=xs_gpu, out=out)
+        want, bound = ref.linear(x, xs, *mats[0], "mx", 32, None, ot)
+    assert torch.cuda.memory_stats(DEV)["allocation.all.allocated"] == before
+    _within(out, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_workspace_of_mx_weights_is_what_the_query_says(dtype):
+    g = _gen(18)
+    rows, n, k = 801, 2033, 8224  # inputs in parts
+    x, xs = ref.make_rows(rows, k, dtype, g)
+    mat = ref.make_weight(n, k, "mx", 32, g, spread=4)
+    w = psispec_w4_pack(*map(_gpu, mat), "mx", 32)
+    need = w.workspace_bytes(rows)
+    assert 0 < need < w4_workspace_bytes(rows, n, k)
+    ws = torch.full((need + 512,), 9, dtype=torch.uint8, device=DEV)
+    y = psispec_w4_linear(_gpu(x), w, x_scale=_gpu(xs), workspace=ws[:need])
+    assert (ws[need:] == 9).all()
+    _within(y, *ref.linear(x, xs, *mat, "mx", 32, None, BF))

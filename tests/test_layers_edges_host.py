@@ -1,4 +1,6 @@
 """Host-side refusals of the layers' entry points at the ends of their ranges (no GPU: every call is refused)."""
+import ctypes
+
 import pytest
 
 import lossless_draft_verification_spec_amd as pkg
@@ -34,3 +36,20 @@ def test_workspace_over_what_a_product_reads_or_writes(L):
     sizes = dict(x=x, xs=k, dtype=F8, sc=scales, ss=k // 32, rows=rows, out=out, os_=n, odtype=BF, wsn=need)
     for at in (x, scales, scales + rows * k // 32 - 256, out, w1):
         assert _linear(L, m, **{**sizes, "ws": at}) == -1, hex(at)
+
+
+def test_workspace_by_format(L):
+    """MX weights have no sums of rows: with uncut inputs nothing is needed, with cut ones the parts' sums alone."""
+    def need(rows, mats=1, **kw):
+        return L.psispec_w4_weight_workspace(ctypes.byref(_weight(**kw)), rows, mats)
+
+    for n, k, rows, mats in ((2039, 160, 1601, 1), (4096, 16512, 131142, 1), (12288, 4096, 576, 2)):
+        assert need(rows, mats, n=n, k=k, **MX) == 0
+        assert need(rows, mats, n=n, k=k) == L.psispec_w4_workspace(rows, n, k, mats) > 0
+    rows, n, k = 576, 4096, 12288  # three parts
+    assert need(rows, n=n, k=k, **MX) == 3 * rows * n * 4
+    assert need(rows, n=n, k=k) == L.psispec_w4_workspace(rows, n, k, 1) > 3 * rows * n * 4
+    assert need(64, n=n, k=k) == need(64, n=n, k=k, **MX) == 0
+    for bad in (dict(rows=0), dict(rows=1 << 24), dict(rows=576, mats=3), dict(rows=576, k=100), dict(rows=576, reserved=1)):
+        assert need(**{"n": n, "k": k, **bad}) == 0
+    assert L.psispec_w4_weight_workspace(None, 576, 1) == 0
