@@ -1010,6 +1010,11 @@ def _idx_stream(idx: int):
     return _raw_stream(idx) if _raw_stream is not None else _stream(None)
 
 
+def _count(n) -> int:
+    """n as the library's 32-bit counts take it: -1, which it refuses, for what they do not hold."""
+    return n if n <= 0x7fffffff else -1
+
+
 _SIXTEEN = {torch.bfloat16: PSISPEC_BF16, torch.float16: PSISPEC_F16}
 _LAYER_DTYPES = {**_SIXTEEN, torch.float8_e4m3fn: PSISPEC_F8E4M3}
 
@@ -1037,6 +1042,8 @@ def psispec_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None,
             return psispec_add_rmsnorm(x, weight, residual, residual_out, eps, quant, out, scale)
     dim = shape[-1]
     rows = x.numel() // dim
+    if rows > 0x7fffffff or dim > 0x7fffffff:
+        raise PsispecError(f"psispec_add_rmsnorm takes no {rows} rows of {dim}")
     xp, xs = _rows_of(x, shape, idx, "x")
     wp = rp = rs = rop = ros = sp = ss = 0
     if weight is not None:
@@ -1122,7 +1129,7 @@ class W4Weight:
 
     def workspace_bytes(self, rows, matrices=1) -> int:
         """What psispec_w4_linear needs for so many rows, psispec_w4_gated with matrices 2; 0: nothing."""
-        return int(lib().psispec_w4_weight_workspace(self._struct, rows, matrices))
+        return int(lib().psispec_w4_weight_workspace(self._struct, _count(rows), matrices))
 
 
 _W4_STRUCT = struct.Struct("Q6i")  # psispec_w4_weight
@@ -1132,7 +1139,8 @@ _W4_ACTIVATIONS = {"silu": PSISPEC_W4_SILU, "gelu": PSISPEC_W4_GELU, "gelu_tanh"
 
 
 def w4_packed_bytes(out_features, in_features, group, format) -> int:
-    return int(lib().psispec_w4_packed_bytes(out_features, in_features, group, _W4_FORMATS[format]))
+    return int(lib().psispec_w4_packed_bytes(_count(out_features), _count(in_features), _count(group),
+                                             _W4_FORMATS[format]))
 
 
 def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "int", group: int = 128,
@@ -1171,7 +1179,7 @@ def psispec_w4_pack(codes: torch.Tensor, scales: torch.Tensor, format: str = "in
 
 def w4_workspace_bytes(rows, out_features, in_features, matrices=1) -> int:
     """Enough for weights of either format; W4Weight.workspace_bytes says what one needs."""
-    return int(lib().psispec_w4_workspace(rows, out_features, in_features, matrices))
+    return int(lib().psispec_w4_workspace(_count(rows), _count(out_features), _count(in_features), matrices))
 
 
 def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace):
@@ -1181,6 +1189,8 @@ def _w4_product(what, x, w, w2, act, x_scale, bias, out, out_dtype, workspace):
     if code is None or not shape or shape[-1] != k:
         raise PsispecError(f"x must be bfloat16, float16 or float8_e4m3fn [..., {k}], got {dt} {list(shape)}")
     rows = x.numel() // k
+    if rows > 0x7fffffff:
+        raise PsispecError(f"{what} takes no {rows} rows")
     xp, xs = _rows_of(x, shape, idx, "x")
     sp = ss = bp = wp = wn = 0
     if code == PSISPEC_F8E4M3:

@@ -7,7 +7,8 @@ import torch
 import layers_ref as ref
 from layers_ref import BF, E8, F8, FH
 from lossless_draft_verification_spec_amd import (
-    psispec_w4_gated, psispec_w4_linear, psispec_w4_pack, w4_workspace_bytes)
+    PsispecError, W4Weight, psispec_add_rmsnorm, psispec_w4_gated, psispec_w4_linear, psispec_w4_pack,
+    w4_workspace_bytes)
 from test_gpu_layers import DEV, _gen, _gpu, _within
 
 pytestmark = pytest.mark.gpu
@@ -162,3 +163,17 @@ def test_workspace_of_mx_weights_is_what_the_query_says(dtype):
     y = psispec_w4_linear(_gpu(x), w, x_scale=_gpu(xs), workspace=ws[:need])
     assert (ws[need:] == 9).all()
     _within(y, *ref.linear(x, xs, *mat, "mx", 32, None, BF))
+
+
+def test_counts_beyond_32_bits_are_refused():
+    """More rows, columns or outputs than the library's counts hold (none of it is written: 9 GB are only reserved)."""
+    x = torch.empty((1 << 32) + 64, dtype=BF, device=DEV)
+    for shape in ((-1, 1), (1, -1)):
+        with pytest.raises(PsispecError):
+            psispec_add_rmsnorm(x.view(shape), out=x.view(shape))
+    codes, s = ref.make_weight(48, 160, "mx", 32, _gen(1))
+    w = psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32)
+    assert w.workspace_bytes((1 << 32) + 576) == 0
+    for n, k, group in (((1 << 32) + 48, 160, 32), (48, (1 << 32) + 160, 32), (48, 160, (1 << 32) + 32)):
+        with pytest.raises(PsispecError):
+            W4Weight(w.packed, n, k, group, "mx", E8)

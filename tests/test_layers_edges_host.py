@@ -53,3 +53,15 @@ def test_workspace_by_format(L):
     for bad in (dict(rows=0), dict(rows=1 << 24), dict(rows=576, mats=3), dict(rows=576, k=100), dict(rows=576, reserved=1)):
         assert need(**{"n": n, "k": k, **bad}) == 0
     assert L.psispec_w4_weight_workspace(None, 576, 1) == 0
+
+
+def test_counts_beyond_32_bits_are_refused():
+    assert pkg.w4_packed_bytes(48, 160, 32, "mx") > 0 and pkg.w4_workspace_bytes(576, 12288, 4096) > 0
+    for wide in (1 << 31, (1 << 32) + 48, (1 << 32) + 160, (1 << 32) + 32):
+        assert pkg.w4_packed_bytes(wide, 160, 32, "mx") == 0
+        assert pkg.w4_packed_bytes(48, wide, 32, "mx") == 0
+        assert pkg.w4_packed_bytes(48, 160, wide, "int") == 0
+    for wide in (1 << 31, (1 << 32) + 576, (1 << 32) + 4096):
+        assert pkg.w4_workspace_bytes(wide, 12288, 4096) == 0
+        assert pkg.w4_workspace_bytes(576, wide, 4096) == 0
+        assert pkg.w4_workspace_bytes(576, 12288, wide) == 0
