@@ -513,8 +513,8 @@ psispec_status psispec_pages_reserve(const psispec_page_pool* pool, int32_t* tab
  *   scale_dtype F32   one s per row: the row's largest |y| / 448
  *   scale_dtype E8M0  one s per 32 columns: the smallest power of two (from 2^-127) with |y| <= 448 s in
  *                     the block; what psispec_w4_linear and psispec_w4_gated take
- * A row (block) of zeros has q = 0; one with an infinity or a NaN has an infinite or NaN scale, its q are
- * unspecified.
+ * A row (block) of zeros gives zeros, with eps 0 too; one with an infinity or a NaN has an infinite or NaN scale,
+ * its q are unspecified.
  *   x             rows of dim elements, x_stride elements apart; dtype PSISPEC_BF16 or PSISPEC_F16
  *   residual      rows of residual_dtype (dtype or PSISPEC_F32), or NULL: h = x
  *   residual_out  rows of residual_dtype, or NULL: h is not written

@@ -157,7 +157,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_rmsnorm(AddNormAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) wide += (double)h[i][e] * (double)h[i][e];
       }
-    wide = 1.0 / sqrt(row_sum<TPR>(wide, s_wide) / (double)a.dim + (double)a.eps);
+    wide = row_sum<TPR>(wide, s_wide) / (double)a.dim + (double)a.eps;
+    wide = wide == 0.0 ? 0.0 : 1.0 / sqrt(wide);  // a row of zeros without eps gives zeros
     // either factor, and h * pre, stay well inside 32 bits
     pre = wide < 0x1p-64 ? 0x1p-64f : wide > 0x1p64 ? 0x1p64f : 1.0f;
     inv = (float)(wide / (double)pre);

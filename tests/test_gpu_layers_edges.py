@@ -177,3 +177,32 @@ def test_counts_beyond_32_bits_are_refused():
     for n, k, group in (((1 << 32) + 48, 160, 32), (48, (1 << 32) + 160, 32), (48, 160, (1 << 32) + 32)):
         with pytest.raises(PsispecError):
             W4Weight(w.packed, n, k, group, "mx", E8)
+
+
+@pytest.mark.parametrize("quant", [None, "row", "mx"])
+@pytest.mark.parametrize("dim", [32, 1024, 1056, 9024, 32768])
+@pytest.mark.parametrize("eps", [0.0, 1e-60, 1e-6])
+def test_norm_of_a_row_of_zeros(quant, dim, eps):
+    """Padding among rows: zeros, whatever eps, and the rows beside it as without it."""
+    g = _gen(dim)
+    x = torch.randn((5, dim), generator=g).to(BF)
+    r = torch.randn((5, dim), generator=g).to(BF)
+    x[2], r[2] = 0.0, 0.0
+    x[3], r[3] = 1.0, -1.0  # a sum of zeros
+    w = (1 + 0.3 * torch.randn(dim, generator=g)).to(BF)
+    out, ro, s = psispec_add_rmsnorm(_gpu(x), _gpu(w), residual=_gpu(r), eps=eps, quant=quant)
+    assert (out[2:4].float() == 0).all() and (ro[2:4] == 0).all()
+    if quant == "row":
+        assert (s[2:4] == 0).all()
+    elif quant == "mx":
+        assert (s.view(torch.uint8)[2:4] == 0).all()
+    rest = [0, 1, 4]
+    alone = psispec_add_rmsnorm(_gpu(x[rest]), _gpu(w), residual=_gpu(r[rest]), eps=eps, quant=quant)
+    for a, b in zip((out, ro, s), alone):
+        if b is not None:
+            assert torch.equal(a.view(5, -1).view(torch.uint8)[rest], b.view(3, -1).view(torch.uint8))
+    y, _ = ref.norm(x[rest], w, r[rest], eps)
+    sc = 1.0 if s is None else s.cpu().double()[rest][:, None] if quant == "row" else (
+        ref.powers(s.cpu())[rest].repeat_interleave(32, 1))
+    step = ref.half_step(y / sc, BF if quant is None else F8) * sc
+    _within(out.cpu().double()[rest] * sc, y, (2 * ref.NORM_REL * y.abs() + step) * (1 + 2.0 ** -8))
