@@ -3,6 +3,7 @@
 #pragma once
 
 #include "launch.h"
+#include "w4_plan.h"
 
 namespace psispec {
 
@@ -84,16 +85,6 @@ hipError_t launch_w4_many_bf16(const W4Args& a, int format, int mats, hipStream_
 hipError_t launch_w4_many_f16(const W4Args& a, int format, int mats, hipStream_t stream);
 hipError_t launch_w4_many_f8(const W4Args& a, int mats, hipStream_t stream);
 
-// How the work of many rows is cut, from the sizes alone (w4.hip)
-struct ManyPlan {
-  bool use;    // else the kernel for few rows takes it
-  int nb;      // tiles of outputs of a wave, of all matrices
-  int mblocks, nblocks, parts, mpad, npad;
-  int band;    // row blocks that follow each other before the next column
-  int steps;   // tiles of 128 inputs of a part, an even number
-  size_t part_at, bytes;
-};
-ManyPlan many_plan(int rows, int n, int k, int mats, int format);
 size_t w4_workspace_bytes(int rows, int n, int k, int mats, int format);
 hipError_t launch_w4(const W4Args& a, psispec_dtype dtype, int format, int mats, hipStream_t stream);
 

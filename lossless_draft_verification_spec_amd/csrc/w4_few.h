@@ -251,55 +251,39 @@ __global__ __launch_bounds__(64 * KW, KW < 8 ? 2 : 1) void k_w4_few(W4Args a) {
   }
 }
 
-// The largest tile whose workgroups still cover most of the 256 CUs: a tile of twice the rows or outputs reads
-// the weights or the rows once instead of twice.  4096 x 4096 INT, 64 rows: 64 rows x 32 outputs (128
-// workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 12288 x 4096, 64 rows: 64 x 64 (192) 15.4,
-// 32 x 32 (768) 15.8.  Eight waves share a tile's inputs, four where several workgroups share a CU (64 rows x 32
-// outputs at 16384 x 4096: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
-// Little more than one workgroup per CU costs as much as two: 639 rows, 2 x 208 x 9856 gated with 16 rows x 32 outputs
-// (280 workgroups) 27.0, 32 x 32 (140) 21.1; 9 rows, 2 x 12288 x 4096 with 32 outputs (384) 13.4, 16 (768) 11.8, but
-// 2 x 8192 and 2 x 24576 (256 and 768) 9.7 and 22.5 against 9.9 and 27.0.
 template <typename X, int GPT, bool SF16, int MATS>
 hipError_t launch_few_scales(const W4Args& a, hipStream_t stream) {
-  constexpr int kFill = 192, kShare = 320, kLong = 64;  // workgroups, workgroups, tiles of 128 inputs
-  constexpr int kOne = 256, kTwo = 448;                 // workgroups: one, nearly two per CU
   constexpr int kWide = MATS == 2 ? 2 : 4;
-  const auto blocks = [&](int r4, int nt) {
-    return (int64_t)((a.ntiles + nt - 1) / nt) * ((a.rows + 4 * r4 - 1) / (4 * r4));
+  const FewPlan p = few_plan(a.rows, a.ntiles, a.ktiles, MATS);
+  const auto go = [&](auto kernel) {
+    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", kernel, dim3((unsigned)p.blocks), dim3(64 * p.kw), 0, stream,
+                   a);
   };
-  const auto go = [&](auto kernel, int r4, int nt, int kw) {
-    PSISPEC_LAUNCH(MATS == 2 ? "w4_gated" : "w4_linear", kernel, dim3((unsigned)blocks(r4, nt)), dim3(64 * kw), 0,
-                   stream, a);
-  };
-  if (a.rows > 32 && blocks(16, kWide) >= kFill) {
-    if (blocks(16, kWide) >= kShare)
-      go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 4>), 16, kWide, 4);
-    else
-      go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 8>), 16, kWide, 8);
-  } else if (MATS == 1 && a.rows > 16 && blocks(8, 4) >= kFill) {
+  if (p.r4 == 16 && p.kw == 4) {
+    go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 4>));
+  } else if (p.r4 == 16) {
+    go((k_w4_few<X, GPT, SF16, 16, kWide, MATS, 8>));
+  } else if (p.r4 == 8 && p.nt == 4) {
     if constexpr (MATS == 1) {
-      if (blocks(8, 4) >= kShare)
-        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 4>), 8, 4, 4);
+      if (p.kw == 4)
+        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 4>));
       else
-        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 8>), 8, 4, 8);
+        go((k_w4_few<X, GPT, SF16, 8, 4, MATS, 8>));
     }
-  } else if (a.rows > 16 && (blocks(8, 2) >= kFill || blocks(4, 2) > kOne)) {
-    if (blocks(8, 2) >= kShare)
-      go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 4>), 8, 2, 4);
-    else
-      go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 8>), 8, 2, 8);
-  } else if (a.rows > 4) {
-    const int64_t b = blocks(4, 2);
-    if ((b >= kFill && b <= kOne) || b >= kTwo)
-      go((k_w4_few<X, GPT, SF16, 4, 2, MATS, 8>), 4, 2, 8);
-    else if (a.ktiles >= kLong && b < kFill)
-      go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 16>), 4, 1, 16);
-    else
-      go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 8>), 4, 1, 8);
-  } else if (a.ktiles >= kLong && blocks(1, 1) <= 256) {
-    go((k_w4_few<X, GPT, SF16, 1, 1, MATS, 16>), 1, 1, 16);
+  } else if (p.r4 == 8 && p.kw == 4) {
+    go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 4>));
+  } else if (p.r4 == 8) {
+    go((k_w4_few<X, GPT, SF16, 8, 2, MATS, 8>));
+  } else if (p.r4 == 4 && p.nt == 2) {
+    go((k_w4_few<X, GPT, SF16, 4, 2, MATS, 8>));
+  } else if (p.r4 == 4 && p.kw == 16) {
+    go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 16>));
+  } else if (p.r4 == 4) {
+    go((k_w4_few<X, GPT, SF16, 4, 1, MATS, 8>));
+  } else if (p.kw == 16) {
+    go((k_w4_few<X, GPT, SF16, 1, 1, MATS, 16>));
   } else {
-    go((k_w4_few<X, GPT, SF16, 1, 1, MATS, 8>), 1, 1, 8);
+    go((k_w4_few<X, GPT, SF16, 1, 1, MATS, 8>));
   }
   return hipGetLastError();
 }
