@@ -1245,8 +1245,9 @@ def psispec_w4_linear(x: torch.Tensor, weight: W4Weight, x_scale: torch.Tensor |
     """A linear layer with weights of 4 bits: x [..., in_features] (bf16, f16; or, with mx weights,
     float8_e4m3fn with x_scale float8_e8m0fnu [..., in_features / 32], psispec_add_rmsnorm's "mx" rows)
     to out [..., out_features] of x's dtype (bf16, or f16 by out_dtype or out, for 8-bit rows).  Sums are of 32
-    bits and no weight is rounded; 8-bit rows: among eight neighbouring inputs each product is cut to a multiple
-    of 2^-13 of the largest one's power of two.
+    bits and no weight is rounded (16-bit rows: but for mx scales 2^36 (f16) or 2^253 (bf16) below the output's
+    largest); 8-bit rows: among eight neighbouring inputs each product is cut to a multiple of 2^-13 of the largest
+    one's power of two.
     Rows 16-byte aligned and evenly spaced; bias [out_features] of out's dtype."""
     if _elsewhere(weight.packed.get_device(), stream):
         with _On.guard(weight.packed.device, stream):

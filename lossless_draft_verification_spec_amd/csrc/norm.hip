@@ -9,16 +9,16 @@
 // wave reads 1 KB at a time, and the 32 columns of a power-of-two scale belong to four neighbouring
 // lanes.  h is squared and normalised as the 32-bit sum, before residual_out rounds it.  BF16 and 32-bit
 // rows reach numbers whose squares 32 bits do not hold: such a row is summed again in 64 bits (all rows in
-// 64 bits: 90 us instead of 88 for 8000 rows of 5120).
-// Bound by memory: 8000 rows of 5120 (F16, residual in 32 bits, out in 8 bits) 87 us, 5.2 TB/s, as fast as a large
-// copy; 576 rows of 4096 6.5 us and one row 4, the launch and one round of loads.
+// 64 bits: 2% more for 8000 rows of 5120).
+// Bound by memory: 8000 rows of 5120 (F16, residual in 32 bits, out in 8 bits) 84 us, 5.4 TB/s, where a large copy
+// reaches 5.1; 576 rows of 4096 6 us and one row 3.5, the launch and one round of loads.
 #include "layers.h"
 
 namespace psispec {
 namespace {
 
 // Rows may start anywhere: vectors of their elements' alignment, which global memory takes as they are (8000 rows of
-// 4096, every second one off 16 bytes: 62 us, element by element 149; all of them on 16 bytes 53)
+// 4096 with a residual, every second one off 16 bytes: 62 us, element by element 149; all of them on 16 bytes 55)
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8), aligned(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -254,10 +254,13 @@ void launch_kind(const AddNormArgs& a, hipStream_t stream) {
                      stream, s);
     }
   };
-  // As few threads per row as hold it in 8 or 16 elements each (a wave waits for no other).  In us, rows x dim:
-  // 8000 x 512 64 threads 7.6, 256 14.9; 8000 x 1024 64 threads 10.7, 256 18.1 (one row 3.5, 3.2); 8000 x 4096 256
-  // threads 36.2, 512 40.5 (576 rows 5.8, 6.3; one row 3.9, 3.7); 8000 x 8192 512 threads 89.4, 1024 95.2;
-  // 4000 x 16384 1024 threads of 16 elements 88, of up to 32 120.
+  // As few threads per row as hold it in 8 or 16 elements each (a wave waits for no other).  In us per launch, BF16
+  // with a residual of the same type, three sets of inputs in turn: 8000 x 512 64 threads 9.4, 256 16.5; 8000 x 1024
+  // 64 threads 12.5, 256 17.5 (one row 3.5, 3.2); 576 x 4096 256 threads 6.0, 512 6.3 (one row 3.8, 3.4); 576 x 8192
+  // 512 threads 10.0, 1024 12.3; 4000 x 16384 1024 threads of 16 elements 99, of up to 32 120.  Where the rows come
+  // from memory, not from the cache behind the L2, twice the threads are as fast or faster: 8000 x 4096 256 threads
+  // 55.0, 512 51.6 (on one set of 196 MB, which that cache holds, 36.2 and 40.5); 8000 x 8192 512 threads 101, 1024 96
+  // (89 and 95).
   if (a.dim <= 512)
     go((k_add_rmsnorm<T, R, KIND, 64, 1>), 4, 256);
   else if (a.dim <= 1024)

@@ -8,9 +8,12 @@
 // order they would be pieces of 16 bytes), so no wave waits for another before the end.  One step per wave is
 // in flight and the waves cover for each other: with two or three the times were the same or worse.
 // Bound by the weights' way from memory and, for one layer, by what a launch and its first loads take (4 us).
-// Device time: one row, 6144 x 4096 INT 6 us, 2 x 12288 x 4096 MX gated 11 (53 MB, 4.9 TB/s); 9 rows, 4096 x 12288
-// MX 8; 64 rows, 4096 x 4096 INT in F16 9, 2 x 12288 x 4096 MX with 8-bit rows gated 16 (3.4 TB/s: the rows' 98 MB
-// from the L2 beside the weights' 53).
+// In us per launch, in a graph of 42 on three sets of inputs: one row, 6144 x 4096 INT 5.7, 2 x 12288 x 4096 MX gated
+// 11 (53 MB, 4.8 TB/s); 9 rows, 4096 x 12288 MX 7.7; 64 rows, 4096 x 4096 INT in F16 8.3 (its waves wait for half of
+// their cycles: four steps each, a step's loads waited for before its products), 12288 x 4096 INT 15.3, 2 x 12288 x
+// 4096 gated INT 25, MX 21, MX with 8-bit rows 17 (3.2 TB/s: the rows' 98 MB from the L2 beside the weights' 53, and
+// one and a half workgroups per CU).  INT tiles of 64 rows need more than the 256 registers that there are: 20 of the
+// 24 instantiations keep 2 to 25 values in scratch memory, since the sums of all their tiles live at once.
 #pragma once
 
 #include "w4.h"

@@ -8,12 +8,14 @@
 // travels with them: formed by the matrix cores here it would be a fifth of their work.  Loads run one step
 // ahead (two steps, 576 rows, 12288 x 4096: 8-bit rows 37 us instead of 35, MX 59 and 59; 128 rows per workgroup
 // were no faster either).  Few tiles: the inputs are cut into parts whose sums are joined in their order by k_w4_join.
-// Device time: 576 rows, 12288 x 4096: INT 65 us (0.89 PFLOP/s), MX 53 (1.1), MX with 8-bit rows 32 (1.8); two
-// such INT layers gated 122; 2048 rows, 4096 x 12288: 187 (1.10), 167 (1.23), 87 (2.4); a library product of 16-bit
-// numbers takes 184 for the last.  INT is bound by the vector units beside the matrix cores (decoding, scales: four
-// instructions of theirs per matrix instruction, which keeps them as long as it takes itself; their order within a
-// tile made no difference), MX by the matrix cores (half of their cycles) and LDS, 8-bit rows by LDS, from which
-// each wave reads all 64 rows.
+// In us per launch, in a graph of 42 on three sets of inputs: 576 rows, 12288 x 4096: INT 64 (0.90 PFLOP/s), MX 53
+// (1.1), MX with 8-bit rows 33 (1.8); two such INT layers gated 123; 2048 rows, 4096 x 12288: 187 (1.10), 157 (1.31),
+// 86 (2.4); a library product of 16-bit numbers takes 184 for the last.  INT scales per 64 and per 32 inputs: 211 and
+// 254 instead of 187 (two and four times the scales' products).  INT is bound by the vector units beside the matrix
+// cores (decoding, scales: four instructions of theirs per matrix instruction, which keeps them as long as it takes
+// itself; their order within a tile made no difference).  With 8-bit rows and 432 workgroups (576 rows, 6144 x 4096)
+// it is the wait for each step's loads: the waves wait for 0.36 of their cycles, the matrix units are busy for 0.35
+// and LDS for 0.23 of them, and 80 CUs hold one workgroup instead of two.
 #pragma once
 
 #include "w4.h"

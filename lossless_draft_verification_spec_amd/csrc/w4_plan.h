@@ -20,11 +20,12 @@ struct ManyPlan {
 };
 // The kernel for many rows reads the weights once per 64 rows and the rows once per 256 outputs, the one for few
 // rows in tiles of at most 64 x 64 whose waves share the inputs: that one where there are not tiles of 64 x 256
-// enough for the CUs.  In us, few / many: 256 rows, 4096 x 4096 (64 tiles) INT 15.8 / 23.0; 576 rows, 4096 x
-// 4096 (144) 32.8 / 36.7; 256 rows, 12288 x 4096 (192) INT 38 / 41, MX 33 / 31, 8-bit rows 25 / 21; 576 rows,
-// 6144 x 4096 (216) 8-bit rows 25 / 21.  Tiles of 64 x 128 up to 1.5 tiles of 64 x 256 per CU (576 rows, 6144 x
-// 4096: MX 31.8 against 36.0; 12288 x 4096: 57 against 53).  Long rows with too few tiles: the inputs are cut so
-// that there are about 432 workgroups (576 rows, 4096 x 12288: INT few 85, three parts 75; 8-bit rows 48 / 39).
+// enough for the CUs.  In us per launch, in a graph of 42 on three sets of inputs, few / many: 256 rows, 4096 x 4096
+// (64 tiles) INT 16 / 45; 576 rows, 4096 x 4096 (144) INT 36.5 / 40.8; 256 rows, 12288 x 4096 (192) INT 38 / 41, MX
+// 32.7 / 30.6, 8-bit rows 24 / 21; 576 rows, 6144 x 4096 (216) 8-bit rows 25.5 / 21.4.  Tiles of 64 x 128 up to 1.5
+// tiles of 64 x 256 per CU (576 rows, 6144 x 4096: INT 41 against 46.5, MX 31.6 against 36.3; 12288 x 4096 MX: 55.2
+// against 52.7).  Long rows with too few tiles: the inputs are cut so that there are about 432 workgroups (576 rows,
+// 4096 x 12288: INT few 92, uncut 117, three parts 72; 8-bit rows 48, 56 and 39).
 inline ManyPlan many_plan(int rows, int n, int k, int mats, int format) {
   constexpr int kRows = 64, kCus = 256;
   ManyPlan p{};
@@ -62,13 +63,14 @@ struct FewPlan {
   int64_t blocks;
 };
 // The largest tile whose workgroups still cover most of the 256 CUs: a tile of twice the rows or outputs reads
-// the weights or the rows once instead of twice.  4096 x 4096 INT, 64 rows: 64 rows x 32 outputs (128
-// workgroups) 10.1 us, 32 x 32 (256) 7.0, 16 x 16 (1024) 8.7; 12288 x 4096, 64 rows: 64 x 64 (192) 15.4,
-// 32 x 32 (768) 15.8.  Eight waves share a tile's inputs, four where several workgroups share a CU (64 rows x 32
-// outputs at 16384 x 4096: 17.9 against 19.7), sixteen for long rows (9 rows, 4096 x 12288: 7.7 against 9.6).
-// Little more than one workgroup per CU costs as much as two: 639 rows, 2 x 208 x 9856 gated with 16 rows x 32 outputs
-// (280 workgroups) 27.0, 32 x 32 (140) 21.1; 9 rows, 2 x 12288 x 4096 with 32 outputs (384) 13.4, 16 (768) 11.8, but
-// 2 x 8192 and 2 x 24576 (256 and 768) 9.7 and 22.5 against 9.9 and 27.0.
+// the weights or the rows once instead of twice.  In us as above: 64 rows, 4096 x 4096 INT: 64 rows x 64 outputs (64
+// workgroups) 13.6, 32 x 64 (128) 9.9, 32 x 32 (256) 7.7, 16 x 32 (512) 8.4, 16 x 16 (1024) 10.4; 12288 x 4096: 64 x 64
+// (192) 15.3, 32 x 64 (384) 15.9, 32 x 32 (768) 16.1.  Eight waves share a tile's inputs, four where several workgroups
+// share a CU (64 rows, 24576 x 4096: INT 24.2 against 27.1, MX 20.7 against 24.4), sixteen for long rows (4096 x 12288:
+// 9 rows 7.8 against 9.3, one row 7.5 against 9.3).  Little more than one workgroup per CU costs as much as two: 639
+// rows, 2 x 208 x 9856 gated with 16 rows x 32 outputs (280 workgroups) 27.1, 32 x 32 (140) 21.3; 9 rows, 2 x 12288 x
+// 4096 with 32 outputs (384) 13.5, 16 (768) 11.9, but 2 x 8192 and 2 x 24576 (256 and 768) 9.7 and 22.0 against 9.4 and
+// 25.7.
 inline FewPlan few_plan(int rows, int ntiles, int ktiles, int mats) {
   constexpr int kFill = 192, kShare = 320, kLong = 64;  // workgroups, workgroups, tiles of 128 inputs
   constexpr int kOne = 256, kTwo = 448;                 // workgroups: one, nearly two per CU
