@@ -9,7 +9,7 @@ from layers_ref import BF, E8, F8, FH
 from lossless_draft_verification_spec_amd import (
     PsispecError, W4Weight, psispec_add_rmsnorm, psispec_w4_gated, psispec_w4_linear, psispec_w4_pack,
     w4_workspace_bytes)
-from test_gpu_layers import DEV, KINDS, _gen, _gpu, _within
+from test_gpu_layers import DEV, KINDS, _gen, _gpu, _product, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,73 @@ def test_8bit_rows_are_off_by_the_cut(rows, n, k):
     bound = (k / 8 + 32) * 2.0 ** -24 * plain  # a rounding per eight products, and the joins of the waves
     y = psispec_w4_linear(_gpu(x), psispec_w4_pack(_gpu(codes), _gpu(s), "mx", 32), x_scale=_gpu(xs), out_dtype=FH)
     _within(y, cut, bound + ref.half_step(cut, FH) * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 1 << 20, 32), (3, 1 << 20, 64), (40, 1 << 18, 32), (1, 16, 1 << 20),
+                                      (20, 16, 1 << 20), (70, 40, 1 << 18)])
+@pytest.mark.parametrize("dtype,fmt,group", [(BF, "int", 128), (FH, "int", 32), (BF, "mx", 32), (F8, "mx", 32)])
+def test_most_outputs_and_inputs(rows, n, k, dtype, fmt, group):
+    _product(rows, n, k, dtype, fmt, group, seed=rows, spread=2)
+
+
+@pytest.mark.parametrize("dtype,fmt,group", [(BF, "int", 32), (FH, "mx", 32), (F8, "mx", 32)])
+def test_most_rows(dtype, fmt, group):
+    """2^24 - 1 rows: the first ones against the reference, all others as those."""
+    g = _gen(41)
+    some, many, n, k = 4096, (1 << 24) - 1, 16, 32
+    x, xs = ref.make_rows(some, k, dtype, g)
+    codes, s = ref.make_weight(n, k, fmt, group, g)
+    idx = torch.arange(many, device=DEV) % some
+    w = psispec_w4_pack(_gpu(codes), _gpu(s), fmt, group)
+    xm = _gpu(x).view(torch.uint8)[idx].view(dtype)
+    xsm = None if xs is None else _gpu(xs).view(torch.uint8)[idx].view(E8)
+    y = psispec_w4_linear(xm, w, x_scale=xsm)
+    _within(y[:some], *ref.linear(x, xs, codes, s, fmt, group, None, BF if dtype == F8 else dtype))
+    for i in range(0, many, 1 << 20):  # whole blocks of `some` rows
+        part = y[i:i + (1 << 20)]
+        assert torch.equal(part, y[:some][idx[:len(part)]])
+
+
+def test_more_inputs_than_16_bits_in_parts():
+    """Rows of 2^18 inputs through the kernel for many rows, its inputs cut: eight rows against the reference, all
+    others as those."""
+    g = _gen(43)
+    rows, n, k = 1500, 1003, 1 << 18
+    x, _ = ref.make_rows(8, k, BF, g)
+    mat = ref.make_weight(n, k, "int", 128, g)
+    w = psispec_w4_pack(*map(_gpu, mat), "int", 128)
+    assert w.workspace_bytes(rows) > rows * n * 4  # sums of parts
+    y = psispec_w4_linear(_gpu(x)[torch.arange(rows, device=DEV) % 8], w)
+    _within(y[:8], *ref.linear(x, None, *mat, "int", 128, None, BF))
+    assert torch.equal(y, y[:8][torch.arange(rows, device=DEV) % 8])
+
+
+def test_rows_of_one_dimension_and_calls_on_a_stream():
+    g = _gen(44)
+    k, n = 160, 40
+    x, xs = ref.make_rows(5, k, F8, g)
+    mats = [ref.make_weight(n, k, "mx", 32, g) for _ in range(2)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    w = [psispec_w4_pack(*map(_gpu, m), "mx", 32, stream=st) for m in mats]
+    st.synchronize()
+    xg, xsg = _gpu(x), _gpu(xs)
+    y, a = psispec_w4_linear(xg, w[0], x_scale=xsg), psispec_w4_gated(xg, *w, x_scale=xsg, out_dtype=FH)
+    _within(y, *ref.linear(x, xs, *mats[0], "mx", 32, None, BF))
+    _within(a, *ref.gated(x, xs, *mats, "mx", 32, "silu", FH))
+    st.wait_stream(torch.cuda.current_stream())
+    for i in (0, 4):
+        y1 = psispec_w4_linear(xg[i], w[0], x_scale=xsg[i], stream=st)
+        a1 = psispec_w4_gated(xg[i], *w, x_scale=xsg[i], out_dtype=FH, stream=st)
+        st.synchronize()
+        want, bound = ref.linear(x[i:i + 1], xs[i:i + 1], *mats[0], "mx", 32, None, BF)
+        assert y1.shape == (n,) and a1.shape == (n,) and a1.dtype == FH
+        _within(y1[None], want, bound)
+        _within(a1[None], *ref.gated(x[i:i + 1], xs[i:i + 1], *mats, "mx", 32, "silu", FH))
+    h = torch.randn((3, 96), generator=g).to(BF).to(DEV)
+    torch.cuda.synchronize()
+    out, _, s = psispec_add_rmsnorm(h, quant="mx", stream=st)
+    st.synchronize()
+    same = psispec_add_rmsnorm(h, quant="mx")
+    assert torch.equal(out.view(torch.uint8), same[0].view(torch.uint8))
+    assert torch.equal(s.view(torch.uint8), same[2].view(torch.uint8))
